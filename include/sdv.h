@@ -456,6 +456,147 @@ int sdv_verify_noalloc(const void* target_logits, const void* draft_logits, cons
                        const int32_t* ragged_offsets, int32_t B, int64_t n_draft_rows, int32_t V, int32_t dtype,
                        double temperature, uint64_t seed, int32_t* accepted_len, int32_t* out_tokens, void* stream);
 
+/*
+ * Drafting: one token per row, drawn from its logits under a sampling profile with a given uniform,
+ * and the distribution it was drawn from (SDCP section "Message Definitions": "drafter MUST sample
+ * each proposed token from exactly the row it publishes"; tokens and probs are the draft_tokens and
+ * draft_probs of a verification call).  All arrays are DEVICE arrays; row r < n_rows:
+ *   logits      row r at logits + r * row_stride elements, V of them (bf16 or binary32; row_stride
+ *               >= V, the base aligned to the element size; what lies between rows is not read)
+ *   temperature T, or temperature[r] of the options.  T = 0: the argmax, ties to the smallest id,
+ *               under any truncation and any uniform.  T > 0, with w_v = exp((z_v - max z) / T):
+ *   top_k       tokens rank by logit, equal logits going to the smaller id; the first top_k ranks
+ *               stay (0 or >= V: all)
+ *   top_p_milli then the shortest run of leading ranks whose mass reaches top_p_milli / 1000 of the
+ *               top-k set's (1000: all; never fewer than one)
+ *   min_p       then of these the tokens with w_v >= min_p (the largest w is 1; 0: all)
+ *   uniform     [n_rows] u_r in [0, 1): the token is min{v : C(v) > u S} in ascending id, over the
+ *               kept w and their sum S
+ * Outputs at index r, or at slots[r] of n_slots when slots is given (a draft step of a ragged batch
+ * writes request i's token j at cu[i] + j; a slot outside [0, n_slots) skips the row, which is then
+ * not read and nothing of it written; two rows with one slot leave an unspecified mix of both):
+ *   tokens [.] int32, prob [.] float   the token and its probability w / S
+ *   kept_tokens [.] int32              tokens the row keeps (V when nothing truncates, 1 at T = 0)
+ *   probs [.][V] float                 the distribution: w_v / S for the kept tokens, 0 elsewhere
+ *                                      (a one-hot row at T = 0)
+ * A NaN logit counts as -inf.  A row without a finite logit or with one of +inf, a temperature that
+ * is negative, NaN or infinite, and at T > 0 a negative top_k, a top_p_milli outside [0, 1000], a
+ * min_p outside [0, 1] or a uniform outside [0, 1), describe no draw: token -1, prob 0, kept 0 and
+ * a probs row of zeros; other rows are unaffected.  Weights and their sums are binary64, and the
+ * same call gives the same bits.
+ * workspace: sdv_sample_workspace_bytes(n_rows, V, dtype) bytes (0 on invalid shapes), 16-byte
+ * aligned, not initialised; it holds nothing between calls.  Errors: NULL required pointers,
+ * n_rows < 1, V < 1, row_stride < V, misaligned logits, a scalar temperature that is negative, NaN
+ * or infinite, n_slots < 0 or n_slots != 0 without slots -> SDV_ERR_INVALID_ARG; unknown dtype ->
+ * SDV_ERR_UNSUPPORTED; V above INT32_MAX - 64, row_stride above 2^40 or more than INT32_MAX rows, chunks of rows or
+ * tiles of probability rows -> SDV_ERR_LIMIT; a workspace that is NULL, small or misaligned ->
+ * SDV_ERR_WORKSPACE.
+ */
+typedef struct sdv_sample_options { /* every member may be NULL / 0 */
+  const float* temperature;   /* [n_rows], in place of the scalar */
+  const int32_t* top_k;       /* [n_rows] */
+  const int32_t* top_p_milli; /* [n_rows] */
+  const float* min_p;         /* [n_rows] */
+  const int32_t* slots;       /* [n_rows] */
+  int64_t n_slots;
+  int32_t* kept_tokens;
+  float* probs;
+} sdv_sample_options;
+size_t sdv_sample_workspace_bytes(int64_t n_rows, int32_t V, int32_t dtype);
+int sdv_sample(const void* logits, int64_t n_rows, int64_t row_stride, int32_t V, int32_t dtype, double temperature,
+               const double* uniform, const sdv_sample_options* options, int32_t* tokens, float* prob,
+               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The paged cache that the scoring of a ragged batch writes and reads.  Request i's rows are those of
+ * its target logits: row (i, j) = cu[i] + i + j, j <= K_i = cu[i + 1] - cu[i] (row 0 the last committed
+ * token, whose logits come first; a prompt is a request of many rows: K_i has no limit here but
+ * for trees).  Keys and values of one layer:
+ *   key_cache, value_cache [n_pages][n_kv_heads][page_size][head_dim]   bf16 or binary32, 16-byte aligned
+ *   page_table [B][max_pages] int32   slot s of request i lies in page page_table[i][s / page_size]
+ *                                     at place s % page_size
+ *   cache_len  [B] int32              L_i: the slots that request i holds before this step
+ * Row j takes slot L_i + j.  Its position, for the rotation and the window, is L_i + depth: j for a
+ * linear draft; with parents (as in sdv_verify_tree, at most 64 nodes) row 0 has depth 0 and row
+ * n + 1 (node n) the depth of its parent's row plus 1.
+ * A page number outside [0, n_pages) is no page: slots there, and slots beyond max_pages *
+ * page_size, are neither written nor seen (a serving engine frees the pages that left a window and
+ * leaves -1).  Rows that no request names by valid offsets are left as they were.  A request with
+ * cache_len < 0, or of a tree with more than 64 nodes or a parent outside [-1, n - 1], is passed
+ * over: sdv_kv_append writes nothing of it, sdv_attend writes zeros for its rows.
+ * page_size is a power of two in [1, 1024]; head_dim is 64, 128 or 256.
+ */
+typedef struct sdv_cache {
+  void* keys;
+  void* values;
+  const int32_t* page_table;
+  const int32_t* cache_len;
+  int64_t n_pages;
+  int32_t max_pages, page_size, n_kv_heads, head_dim, dtype;
+} sdv_cache;
+
+/*
+ * Appends the batch's keys and values, the keys rotated by their positions, and rotates the queries.
+ *   keys, values [n_draft_rows + B][n_kv_heads][head_dim], rows key_stride / value_stride elements
+ *                apart (slices of a fused projection), dtype as the cache's, rows 16-byte aligned
+ *   inv_freq     [rotary / 2] float, NULL (rotary 0): no rotation.  Pair f of a head's first rotary
+ *                values turns by the angle position * inv_freq[f]: (a, b) -> (a cos - b sin,
+ *                b cos + a sin), a and b at f and f + rotary / 2, or with interleaved at 2 f and
+ *                2 f + 1; the other values stay.  The angle is reduced in binary64, the rotation
+ *                is binary32 and rounded once.
+ *   queries      [n_draft_rows + B][n_q_heads][head_dim], rows query_stride apart, or NULL
+ *                (n_q_heads 0); queries_out [n_draft_rows + B][n_q_heads][head_dim] contiguous (or
+ *                queries itself, when that is contiguous)
+ *   parents      [n_draft_rows] int32, or NULL for linear drafts
+ * Two requests must not share a page that either writes.  Errors: NULL required pointers, sizes
+ * < 1, an unsupported page_size or head_dim, strides smaller than a row or off the 16-byte grid,
+ * misaligned pointers, rotary outside [0, head_dim] or not a multiple of 16, queries without queries_out
+ * or n_q_heads -> SDV_ERR_INVALID_ARG; unknown dtype -> SDV_ERR_UNSUPPORTED; more than INT32_MAX
+ * rows, or more than 1024 heads of a kind -> SDV_ERR_LIMIT.
+ */
+int sdv_kv_append(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, const int32_t* ragged_offsets,
+                  const int32_t* parents, const void* keys, int64_t key_stride, const void* values,
+                  int64_t value_stride, const float* inv_freq, int32_t rotary, int32_t interleaved,
+                  const void* queries, int64_t query_stride, int32_t n_q_heads, void* queries_out, void* stream);
+
+/*
+ * Attention of the batch's rows over the cache (after their own keys and values were appended).  Query
+ * head h reads key/value head h / (n_q_heads / n_kv_heads).  Row (i, j) sees slot s iff
+ *   s < L_i, or s is the slot of j itself or of one of its ancestors (every row before it in a
+ *   linear draft, the path to row 0 in a tree); and
+ *   window == 0, or position(j) - position(s) < window, or s < sinks (the first tokens stay visible).
+ * out[r][h] = sum_s softmax_s(scale * <q, k_s>) v_s, zeros for a row that sees nothing.
+ *   queries [n_draft_rows + B][n_q_heads][head_dim], rows query_stride elements apart, 16-byte aligned;
+ *   out     [n_draft_rows + B][n_q_heads][head_dim] contiguous, 16-byte aligned
+ * Scores, statistics and sums are binary32; with bf16 the probabilities are rounded to bf16 for their
+ * product with the values (relative 2^-9 each).  The same call gives the same bits.
+ * workspace: sdv_attend_workspace_bytes(...), 16-byte aligned, not initialised.
+ * Errors as sdv_kv_append, plus n_q_heads not a multiple of n_kv_heads, window < 0, sinks < 0 or a
+ * scale that is not finite -> SDV_ERR_INVALID_ARG; a small workspace -> SDV_ERR_WORKSPACE.
+ */
+size_t sdv_attend_workspace_bytes(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, int32_t n_q_heads,
+                                  int32_t window, int32_t sinks);
+int sdv_attend(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, const int32_t* ragged_offsets,
+               const int32_t* parents, const void* queries, int64_t query_stride, int32_t n_q_heads, float scale,
+               int32_t window, int32_t sinks, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Settles a verified token tree in the caches of n_layers layers: with accepted_len and accepted_nodes
+ * of sdv_verify_tree, the keys and values at slot L_i + 1 + accepted_nodes[cu[i] + d] move to slot
+ * L_i + 1 + d, d < accepted_len[i], where the committed sequence continues (their positions, and so
+ * their rotations, already are L_i + 1 + d).  new_len [B] int32 = L_i + 1 + accepted_len[i], the
+ * cached slots after the round (SDCP's committed prefix and the accepted drafts; the extra token is
+ * the next step's row 0).  Layer l's caches start l * n_pages * n_kv_heads * page_size * head_dim elements
+ * behind cache->keys / values.  A rejected request (accepted_len -1), one whose offsets are not
+ * valid, or whose accepted nodes do not ascend within its tree, moves nothing and keeps new_len = L_i.
+ * A move from or to a slot without a page is dropped.  Slots that no accepted node moved to are left
+ * as they were.  Errors as sdv_kv_append; n_layers < 1 -> SDV_ERR_INVALID_ARG, more than 65535 layers x
+ * heads x 2 -> SDV_ERR_LIMIT.
+ */
+int sdv_kv_settle(const sdv_cache* cache, int32_t n_layers, int32_t B, int64_t n_draft_rows,
+                  const int32_t* ragged_offsets, const int32_t* accepted_len, const int32_t* accepted_nodes,
+                  int32_t* new_len, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* sdv_status_string(int status);
 

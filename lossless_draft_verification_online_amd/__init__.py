@@ -15,7 +15,8 @@ from . import _native
 from ._native import (SDV_BF16, SDV_FP32, SDV_MAX_DEPTH, TERM_BAD, TERM_BONUS, TERM_GREEDY, TERM_NONE,
                       TERM_RESIDUAL, TERM_RESIDUAL_EMPTY, SdvError)
 
-__all__ = ["verify", "verify_ex", "verify_tree", "commit", "repad", "workspace_bytes", "philox4x32_10", "philox_uniforms", "read_ceiling", "sdcp_uniforms", "abi_version", "SdvError", "SDV_MAX_DEPTH",
+__all__ = ["verify", "verify_ex", "verify_tree", "commit", "repad", "sample", "kv_append", "attend",
+           "kv_settle", "workspace_bytes", "philox4x32_10", "philox_uniforms", "read_ceiling", "sdcp_uniforms", "abi_version", "SdvError", "SDV_MAX_DEPTH",
            "TERM_BAD", "TERM_BONUS", "TERM_GREEDY", "TERM_NONE", "TERM_RESIDUAL", "TERM_RESIDUAL_EMPTY", "library_path"]
 
 _DTYPES = {torch.bfloat16: SDV_BF16, torch.float32: SDV_FP32}
@@ -412,3 +413,217 @@ def repad(offsets: torch.Tensor, accepted_len: torch.Tensor, out_tokens: torch.T
     if rc != 0:
         raise SdvError(rc, "sdv_repad")
     return res
+
+
+def _scratch(nbytes: int, device: torch.device) -> torch.Tensor | None:
+    """Device scratch of a call: the stream's cached workspace, or, while a graph is captured, memory of
+    that graph's own (two graphs captured on one stream may be replayed on two)."""
+    if nbytes == 0:
+        return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return _workspace(nbytes, device)
+
+
+def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, *, top_k: torch.Tensor | None = None,
+           top_p_milli: torch.Tensor | None = None, min_p: torch.Tensor | None = None, probs=False,
+           slots: torch.Tensor | None = None, out: tuple | None = None, kept_tokens: torch.Tensor | None = None,
+           workspace: torch.Tensor | None = None):
+    """sdv_sample: one token per row of logits [n, V] (bf16 or float32; rows may be further apart than
+    V), drawn with the caller's uniform (float64 [n], in [0, 1)) at temperature (a number, or float32
+    [n]) under top_k, top_p_milli (int32 [n]) and min_p (float32 [n]).  Returns (tokens int32, prob
+    float32, extra): extra holds "kept_tokens" int32 and, with probs (True, or a float32 [n_out, V]
+    tensor to fill), "probs", the rows that verify_ex takes as draft_probs.  With slots (int32 [n]) row r's outputs
+    go to index slots[r] of ``out`` = (tokens, prob), which is then given (kept_tokens and probs of as many rows); a
+    slot outside it skips the row."""
+    if not logits.is_cuda:
+        raise ValueError("logits must be on the GPU")
+    if logits.dtype not in _DTYPES:
+        raise TypeError("logits must be bfloat16 or float32")
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be an [n, V] tensor with neighbouring tokens next to each other")
+    dev = logits.device
+    n, V = logits.shape
+    stride = logits.stride(0) if n > 1 else max(V, logits.stride(0))
+    if n < 1 or V < 1 or stride < V:
+        raise ValueError("logits must be an [n, V] tensor of rows that do not overlap")
+    _device_vector(uniform, torch.float64, n, dev, "uniform")
+    opt = _native.SdvSampleOptions()
+    if isinstance(temperature, torch.Tensor):
+        opt.temperature = _device_vector(temperature, torch.float32, n, dev, "temperature").data_ptr()
+        temperature = 0.0
+    if top_k is not None:
+        opt.top_k = _device_vector(top_k, torch.int32, n, dev, "top_k").data_ptr()
+    if top_p_milli is not None:
+        opt.top_p_milli = _device_vector(top_p_milli, torch.int32, n, dev, "top_p_milli").data_ptr()
+    if min_p is not None:
+        opt.min_p = _device_vector(min_p, torch.float32, n, dev, "min_p").data_ptr()
+    n_out = n
+    if out is not None:
+        tokens, prob = out
+        n_out = tokens.shape[0] if slots is not None else n
+        _device_vector(tokens, torch.int32, n_out, dev, "out[0]")
+        _device_vector(prob, torch.float32, n_out, dev, "out[1]")
+    elif slots is not None:
+        raise ValueError("slots place rows in given tensors: out is needed")
+    else:
+        tokens = torch.empty(n, dtype=torch.int32, device=dev)
+        prob = torch.empty(n, dtype=torch.float32, device=dev)
+    if slots is not None:
+        opt.slots = _device_vector(slots, torch.int32, n, dev, "slots").data_ptr()
+        opt.n_slots = n_out
+    fresh = torch.empty if slots is None else torch.zeros
+    if kept_tokens is None:
+        kept_tokens = fresh(n_out, dtype=torch.int32, device=dev)
+    opt.kept_tokens = _device_vector(kept_tokens, torch.int32, n_out, dev, "kept_tokens").data_ptr()
+    extra = {"kept_tokens": kept_tokens}
+    if probs is not False and probs is not None:
+        if probs is True:
+            probs = fresh((n_out, V), dtype=torch.float32, device=dev)
+        elif probs.dtype != torch.float32 or probs.device != dev or probs.shape != (n_out, V) or not probs.is_contiguous():
+            raise ValueError("probs must be a contiguous float32 [n_out, V] tensor on the logits' device")
+        opt.probs = probs.data_ptr()
+        extra["probs"] = probs
+    dt = _DTYPES[logits.dtype]
+    lib = _native.lib()
+    ctx, stream = _launch_on(dev)
+    with ctx:
+        ws = _scratch(lib.sdv_sample_workspace_bytes(n, V, dt), dev) if workspace is None else workspace
+        rc = lib.sdv_sample(logits.data_ptr(), n, stride, V, dt, float(temperature), uniform.data_ptr(),
+                            ctypes.byref(opt), tokens.data_ptr(), prob.data_ptr(), _ptr(ws),
+                            0 if ws is None else ws.numel() * ws.element_size(), stream)
+    if rc != 0:
+        raise SdvError(rc, "sdv_sample")
+    return tokens, prob, extra
+
+
+def _cache(key_cache, value_cache, page_table, cache_len, offsets, layers=False):
+    """Checks one layer's cache (or, with layers, [L, ...] of them) and marshals it: (sdv_cache, B, dims)."""
+    dev = key_cache.device
+    if not key_cache.is_cuda:
+        raise ValueError("the cache must be on the GPU")
+    if key_cache.dtype not in _DTYPES:
+        raise TypeError("the cache must be bfloat16 or float32")
+    if key_cache.dim() != (5 if layers and key_cache.dim() == 5 else 4) or not key_cache.is_contiguous():
+        raise ValueError("key_cache must be a contiguous [n_pages, n_kv_heads, page_size, head_dim] tensor")
+    if value_cache.dtype != key_cache.dtype or value_cache.device != dev or value_cache.shape != key_cache.shape \
+            or not value_cache.is_contiguous():
+        raise ValueError("value_cache must be like key_cache")
+    B = offsets.shape[0] - 1
+    _device_vector(offsets, torch.int32, B + 1, dev, "offsets")
+    _device_vector(cache_len, torch.int32, B, dev, "cache_len")
+    if page_table.dtype != torch.int32 or page_table.device != dev or page_table.dim() != 2 \
+            or page_table.shape[0] != B or not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous int32 [B, max_pages] tensor on the cache's device")
+    n_pages, heads, page_size, head_dim = key_cache.shape[-4:]
+    c = _native.SdvCache(key_cache.data_ptr(), value_cache.data_ptr(), page_table.data_ptr(), cache_len.data_ptr(),
+                         n_pages, page_table.shape[1], page_size, heads, head_dim, _DTYPES[key_cache.dtype])
+    return c, B, heads, head_dim
+
+
+def _rows(t, name, rows, heads, head_dim, like):
+    """The row stride of a [rows, heads, head_dim] tensor whose heads lie next to each other."""
+    if t.dtype != like.dtype or t.device != like.device or t.dim() != 3 or (rows is not None and t.shape[0] != rows) \
+            or (heads is not None and t.shape[1] != heads) or t.shape[2] != head_dim or t.stride(2) != 1 \
+            or (t.shape[1] > 1 and t.stride(1) != head_dim):
+        raise ValueError(f"{name} must be a [rows, heads, head_dim] tensor of the cache's dtype and device, "
+                         "each row contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * head_dim
+
+
+def kv_append(keys: torch.Tensor, values: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+              page_table: torch.Tensor, cache_len: torch.Tensor, offsets: torch.Tensor, *,
+              parents: torch.Tensor | None = None, inv_freq: torch.Tensor | None = None, interleaved: bool = False,
+              queries: torch.Tensor | None = None, queries_out: torch.Tensor | None = None):
+    """sdv_kv_append: the batch's keys and values ([n_draft_rows + B, n_kv_heads, head_dim], rows may be
+    slices of a fused projection) into the pages of key_cache / value_cache [n_pages, n_kv_heads,
+    page_size, head_dim] at slots cache_len[i] + j, the keys rotated by their positions with inv_freq
+    (float32 [rotary / 2]; pairs half a rotation apart, or neighbours when interleaved).  page_table is
+    int32 [B, max_pages], parents (int32 [n_draft_rows]) the tree of verify_tree.  Returns the queries
+    rotated the same way (queries_out, or a new contiguous tensor), or None without queries."""
+    c, B, heads, head_dim = _cache(key_cache, value_cache, page_table, cache_len, offsets)
+    dev = key_cache.device
+    rows = keys.shape[0]
+    ks = _rows(keys, "keys", None, heads, head_dim, key_cache)
+    vs = _rows(values, "values", rows, heads, head_dim, key_cache)
+    if rows < B:
+        raise ValueError("keys must have n_draft_rows + B rows")
+    _device_vector(parents, torch.int32, rows - B, dev, "parents")
+    rotary = 0
+    if inv_freq is not None:
+        rotary = 2 * _device_vector(inv_freq, torch.float32, inv_freq.numel(), dev, "inv_freq").shape[0]
+    n_q = qs = 0
+    if queries is not None:
+        n_q = queries.shape[1] if queries.dim() == 3 else 0
+        qs = _rows(queries, "queries", rows, n_q, head_dim, key_cache)
+        if queries_out is None:
+            queries_out = torch.empty((rows, n_q, head_dim), dtype=queries.dtype, device=dev)
+        elif queries_out.dtype != queries.dtype or queries_out.device != dev or queries_out.shape != queries.shape \
+                or not queries_out.is_contiguous():
+            raise ValueError("queries_out must be a contiguous tensor like queries")
+    elif queries_out is not None:
+        raise ValueError("queries_out without queries")
+    ctx, stream = _launch_on(dev)
+    with ctx:
+        rc = _native.lib().sdv_kv_append(ctypes.byref(c), B, rows - B, offsets.data_ptr(), _ptr(parents),
+                                         keys.data_ptr(), ks, values.data_ptr(), vs, _ptr(inv_freq), rotary,
+                                         int(bool(interleaved)), _ptr(queries), qs, n_q, _ptr(queries_out), stream)
+    if rc != 0:
+        raise SdvError(rc, "sdv_kv_append")
+    return queries_out
+
+
+def attend(queries: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor, page_table: torch.Tensor,
+           cache_len: torch.Tensor, offsets: torch.Tensor, *, parents: torch.Tensor | None = None,
+           scale: float | None = None, window: int = 0, sinks: int = 0, out: torch.Tensor | None = None,
+           workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """sdv_attend: attention of the batch's queries [n_draft_rows + B, n_q_heads, head_dim] over the cache
+    that kv_append wrote (arguments as there), each row over the slots before it (in a tree, the cached
+    slots and its ancestors) within window positions (0: all) or among the first ``sinks`` slots.  scale
+    defaults to head_dim ** -0.5.  Returns [n_draft_rows + B, n_q_heads, head_dim]."""
+    c, B, heads, head_dim = _cache(key_cache, value_cache, page_table, cache_len, offsets)
+    dev = key_cache.device
+    qs = _rows(queries, "queries", None, None, head_dim, key_cache)
+    rows, n_q = queries.shape[:2]
+    if rows < B:
+        raise ValueError("queries must have n_draft_rows + B rows")
+    if n_q < 1 or n_q % heads:
+        raise ValueError("the number of query heads must be a multiple of the cache's heads")
+    _device_vector(parents, torch.int32, rows - B, dev, "parents")
+    if out is None:
+        out = torch.empty((rows, n_q, head_dim), dtype=queries.dtype, device=dev)
+    elif out.dtype != queries.dtype or out.device != dev or out.shape != queries.shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor like queries")
+    lib = _native.lib()
+    ctx, stream = _launch_on(dev)
+    with ctx:
+        ws = workspace
+        if ws is None:
+            ws = _scratch(lib.sdv_attend_workspace_bytes(ctypes.byref(c), B, rows - B, n_q, int(window), int(sinks)), dev)
+        rc = lib.sdv_attend(ctypes.byref(c), B, rows - B, offsets.data_ptr(), _ptr(parents), queries.data_ptr(), qs, n_q,
+                            head_dim ** -0.5 if scale is None else float(scale), int(window), int(sinks),
+                            out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), stream)
+    if rc != 0:
+        raise SdvError(rc, "sdv_attend")
+    return out
+
+
+def kv_settle(key_cache: torch.Tensor, value_cache: torch.Tensor, page_table: torch.Tensor, cache_len: torch.Tensor,
+              offsets: torch.Tensor, accepted_len: torch.Tensor, accepted_nodes: torch.Tensor) -> torch.Tensor:
+    """sdv_kv_settle: moves the accepted path of verified token trees (accepted_len and accepted_nodes of
+    verify_tree) to the slots where the sequences continue, in one layer's cache or in all of
+    [n_layers, n_pages, n_kv_heads, page_size, head_dim].  Returns the new cache lengths, int32 [B]."""
+    c, B, _, _ = _cache(key_cache, value_cache, page_table, cache_len, offsets, layers=True)
+    dev = key_cache.device
+    n_d = accepted_nodes.numel()
+    _device_vector(accepted_len, torch.int32, B, dev, "accepted_len")
+    _device_vector(accepted_nodes, torch.int32, n_d, dev, "accepted_nodes")
+    new_len = torch.empty(B, dtype=torch.int32, device=dev)
+    ctx, stream = _launch_on(dev)
+    with ctx:
+        rc = _native.lib().sdv_kv_settle(ctypes.byref(c), key_cache.shape[0] if key_cache.dim() == 5 else 1, B, n_d,
+                                         offsets.data_ptr(), accepted_len.data_ptr(), _ptr(accepted_nodes) if n_d else None,
+                                         new_len.data_ptr(), stream)
+    if rc != 0:
+        raise SdvError(rc, "sdv_kv_settle")
+    return new_len

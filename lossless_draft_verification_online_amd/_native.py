@@ -56,6 +56,34 @@ class SdvOptions(ctypes.Structure):
     ]
 
 
+class SdvSampleOptions(ctypes.Structure):
+    _fields_ = [
+        ("temperature", ctypes.c_void_p),
+        ("top_k", ctypes.c_void_p),
+        ("top_p_milli", ctypes.c_void_p),
+        ("min_p", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("n_slots", ctypes.c_int64),
+        ("kept_tokens", ctypes.c_void_p),
+        ("probs", ctypes.c_void_p),
+    ]
+
+
+class SdvCache(ctypes.Structure):
+    _fields_ = [
+        ("keys", ctypes.c_void_p),
+        ("values", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("cache_len", ctypes.c_void_p),
+        ("n_pages", ctypes.c_int64),
+        ("max_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
 _LIB = None
 
 _VERIFY_ARGS = [
@@ -106,6 +134,28 @@ def lib(path: str = LIBRARY) -> ctypes.CDLL:
     L.sdv_philox4x32_10.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]
     L.sdv_philox_uniforms.restype = ctypes.c_int
     L.sdv_philox_uniforms.argtypes = [ctypes.c_uint64, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]
+    L.sdv_sample_workspace_bytes.restype = ctypes.c_size_t
+    L.sdv_sample_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32]
+    L.sdv_sample.restype = ctypes.c_int
+    L.sdv_sample.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                             ctypes.c_double, ctypes.c_void_p, ctypes.POINTER(SdvSampleOptions), ctypes.c_void_p,
+                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+    L.sdv_kv_append.restype = ctypes.c_int
+    L.sdv_kv_append.argtypes = [ctypes.POINTER(SdvCache), ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
+                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                                ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]
+    L.sdv_attend_workspace_bytes.restype = ctypes.c_size_t
+    L.sdv_attend_workspace_bytes.argtypes = [ctypes.POINTER(SdvCache), ctypes.c_int32, ctypes.c_int64, ctypes.c_int32,
+                                             ctypes.c_int32, ctypes.c_int32]
+    L.sdv_attend.restype = ctypes.c_int
+    L.sdv_attend.argtypes = [ctypes.POINTER(SdvCache), ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
+                             ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
+                             ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                             ctypes.c_void_p]
+    L.sdv_kv_settle.restype = ctypes.c_int
+    L.sdv_kv_settle.argtypes = [ctypes.POINTER(SdvCache), ctypes.c_int32, ctypes.c_int32, ctypes.c_int64] + \
+        [ctypes.c_void_p] * 5
     L.sdv_status_string.restype = ctypes.c_char_p
     L.sdv_read_yardstick.restype = ctypes.c_int
     L.sdv_read_yardstick.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]

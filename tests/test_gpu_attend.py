@@ -1,0 +1,202 @@
+"""Attention over the paged cache on the GPU against the binary64 oracle.
+
+Tolerance of an output value o = sum p v with A = sum p |v|.  A score is a binary32 sum of D products (bf16
+products are exact in binary32), so it is off by at most (D + 2) 2^-24 sum |q k| scale, and so is its weight
+relatively; the exponential and the running rescales add 2^-22 per step of the longest chain of maxima (at
+most the number of 32-token tiles a wave takes, joined over waves and splits); the sums over the n visible
+tokens n 2^-24.  With bf16 a weight is rounded to 2^-8 for its product, and the result to 2^-8 of itself.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import lossless_draft_verification_online_amd as sdv
+from oracle import cache as oracle
+from cache_helpers import DEV, DT, Batch, np64
+
+pytestmark = pytest.mark.gpu
+
+
+def check(b, dtype, window=0, sinks=0, scale=None, q=None):
+    table, length, cu = b.index_args()
+    D = b.kc.shape[-1]
+    args = (q if q is not None else b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), table, length, cu)
+    out = sdv.attend(*args, parents=b.tree_arg(), scale=scale, window=window, sinks=sinks)
+    s = D ** -0.5 if scale is None else scale
+    ref, mag, span = oracle.attend(np64(b.q), np64(b.kc), np64(b.vc), b.table, b.len, b.cu, s, window, sinks, b.parents)
+    n = int(b.len.max()) + int(max(b.ks)) + 1
+    rel = (D + 2) * 2.0 ** -24 * span[..., None] + 2.0 ** -22 * (n / 32 + 4) + n * 2.0 ** -24
+    tol = mag * rel + np.abs(ref) * 2.0 ** -24 + 1e-30
+    if dtype == "bf16":
+        tol += 2.0 ** -8 * mag + 2.0 ** -8 * np.abs(ref)
+    got = np64(out)
+    bad = ~(np.abs(got - ref) <= tol)
+    assert not bad.any(), (bad.sum(), np.argwhere(bad)[:4], got[bad][:4], ref[bad][:4])
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hkv,G", [(1, 1), (2, 4), (3, 7), (1, 16), (2, 20)])
+def test_heads(Hkv, G, D, dtype):
+    check(Batch([0, 3, 8, 1], [0, 17, 300, 31], Hkv, D, 16, dtype, D + G, Hq=Hkv * G), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (0, 5), (1, 0), (1, 1), (33, 0), (64, 4), (100, 40), (5000, 3), (200, 10000)])
+def test_windows_and_sinks(window, sinks, dtype):
+    check(Batch([0, 3, 12, 0, 5], [0, 97, 640, 31, 200], 2, 64, 16, dtype, window + sinks, Hq=8), dtype, window, sinks)
+
+
+@pytest.mark.parametrize("page", [1, 2, 8, 32, 128, 1024])
+def test_pages(page):
+    check(Batch([0, 2, 7], [1, 130, 777], 2, 128, page, "bf16", page, Hq=4), "bf16", 300, 7)
+    check(Batch([0, 2, 7], [1, 130, 777], 2, 64, page, "fp32", page, Hq=4), "fp32")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (3, 0), (40, 60), (2, 105)])
+def test_trees(window, sinks, dtype):
+    check(Batch([0, 64, 12, 30, 1], [3, 100, 0, 63, 7], 2, 64, 16, dtype, window, tree=True, Hq=6), dtype, window, sinks)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_prompts(dtype):
+    check(Batch([300, 0, 97], [40, 0, 0], 2, 64, 32, dtype, 1, Hq=4), dtype)
+    check(Batch([513], [200], 1, 128, 64, dtype, 2, Hq=5), dtype, 128, 4)
+    check(Batch([258, 130], [0, 77], 1, 256, 16, dtype, 3, Hq=2), dtype, 50, 0)
+
+
+def test_long_caches_are_split():
+    check(Batch([0], [9000], 1, 128, 16, "bf16", 4, Hq=8), "bf16")
+    check(Batch([4, 0], [5000, 20], 1, 64, 16, "fp32", 5, Hq=4), "fp32", 4096, 4)
+    check(Batch([0, 1], [6000, 0], 1, 256, 64, "bf16", 6, Hq=4), "bf16", 0, 0)
+
+
+def test_many_requests():
+    rng = np.random.default_rng(7)
+    check(Batch(rng.integers(0, 6, 200), rng.integers(0, 90, 200), 1, 64, 16, "bf16", 8, Hq=4), "bf16", 40, 2)
+
+
+def test_strided_queries_and_scales():
+    b = Batch([3, 1], [50, 20], 2, 64, 16, "bf16", 9, Hq=4)
+    wide = torch.randn((b.rows, 9, 64)).to(torch.bfloat16)
+    wide[:, :4] = b.q
+    check(b, "bf16", q=wide.to(DEV)[:, :4])
+    for scale in (0.0, 1.0, -0.5):
+        check(b, "bf16", scale=scale)
+    b = Batch([3, 1], [500, 20], 2, 64, 16, "fp32", 10, Hq=4)
+    b.q *= 30  # far apart scores: most weights vanish
+    check(b, "fp32", scale=1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_what_no_row_sees_may_hold_anything(dtype):
+    """NaN and infinities behind the last row, before the window, in pages of nobody and in freed places."""
+    b = Batch([2, 0, 5], [70, 9, 333], 2, 128, 16, dtype, 11, Hq=4)
+    window, sinks = 64, 3
+    want = check(b, dtype, window, sinks)
+    seen = np.zeros((b.n_pages, 16), dtype=bool)
+    for i, _, K, L, _, _ in oracle.requests(b.cu, b.len, b.n_d):
+        for s in range(L + K + 1):
+            if s < sinks or s > L - window:
+                p = oracle.place(b.table[i], b.n_pages, 16, s)
+                seen[p] = True
+    for c in (b.kc, b.vc):
+        hole = torch.from_numpy(~seen)[:, None, :, None].expand(c.shape)
+        c[hole] = torch.tensor([float("nan"), float("inf"), -float("inf")]).to(c.dtype).repeat(c.numel())[:int(hole.sum())]
+    table, length, cu = b.index_args()
+    out = sdv.attend(b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), table, length, cu, window=window, sinks=sinks)
+    assert torch.equal(out, want)
+
+
+def test_pages_that_left_the_window_and_pages_that_are_missing():
+    b = Batch([2, 0, 5], [70, 200, 333], 2, 64, 16, "bf16", 12, Hq=4)
+    want = check(b, "bf16", 64, 3)
+    b.table[1, 1:8] = -1  # slots 16 .. 127: out of the window of position 200
+    b.table[2, 1:16] = [-1, b.n_pages, 2 ** 31 - 1, -2 ** 31, -7] * 3
+    assert torch.equal(check(b, "bf16", 64, 3), want)
+    b.table[0, 1] = -1  # missing inside the window: not seen
+    b.table[2, :] = -1  # nothing left to see: zeros
+    out = check(b, "bf16", 64, 3)
+    assert not out[4:].any() and out[:3].any()
+
+
+def test_requests_that_are_passed_over():
+    b = Batch([2, 1, 5, 3], [70, 20, 33, 4], 2, 64, 16, "bf16", 13, Hq=4)
+    b.len[1] = -3
+    assert not check(b, "bf16")[3:5].any()
+    b = Batch([2, 3, 5], [70, 20, 33], 2, 64, 16, "bf16", 14, Hq=4, tree=True)
+    b.parents[3] = 1
+    assert not check(b, "bf16")[3:7].any()
+    b = Batch([70, 3], [10, 20], 2, 64, 16, "bf16", 15, Hq=4, tree=True)
+    assert not check(b, "bf16")[:71].any()
+    b = Batch([3, 2, 5], [30, 7, 15], 1, 64, 16, "bf16", 16, Hq=2)
+    b.len[0] = 16 * b.table.shape[1] - 1  # rows behind the table's end
+    check(b, "bf16")
+    table, length, _ = b.index_args()
+    for bad in ([0, 3, 2, 10], [0, -5, 5, 10], [0, 3, 50, 10], [4, 3, 2, 1], [-1, -1, -1, -1]):
+        out = torch.full((13, 2, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+        sdv.attend(b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), table, length, torch.tensor(bad, dtype=torch.int32, device=DEV),
+                   out=out)
+        torch.cuda.synchronize()
+
+
+def test_a_row_does_not_depend_on_its_batch():
+    b = Batch([4, 0, 2], [100, 50, 30], 2, 128, 16, "fp32", 17, Hq=4)
+    table, length, cu = b.index_args()
+    args = (b.kc.to(DEV), b.vc.to(DEV))
+    first = sdv.attend(b.q.to(DEV), *args, table, length, cu, window=40, sinks=2)
+    again = sdv.attend(b.q.to(DEV), *args, table, length, cu, window=40, sinks=2)
+    assert torch.equal(first, again)
+    one = sdv.attend(b.q[5:6].to(DEV), *args, table[1:2].contiguous(), length[1:2].contiguous(),
+                     torch.zeros(2, dtype=torch.int32, device=DEV), window=40, sinks=2)
+    assert (one - first[5:6]).abs().max() <= 2.0 ** -18 * first.abs().max()
+
+
+def test_graph_replays():
+    b = Batch([4, 0, 2], [3000, 50, 30], 2, 128, 16, "bf16", 18, Hq=4)
+    table, length, cu = b.index_args()
+    q, kc, vc = b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        sdv.attend(q, kc, vc, table, length, cu)
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                out = sdv.attend(q, kc, vc, table, length, cu)
+            graphs.append((g, out))
+    torch.cuda.synchronize()
+    for step in range(4):
+        q.copy_(torch.randn(q.shape, generator=torch.Generator().manual_seed(step)))
+        length.copy_(torch.tensor([3000 - 7 * step, 50, 30 + step // 2], dtype=torch.int32))
+        want = sdv.attend(q, kc, vc, table, length, cu)
+        torch.cuda.synchronize()
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            assert torch.equal(out, want)
+
+
+def test_refusals():
+    b = Batch([2, 0], [5, 7], 2, 64, 16, "bf16", 19, Hq=4)
+    table, length, cu = b.index_args()
+    q, kc, vc = b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV)
+    for bad in (q.float(), q[:1], q[:, :3], q.transpose(0, 1), q[:, :, :32]):
+        with pytest.raises(ValueError):
+            sdv.attend(bad, kc, vc, table, length, cu)
+    for kw in (dict(window=-1), dict(sinks=-1), dict(scale=math.inf), dict(scale=math.nan)):
+        with pytest.raises(sdv.SdvError):
+            sdv.attend(q, kc, vc, table, length, cu, **kw)
+    with pytest.raises(ValueError):
+        sdv.attend(q, kc, vc, table, length, cu, out=torch.empty_like(q)[:2])
+    long = Batch([0], [9000], 1, 128, 16, "bf16", 4, Hq=8)
+    table, length, cu = long.index_args()
+    with pytest.raises(sdv.SdvError):
+        sdv.attend(long.q.to(DEV), long.kc.to(DEV), long.vc.to(DEV), table, length, cu,
+                   workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
