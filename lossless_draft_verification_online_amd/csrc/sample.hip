@@ -12,10 +12,10 @@
 // thousand on the neighbour.  Weights and sums are therefore binary64 (the weight to 2e-12), and
 // every sum has a fixed order, so the token is that of the definition and the same on every run.
 //
-// Three passes: row_stats streams every row once (a wave per chunk of 64 lanes x kVpl vectors:
-// maximum and sum), row_draw finishes each row in one workgroup (fold, cut, pick a chunk by prefix
-// sums, search that chunk), and row_probs, when the probability rows are asked for, streams
-// them out.
+// A row that fits a workgroup's shared memory takes one launch (row_whole).  A longer one takes two:
+// row_stats streams every row once, a wave per chunk of 64 lanes x kVpl vectors (sum of weights,
+// maximum), and row_draw finishes each row in one workgroup: fold, cut, pick a chunk by prefix
+// sums, search that chunk.  row_probs, when the probability rows are asked for, streams them out.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -28,17 +28,18 @@ using namespace sdv;
 
 constexpr int kStatsWaves = 4;
 constexpr int kDrawThreads = 1024;
-constexpr int kDrawWaves = kDrawThreads / kWave;
-constexpr int kBins = 2048;
+constexpr int kWindow = 4096;  // bins of the counts below the maximum
 
-struct Record {  // one chunk of a row: sum of weights in the frame of its own maximum
-  double s;
-  float m;
-  uint32_t eq;  // copies of the cut's key in the chunk (truncated rows)
+struct Record {  // one chunk of a row
+  double s;      // sum of weights: absolute ones, 2^(z k2), or with far those in the frame of m
+  float m;       // maximum (far chunks, and rows that are cut or take their argmax)
+  uint32_t far;  // truncated rows: copies of the cut's key
 };
 
 struct RowState {  // what row_probs needs of a row
-  double m, k2, inv_s;
+  double base, k2;
+  float inv_s;    // 1 / S, S taken into [1/2, 1)
+  int32_t exp_s;  // by 2^exp_s
   uint32_t key;   // kept: order key above this, or equal to it at an id of at most last
   int32_t last;
   int32_t token;  // kOneToken
@@ -70,73 +71,140 @@ struct Args {
 // from base are the row's; what a block holds beside them is not read.
 template <class E>
 struct RowView {
-  const char* base;
+  typedef const __attribute__((address_space(1))) u32x4* Vectors;
+  typedef const __attribute__((address_space(1))) uint16_t* Halves;
+  typedef const __attribute__((address_space(1))) uint32_t* Words;
+  static constexpr int P = E::kPerVec;
+  uintptr_t base;
   int32_t lead, end;
+  int32_t whole_lo, whole_hi;  // vectors that lie within the row
   __device__ RowView(const Args& a, int64_t row) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(a.logits) + (uintptr_t)(row * a.stride * E::kBytes);
     lead = (int32_t)(p & 15) / E::kBytes;
-    base = reinterpret_cast<const char*>(p & ~(uintptr_t)15);
+    base = p & ~(uintptr_t)15;
     end = lead + a.V;
+    whole_lo = lead ? 1 : 0;
+    whole_hi = end / P;
   }
-  __device__ bool whole(int32_t e0, int32_t n) const { return e0 >= lead && (int64_t)e0 + n <= end; }
-  __device__ u32x4 vec(int64_t j) const { return *reinterpret_cast<const u32x4*>(base + j * 16); }
-  __device__ u32x4 vec_edge(int64_t j) const {  // a vector that may lie partly or wholly outside
+  __device__ __forceinline__ u32x4 vec(int64_t j) const { return reinterpret_cast<Vectors>(base)[j]; }
+  static __device__ __forceinline__ u32x4 nothing() {
     u32x4 v;
     v.x = v.y = v.z = v.w = E::kNegInfWord;
-    const int64_t e0 = j * E::kPerVec;
-    if (e0 + E::kPerVec <= lead || e0 >= end) return v;
-    if (e0 >= lead && e0 + E::kPerVec <= end) return vec(j);
+    return v;
+  }
+  // Vector j element by element: the row's own, -inf beside them.
+  __device__ u32x4 part(int32_t j) const {
+    u32x4 v = nothing();
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int i = 0; i < E::kPerVec; ++i) {
-      const int64_t e = e0 + i;
+    for (int i = 0; i < P; ++i) {
+      const int32_t e = j * P + i;
       if (e < lead || e >= end) continue;
-      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
       if constexpr (E::kBytes == 4) {
-        w[i] = reinterpret_cast<const uint32_t*>(base)[e];
+        w[i] = reinterpret_cast<Words>(base)[e];
       } else {
-        const uint32_t h = reinterpret_cast<const uint16_t*>(base)[e];
+        const uint32_t h = reinterpret_cast<Halves>(base)[e];
         const int sh = (i & 1) * 16;
         w[i >> 1] = (w[i >> 1] & ~(0xffffu << sh)) | (h << sh);
       }
     }
+    v.x = w[0];
+    v.y = w[1];
+    v.z = w[2];
+    v.w = w[3];
     return v;
   }
-  // The chunk's vectors of this lane, lane-interleaved (vector c0 + 64 i + lane).
-  template <int kVpl>
-  __device__ void chunk(int32_t c, int lane, u32x4 (&v)[kVpl]) const {
-    const int64_t j0 = (int64_t)c * (kVpl * kWave);
-    if (j0 * E::kPerVec >= lead && (j0 + kVpl * kWave) * E::kPerVec <= end) {
+  // N vectors of a lane, j0 + i * step, any of which may lie partly or wholly outside: the whole ones by
+  // vector loads; at most two of a row are parts, and those are put in their places.
+  template <int N>
+  __device__ __forceinline__ void edge(int32_t j0, int32_t step, u32x4 (&v)[N]) const {
 #pragma unroll
-      for (int i = 0; i < kVpl; ++i) v[i] = vec(j0 + i * kWave + lane);
+    for (int i = 0; i < N; ++i) {
+      const int32_t j = j0 + i * step;
+      v[i] = nothing();
+      if (j >= whole_lo && j < whole_hi) v[i] = vec(j);
+    }
+    bool head = false, tail = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int32_t j = j0 + i * step;
+      head = head || (j == 0 && whole_lo > 0);
+      tail = tail || (j == whole_hi && j >= whole_lo);
+    }
+    if (head) {
+      const u32x4 p = part(0);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (j0 + i * step == 0) v[i] = p;
+    }
+    if (tail) {
+      const u32x4 p = part(whole_hi);
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (j0 + i * step == whole_hi) v[i] = p;
+    }
+  }
+  __device__ __forceinline__ u32x4 one(int32_t j) const {
+    u32x4 v[1];
+    edge<1>(j, 1, v);
+    return v[0];
+  }
+  __device__ __forceinline__ bool inside(int32_t j0, int32_t n) const { return j0 >= whole_lo && j0 + n <= whole_hi; }
+  // N vectors of this lane from j0, lane-interleaved (j0 + 64 i + lane).
+  template <int N>
+  __device__ __forceinline__ void load(int32_t j0, int lane, u32x4 (&v)[N]) const {
+    if (inside(j0, N * kWave)) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = vec((int64_t)j0 + i * kWave + lane);
     } else {
-#pragma unroll
-      for (int i = 0; i < kVpl; ++i) v[i] = vec_edge(j0 + i * kWave + lane);
+      edge<N>(j0 + lane, kWave, v);
     }
   }
 };
 
-// 2^t for t = (z - m) k2 <= 0: t = n + r with |r| <= 1/2 by adding 1.5 x 2^52, and 2^r = 1 + r q(r)
-// with q the interpolation of (2^r - 1) / r at the eight Chebyshev nodes (relative error 2.1e-12).
-// -inf and NaN logits take the lower bound of d, whose weight is 0.
+// Hides from the compiler that a pass works on the values of the pass before: it would keep every
+// unpacked logit and weight in registers for the second use, and spill.
+template <int N>
+__device__ __forceinline__ void forget(u32x4 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
+}
+
+// 2^t: t = n + r with |r| <= 1/2 by adding 1.5 x 2^52, and 2^r = 1 + r q(r) with q the
+// interpolation of (2^r - 1) / r at the eight Chebyshev nodes (relative error 2.1e-12).  t = d k2
+// enters both steps unrounded; |t| is below 2^31.
+__device__ __forceinline__ double exp2_of(double d, double k2) {
+  constexpr double kMagic = 0x1.8p52;
+  const double y = fma(d, k2, kMagic);
+  const double r = fma(d, k2, kMagic - y);
+  double q = 0x1.63b2d7967b894p-20;
+  q = fma(q, r, 0x1.00c0e4e14e280p-16);
+  q = fma(q, r, 0x1.4308c7183de44p-13);
+  q = fma(q, r, 0x1.5d8775983512bp-10);
+  q = fma(q, r, 0x1.3b2ab70ad2562p-7);
+  q = fma(q, r, 0x1.c6b08da70cce3p-5);
+  q = fma(q, r, 0x1.ebfbdff82a734p-3);
+  q = fma(q, r, 0x1.62e42fef9cc69p-1);
+  return __builtin_amdgcn_ldexp(fma(q, r, 1.0), __double2loint(y));
+}
+
+// Weights relative to a base logit (the maximum: its weight is exactly 1, so sums of equal weights are exact).
+// -inf and NaN take the lower bound of d, whose weight is 0.
 struct Frame {
-  double m, k2, d_min;
-  __device__ Frame(double m_, double k2_) : m(m_), k2(k2_), d_min(-1100.0 / k2_) {}
-  __device__ double weight(float z) const {
-    constexpr double kMagic = 0x1.8p52;
-    const double d = fmax((double)z - m, d_min);
-    const double y = fma(d, k2, kMagic);
-    const double r = fma(d, k2, kMagic - y);
-    double q = 0x1.63b2d7967b894p-20;
-    q = fma(q, r, 0x1.00c0e4e14e280p-16);
-    q = fma(q, r, 0x1.4308c7183de44p-13);
-    q = fma(q, r, 0x1.5d8775983512bp-10);
-    q = fma(q, r, 0x1.3b2ab70ad2562p-7);
-    q = fma(q, r, 0x1.c6b08da70cce3p-5);
-    q = fma(q, r, 0x1.ebfbdff82a734p-3);
-    q = fma(q, r, 0x1.62e42fef9cc69p-1);
-    return __builtin_amdgcn_ldexp(fma(q, r, 1.0), __double2loint(y));
-  }
+  double base, k2, d_min;
+  __device__ Frame(double base_, double k2_) : base(base_), k2(k2_), d_min(-1100.0 / k2_) {}
+  __device__ double weight(float z) const { return exp2_of(fmax((double)z - base, d_min), k2); }
 };
+
+// Absolute weights, without a maximum found first: binary64 holds 2^(z k2) for |z k2| < 1000.  Beyond, a weight
+// becomes 0 or infinity and the sum of a chunk that leaves [2^-900, 2^1000] says so.
+struct NearFrame {
+  double k2;
+  float lo, hi;
+  __device__ NearFrame(double k2_) : k2(k2_), lo((float)(-1100.0 / k2_)), hi((float)(1100.0 / k2_)) {}
+  __device__ double weight(float z) const { return exp2_of((double)__builtin_amdgcn_fmed3f(z, lo, hi), k2); }
+};
+__device__ __forceinline__ bool near_sum(double s) { return s >= 0x1p-900 && s <= 0x1p1000; }
 
 // Unsigned order of the keys is the order of the logits; -0 shares +0's key, NaN shares -inf's.
 __device__ __forceinline__ uint32_t order_key(float z) {
@@ -195,6 +263,8 @@ __device__ __forceinline__ int64_t slot_of(const Args& a, int64_t row) {
 
 constexpr double kLog2e = 0x1.71547652b82fep0;
 
+// The row pass: 17 instructions of binary64 arithmetic per logit of a row whose weights are all
+// needed, about the time the loads take; a row that only needs its maximum is bound by the loads.
 template <class E, int kVpl>
 __global__ __launch_bounds__(kStatsWaves* kWave) void row_stats(Args a) {
   const int lane = threadIdx.x & (kWave - 1);
@@ -206,101 +276,183 @@ __global__ __launch_bounds__(kStatsWaves* kWave) void row_stats(Args a) {
   if (slot_of(a, row) < 0) return;
   const RowView<E> view(a, row);
   u32x4 v[kVpl];
-  view.template chunk<kVpl>(c, lane, v);
+  view.template load<kVpl>(c * (kVpl * kWave), lane, v);
   const Profile f = profile_of(a, row);
-  float m = -__builtin_inff();
-#pragma unroll
-  for (int i = 0; i < kVpl; ++i) {
-    float z[E::kPerVec];
-    E::unpack(v[i], z);
-#pragma unroll
-    for (int e = 0; e < E::kPerVec; ++e) m = fmaxf(m, z[e]);
-  }
-  m = wave_max(m);
-  double s = 0.0;
-  if (f.ok && !f.greedy && !f.cut) {  // a cut row's sums wait for the cut
-    const Frame frame(m, kLog2e / f.T);
+  Record r;
+  r.s = 0.0;
+  r.m = -__builtin_inff();
+  r.far = 0;
+  if (f.ok && !f.greedy && !f.cut) {
+    const NearFrame frame(kLog2e / f.T);
+    double s = 0.0;
 #pragma unroll
     for (int i = 0; i < kVpl; ++i) {
       float z[E::kPerVec];
       E::unpack(v[i], z);
 #pragma unroll
       for (int e = 0; e < E::kPerVec; ++e) s += frame.weight(z[e]);
+      __builtin_amdgcn_sched_barrier(0);  // vectors one after another: interleaved they spill
     }
-    s = wave_sum(s);
+    r.s = wave_sum(s);
   }
-  if (lane == 0) {
-    Record r;
-    r.s = s;
-    r.m = m;
-    r.eq = 0;
-    a.rec[unit] = r;
-  }
-}
-
-struct Shared {
-  uint64_t hist[kBins];
-  double wave_d[kDrawWaves];
-  uint64_t wave_u[kDrawWaves];
-  float wave_f[kDrawWaves];
-  uint64_t found_before, found_at;
-  double before;
-  uint32_t found_bin, key;
-  int32_t chunk, first, last, eq_last;
-};
-
-// Exclusive prefix over the workgroup's threads in thread order; total in every thread.
-__device__ __forceinline__ double block_scan(double v, double* wave_d, double& total) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const double inc = wave_detail::inclusive_scan(v);
-  __syncthreads();
-  if (lane == kWave - 1) wave_d[wave] = inc;
-  __syncthreads();
-  double base = 0.0;
-  total = 0.0;
-  for (int w = 0; w < kDrawWaves; ++w) {
-    if (w == wave) base = total;
-    total += wave_d[w];
-  }
-  return base + (inc - v);
-}
-__device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* wave_u, uint64_t& total) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-  const uint64_t inc = wave_inclusive_scan(v);
-  __syncthreads();
-  if (lane == kWave - 1) wave_u[wave] = inc;
-  __syncthreads();
-  uint64_t base = 0;
-  total = 0;
-  for (int w = 0; w < kDrawWaves; ++w) {
-    if (w == wave) base = total;
-    total += wave_u[w];
-  }
-  return base + (inc - v);
-}
-
-// Every element of the row once, each chunk by one wave: f(z) for the row's own elements (padding
-// arrives as -inf and must not count, so its place decides).
-template <class E, int kVpl, class F>
-__device__ __forceinline__ void each_element(const RowView<E>& view, int32_t C, F f) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
-  for (int32_t c = wave; c < C; c += kDrawWaves) {
-    u32x4 v[kVpl];
-    view.template chunk<kVpl>(c, lane, v);
-    const int64_t j0 = (int64_t)c * (kVpl * kWave) + lane;
+  const bool mass = f.ok && !f.greedy && f.top_p && !f.top_k;  // the nucleus is a share of the whole row
+  if (f.ok && (f.greedy || f.cut || !near_sum(r.s))) {
+    float m = -__builtin_inff();
+    forget(v);
 #pragma unroll
     for (int i = 0; i < kVpl; ++i) {
       float z[E::kPerVec];
       E::unpack(v[i], z);
 #pragma unroll
-      for (int e = 0; e < E::kPerVec; ++e) {
-        const int64_t at = (j0 + i * kWave) * E::kPerVec + e;
-        if (at >= view.lead && at < view.end) f(z[e]);
+      for (int e = 0; e < E::kPerVec; ++e) m = fmaxf(m, z[e]);
+    }
+    r.m = wave_max(m);
+    r.far = 1;
+    if (!f.greedy && (!f.cut || mass)) {
+      forget(v);
+      double s = 0.0;
+      const Frame frame(r.m, kLog2e / f.T);
+#pragma unroll
+      for (int i = 0; i < kVpl; ++i) {
+        float z[E::kPerVec];
+        E::unpack(v[i], z);
+#pragma unroll
+        for (int e = 0; e < E::kPerVec; ++e) s += frame.weight(z[e]);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      r.s = wave_sum(s);
     }
   }
+  if (lane == 0) a.rec[unit] = r;
 }
+
+template <int kThreads>
+struct Shared {
+  static constexpr int kWaves = kThreads / kWave;
+  uint64_t hist[kWindow];
+  double wave_d[kWaves];
+  uint64_t wave_u[kWaves];
+  float wave_f[kWaves];
+  int32_t wave_i[2][kWaves];
+  uint64_t found_before, found_at;
+  double mass_before;
+  uint32_t found_bin, key;
+  int32_t eq_last, chunk;
+};
+
+// Exclusive prefix over the workgroup's threads in thread order; the total in every thread.
+template <int kWaves, class T>
+__device__ __forceinline__ T block_scan(T v, T* wave_sums, T& total) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const T inc = wave_detail::inclusive_scan(v);
+  __syncthreads();
+  if (lane == kWave - 1) wave_sums[wave] = inc;
+  __syncthreads();
+  T base = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    const T x = wave_sums[w];
+    base += w < wave ? x : T(0);
+    total += x;
+  }
+  return base + (inc - v);
+}
+
+// The first (or last) of the threads' ids in thread order, kNone from a thread that has none.
+constexpr int32_t kNone = 0x7fffffff;
+template <int kWaves>
+__device__ __forceinline__ int32_t block_first(int32_t id, int32_t* wave_ids) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const uint64_t who = __ballot(id != kNone);
+  __syncthreads();
+  if (who ? lane == __ffsll((unsigned long long)who) - 1 : lane == 0) wave_ids[wave] = id;
+  __syncthreads();
+  int32_t first = kNone;
+#pragma unroll
+  for (int w = kWaves - 1; w >= 0; --w) first = wave_ids[w] != kNone ? wave_ids[w] : first;
+  return first;
+}
+template <int kWaves>
+__device__ __forceinline__ int32_t block_last(int32_t id, int32_t* wave_ids) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const uint64_t who = __ballot(id != kNone);
+  __syncthreads();
+  if (who ? lane == 63 - __builtin_clzll(who) : lane == 0) wave_ids[wave] = id;
+  __syncthreads();
+  int32_t last = kNone;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) last = wave_ids[w] != kNone ? wave_ids[w] : last;
+  return last;
+}
+
+// A row's elements for the passes of a cut.  Each pass is a loop over single vectors, small enough
+// to stay in the instruction cache: unrolled over a thread's whole share (32 logits) the passes of a row are
+// 160 KiB of code that each workgroup fetches to run once, and that fetch set their time (56 us against 20 us for
+// one row of 32000 under top-k).
+// In memory, a wave's vectors interleaved by lane and kAhead of them loaded ahead ...
+constexpr int kAhead = 4;
+
+template <class E, int kThreads>
+struct MemorySource {
+  const RowView<E>& view;
+  // f(id of the vector's first value, vector, whole: every value is the row's)
+  template <class F>
+  __device__ __forceinline__ void vectors(int32_t j0, int32_t j1, int32_t step, F f) const {
+    const int lane = threadIdx.x & (kWave - 1);
+    u32x4 ahead[kAhead];
+    auto load = [&](int32_t j, u32x4& v) {
+      u32x4 one[1];
+      if (j < j1) {
+        view.template load<1>(j, lane, one);
+        v = one[0];
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(j0 + i * step, ahead[i]);
+#pragma unroll 1
+    for (int32_t j = j0; j < j1; j += step) {
+      const u32x4 v = ahead[0];
+#pragma unroll
+      for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+      load(j + kAhead * step, ahead[kAhead - 1]);
+      f((j + lane) * E::kPerVec - view.lead, v, view.inside(j, kWave));
+    }
+  }
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
+    vectors(wave * kWave, (view.end + E::kPerVec - 1) / E::kPerVec, kThreads, [&](int32_t id, u32x4 v, bool whole) {
+      float z[E::kPerVec];
+      E::unpack(v, z);
+#pragma unroll
+      for (int e = 0; e < E::kPerVec; ++e)
+        if (whole || (uint32_t)(id + e) < (uint32_t)(view.end - view.lead)) f(z[e]);
+    });
+  }
+};
+
+// ... or in shared memory.
+template <class E, int kThreads>
+struct SharedSource {
+  const u32x4* v;
+  int32_t n, lead, V;  // vectors; values beside the row's in the first; the row's
+  template <class F>
+  __device__ __forceinline__ void vectors(F f) const {
+#pragma unroll 1
+    for (int32_t j = threadIdx.x; j < n; j += kThreads) f(j, j * E::kPerVec - lead, v[j]);
+  }
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    vectors([&](int32_t, int32_t id, u32x4 x) {
+      float z[E::kPerVec];
+      E::unpack(x, z);
+#pragma unroll
+      for (int e = 0; e < E::kPerVec; ++e)
+        if ((uint32_t)(id + e) < (uint32_t)V) f(z[e]);
+    });
+  }
+};
 
 struct Selected {
   uint32_t key;
@@ -311,21 +463,22 @@ struct Selected {
 // need_of(total): one pass of the row per digit (11 + 5 bits of a bf16 key, 11 + 11 + 10 of a
 // binary32 key) fills a histogram of the keys that share the digits found so far.  Sums are
 // integers, so the order of the adds changes nothing.
-template <class E, int kVpl, class Value, class Need>
-__device__ Selected radix_select(const RowView<E>& view, int32_t C, Shared& sh, Value value, Need need_of) {
-  constexpr int kLevels = E::kBytes == 2 ? 2 : 3;
+template <class E, int kThreads, class Source, class Value, class Need>
+__device__ Selected radix_select(const Source& source, Shared<kThreads>& sh, Value value, Need need_of) {
+  constexpr int kLevels = E::kBytes == 2 ? 2 : 3, kBins = 2048, kPer = kBins / kThreads;
   const int t = threadIdx.x;
   Selected r;
   r.key = 0;
   r.before = r.need = r.at = 0;
+#pragma unroll 1
   for (int level = 0; level < kLevels; ++level) {
     const int shift = level == 0 ? 21 : (E::kBytes == 2 ? 16 : (level == 1 ? 10 : 0));
     const int width = level == 0 ? 11 : (E::kBytes == 2 ? 5 : (level == 1 ? 11 : 10));
     const int bins = 1 << width;
     __syncthreads();
-    for (int b = t; b < kBins; b += kDrawThreads) sh.hist[b] = 0;
+    for (int b = t; b < kBins; b += kThreads) sh.hist[b] = 0;
     __syncthreads();
-    each_element<E, kVpl>(view, C, [&](float z) {
+    source.each([&](float z) {
       const uint32_t key = order_key(z);
       if (level > 0 && ((key ^ r.key) >> (shift + width)) != 0) return;
       const uint64_t x = value(z);
@@ -333,21 +486,25 @@ __device__ Selected radix_select(const RowView<E>& view, int32_t C, Shared& sh, 
         atomicAdd(reinterpret_cast<unsigned long long*>(&sh.hist[(key >> shift) & (bins - 1)]), (unsigned long long)x);
     });
     __syncthreads();
-    // two bins per thread, from the top bin down
-    const int hi = bins - 1 - 2 * t, lo = hi - 1;
-    const uint64_t x = hi >= 0 ? sh.hist[hi] : 0, y = lo >= 0 ? sh.hist[lo] : 0;
+    // kPer bins per thread, from the top bin down
+    uint64_t own = 0;
+    for (int b = 0; b < kPer; ++b) {
+      const int bin = bins - 1 - (kPer * t + b);
+      own += bin >= 0 ? sh.hist[bin] : 0;
+    }
     uint64_t total;
-    const uint64_t pre = block_scan(x + y, sh.wave_u, total);
+    uint64_t pre = block_scan<kThreads / kWave>(own, sh.wave_u, total);
     if (level == 0) r.need = need_of(total);
     const uint64_t want = r.need - r.before;
-    if (pre < want && pre + x >= want) {
-      sh.found_bin = hi;
-      sh.found_before = r.before + pre;
-      sh.found_at = x;
-    } else if (pre + x < want && pre + x + y >= want) {
-      sh.found_bin = lo;
-      sh.found_before = r.before + pre + x;
-      sh.found_at = y;
+    for (int b = 0; b < kPer; ++b) {
+      const int bin = bins - 1 - (kPer * t + b);
+      const uint64_t x = bin >= 0 ? sh.hist[bin] : 0;
+      if (pre < want && pre + x >= want) {
+        sh.found_bin = bin;
+        sh.found_before = r.before + pre;
+        sh.found_at = x;
+      }
+      pre += x;
     }
     __syncthreads();
     r.key |= sh.found_bin << shift;
@@ -358,330 +515,710 @@ __device__ Selected radix_select(const RowView<E>& view, int32_t C, Shared& sh, 
   return r;
 }
 
-template <class E, int kVpl>
-__global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
-  __shared__ Shared sh;
-  constexpr int kVecs = kVpl * kWave;  // vectors of a chunk
-  constexpr int P = E::kPerVec;
-  static_assert(kVecs <= kDrawThreads, "one vector of a chunk per thread");
-  const int t = threadIdx.x, lane = t & (kWave - 1);
-  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
-  const int64_t row = blockIdx.x;
-  const int64_t slot = slot_of(a, row);
-  RowState st;
-  st.m = st.k2 = st.inv_s = 0.0;
-  st.key = 0;
-  st.last = 0x7fffffff;
-  st.token = -1;
-  st.kind = kSkipped;
-  st.slot = slot;
-  if (slot < 0) {
-    if (a.probs && t == 0) a.state[row] = st;
-    return;
-  }
-  const RowView<E> view(a, row);
-  const Profile f = profile_of(a, row);
-  Record* rec = a.rec + row * a.C;
-  const int32_t C = a.C;
+struct Cut {
+  uint32_t key;  // kept: keys above it, and its first `copies` copies
+  uint64_t copies;
+};
 
-  float m = -__builtin_inff();
-  for (int32_t c = t; c < C; c += kDrawThreads) m = fmaxf(m, rec[c].m);
-  m = wave_max(m);
-  if (lane == 0) sh.wave_f[wave] = m;
-  if (t == 0) {
-    sh.chunk = 0x7fffffff;
-    sh.first = 0x7fffffff;
-    sh.last = -1;
-    sh.eq_last = 0x7fffffff;
-  }
+// Top-k and top-p of a bf16 row from one pass: the counts of the 4096 keys at and below the maximum's
+// (32 binades of positive logits) give ranks by prefix sums, and masses as count x weight, so no
+// other logit's weight is computed.  False if a cut lies below the window.  S: the whole row's mass
+// in the frame (used without top-k).
+template <class E, int kThreads, class Source>
+__device__ bool window_cut(const Source& source, Shared<kThreads>& sh, const Profile& f, const Frame& frame,
+                           uint32_t top, double S, Cut& cut) {
+  constexpr int kPer = kWindow / kThreads, kWaves = kThreads / kWave;
+  const int t = threadIdx.x;
+  uint32_t* const count = reinterpret_cast<uint32_t*>(sh.hist);
   __syncthreads();
-  for (int w = 0; w < kDrawWaves; ++w) m = fmaxf(m, sh.wave_f[w]);
-
-  const double u = f.greedy ? 0.0 : a.uniform[row];
-  if (!f.ok || !(m > -__builtin_inff() && m < __builtin_inff()) || !(u >= 0.0 && u < 1.0)) {
-    if (t == 0) {
-      a.tokens[slot] = -1;
-      a.prob[slot] = 0.0f;
-      if (a.kept) a.kept[slot] = 0;
-      st.kind = kNothing;
-      if (a.probs) a.state[row] = st;
-    }
-    return;
-  }
-
-  if (f.greedy) {  // the first chunk that holds the maximum, then its first element
-    for (int32_t c = t; c < C; c += kDrawThreads)
-      if (rec[c].m == m) atomicMin(&sh.chunk, c);
-    __syncthreads();
-    const int64_t j = (int64_t)sh.chunk * kVecs + t;
-    if (t < kVecs) {
-      float z[P];
-      E::unpack(view.vec_edge(j), z);
+  for (int b = t; b < kWindow; b += kThreads) count[b] = 0;
+  if (t == 0) sh.found_bin = kWindow;
+  __syncthreads();
+  const uint32_t top16 = top >> 16;
+  source.each([&](float z) {
+    const uint32_t d = top16 - (order_key(z) >> 16);
+    if (d < kWindow) atomicAdd(&count[d], 1u);
+  });
+  __syncthreads();
+  uint64_t c[kPer], own = 0;
 #pragma unroll
-      for (int e = P - 1; e >= 0; --e)
-        if (z[e] == m) atomicMin(&sh.first, (int32_t)(j * P + e - view.lead));
-    }
-    __syncthreads();
-    if (t == 0) {
-      a.tokens[slot] = sh.first;
-      a.prob[slot] = 1.0f;
-      if (a.kept) a.kept[slot] = 1;
-      st.token = sh.first;
-      st.kind = kOneToken;
-      if (a.probs) a.state[row] = st;
-    }
-    return;
+  for (int b = 0; b < kPer; ++b) {
+    c[b] = count[kPer * t + b];
+    own += c[b];
   }
-
-  const Frame frame(m, kLog2e / f.T);
-  uint32_t cut_key = 0;  // kept: keys above it, and its first cut_copies copies
-  uint64_t cut_copies = ~0ull, k_copies_all = 0;
+  auto key_of = [&](uint32_t bin) { return ((top16 - bin) << 16) | 0xffffu; };
   if (f.top_k) {
     const uint64_t k = (uint64_t)f.k;
-    const Selected r = radix_select<E, kVpl>(
-        view, C, sh, [](float) { return (uint64_t)1; }, [k](uint64_t) { return k; });
-    cut_key = r.key;
-    cut_copies = k - r.before;
-    k_copies_all = r.at;
+    uint64_t total;
+    uint64_t pre = block_scan<kWaves>(own, sh.wave_u, total);
+    if (total < k) return false;
+#pragma unroll
+    for (int b = 0; b < kPer; ++b) {
+      if (pre < k && pre + c[b] >= k) {
+        sh.found_bin = kPer * t + b;
+        sh.found_before = k - pre;
+      }
+      pre += c[b];
+      if (pre > k) c[b] = pre - c[b] >= k ? 0 : c[b] - (pre - k);  // ranks behind k
+    }
+    __syncthreads();
+    cut.key = key_of(sh.found_bin);
+    cut.copies = sh.found_before;
   }
   if (f.top_p) {
-    // Masses as integers, with room for V of them in 62 bits.  The copies of the top-k key behind
-    // rank k count in the passes and are taken off the total; they rank last, so no prefix that
-    // the smaller sum asks for reaches them.
-    const int bits = 62 - (32 - __builtin_clz((unsigned)a.V));
-    auto mass = [&](float z) { return (uint64_t)__builtin_rint(__builtin_amdgcn_ldexp(frame.weight(z), bits)); };
-    const uint32_t k_key = cut_key;
-    const uint64_t p = (uint64_t)f.p;
-    const uint64_t over = f.top_k ? (k_copies_all - cut_copies) * mass(row_key_logit<E>(k_key)) : 0;
-    const Selected r = radix_select<E, kVpl>(
-        view, C, sh, [&](float z) { return row_key<E>(z) >= k_key ? mass(z) : (uint64_t)0; },
-        [&](uint64_t total) {
-          const uint64_t need = (uint64_t)(((unsigned __int128)(total - over) * p + 999) / 1000);
-          return need ? need : (uint64_t)1;
-        });
-    const uint64_t one = mass(row_key_logit<E>(r.key));
-    cut_key = r.key;
-    cut_copies = (r.need - r.before + one - 1) / one;
+    double w[kPer], x = 0.0;
+#pragma unroll
+    for (int b = 0; b < kPer; ++b) {
+      const uint32_t bin = kPer * t + b;
+      w[b] = bin <= top16 ? frame.weight(row_key_logit<E>(key_of(bin))) : 0.0;
+      x += (double)c[b] * w[b];
+    }
+    double total;
+    double pre = block_scan<kWaves>(x, sh.wave_d, total);
+    if (f.top_k) S = total;
+    const double want = (double)f.p * S;  // thousandths of S
+    int32_t bin = kNone;
+#pragma unroll
+    for (int b = kPer - 1; b >= 0; --b) {
+      double before = pre;
+#pragma unroll
+      for (int q = 0; q < b; ++q) before += (double)c[q] * w[q];
+      if (c[b] > 0 && (before + (double)c[b] * w[b]) * 1000.0 >= want) bin = kPer * t + b;
+    }
+    const int32_t first = block_first<kWaves>(bin, sh.wave_i[0]);
+    if (first == kNone) {
+      if (!f.top_k) return false;
+      return true;  // the sums' rounding: every rank of the top-k set is needed
+    }
+    if (bin == first) {
+      const int b = bin - kPer * t;
+      double before = pre, one = 0.0;
+      uint64_t n = 0;
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        if (q < b) before += (double)c[q] * w[q];
+        if (q == b) {
+          one = w[q];
+          n = c[q];
+        }
+      }
+      double need = ceil((want / 1000.0 - before) / one);
+      need = need < 1.0 ? 1.0 : (need > (double)n ? (double)n : need);
+      while (need > 1.0 && (before + (need - 1.0) * one) * 1000.0 >= want) need -= 1.0;
+      while (need < (double)n && (before + need * one) * 1000.0 < want) need += 1.0;
+      sh.found_before = (uint64_t)need;
+    }
+    __syncthreads();
+    cut.key = key_of(first);
+    cut.copies = sh.found_before;
+  }
+  return true;
+}
+
+// The cut of a row's profile.  S: the whole row's mass in the frame (of a row with top-p, without top-k).
+template <class E, int kThreads, class Source>
+__device__ Cut cut_of(const Source& source, Shared<kThreads>& sh, const Args& a, const Profile& f, const Frame& frame,
+                      float m, double S) {
+  Cut cut;
+  cut.key = 0;
+  cut.copies = ~0ull;
+  bool done = !f.top_k && !f.top_p;
+  if constexpr (E::kBytes == 2) {
+    if (!done) done = window_cut<E, kThreads>(source, sh, f, frame, row_key<E>(m), S, cut);
+  }
+  if (!done) {
+    uint64_t k_copies_all = 0;
+    cut.key = 0;
+    cut.copies = ~0ull;
+    if (f.top_k) {
+      const uint64_t k = (uint64_t)f.k;
+      const Selected r = radix_select<E, kThreads>(
+          source, sh, [](float) { return (uint64_t)1; }, [k](uint64_t) { return k; });
+      cut.key = r.key;
+      cut.copies = k - r.before;
+      k_copies_all = r.at;
+    }
+    if (f.top_p) {
+      // Masses as integers, with room for V of them in 62 bits.  The copies of the top-k key behind
+      // rank k count in the passes and are taken off the total; they rank last, so no prefix that
+      // the smaller sum asks for reaches them.
+      const int bits = 62 - (32 - __builtin_clz((unsigned)a.V));
+      auto mass = [&](float z) { return (uint64_t)__builtin_rint(__builtin_amdgcn_ldexp(frame.weight(z), bits)); };
+      const uint32_t k_key = cut.key;
+      const uint64_t p = (uint64_t)f.p;
+      const uint64_t over = f.top_k ? (k_copies_all - cut.copies) * mass(row_key_logit<E>(k_key)) : 0;
+      const Selected r = radix_select<E, kThreads>(
+          source, sh, [&](float z) { return row_key<E>(z) >= k_key ? mass(z) : (uint64_t)0; },
+          [&](uint64_t total) {
+            const uint64_t need = (uint64_t)(((unsigned __int128)(total - over) * p + 999) / 1000);
+            return need ? need : (uint64_t)1;
+          });
+      const uint64_t one = mass(row_key_logit<E>(r.key));
+      cut.key = r.key;
+      cut.copies = (r.need - r.before + one - 1) / one;
+    }
   }
   if (f.min_p > 0.0f) {
     // the smallest key of weight min_p or more lies within rounding of z_max + T ln(min_p)
-    if (wave == 0) {
+    __syncthreads();
+    const int lane = threadIdx.x & (kWave - 1);
+    if (threadIdx.x < kWave) {
       const float z0 = (float)((double)m + f.T * log((double)f.min_p));
       const int64_t step = E::kBytes == 2 ? 0x10000 : 1;
       const int64_t k = (int64_t)row_key<E>(z0) + (lane - 32) * step;
       const bool in = k >= 0 && k <= 0xffffffffll;
       const bool reach = in && frame.weight(row_key_logit<E>((uint32_t)k)) >= (double)f.min_p;
       const uint64_t who = __ballot(reach);
-      if (who && lane == __ffsll((unsigned long long)who) - 1) sh.key = (uint32_t)k;
-      if (!who && lane == 0) sh.key = row_key<E>(m);
+      if (who ? lane == __ffsll((unsigned long long)who) - 1 : lane == 0) sh.key = who ? (uint32_t)k : row_key<E>(m);
     }
     __syncthreads();
-    if (sh.key > cut_key) {
-      cut_key = sh.key;
-      cut_copies = ~0ull;
+    if (sh.key > cut.key) {
+      cut.key = sh.key;
+      cut.copies = ~0ull;
     }
   }
+  return cut;
+}
 
-  int64_t n_kept = a.V;
-  if (f.cut) {
-    // each chunk's mass above the cut and its copies of the cut's key
-    uint32_t above = 0;
-    for (int32_t c = wave; c < C; c += kDrawWaves) {
-      u32x4 v[kVpl];
-      view.template chunk<kVpl>(c, lane, v);
-      const int64_t j0 = (int64_t)c * kVecs + lane;
-      double s = 0.0;
-      uint32_t eq = 0;
+__device__ __forceinline__ RowState empty_state(int64_t slot, int32_t kind) {
+  RowState st;
+  st.base = st.k2 = 0.0;
+  st.inv_s = 0.0f;
+  st.exp_s = 0;
+  st.key = 0;
+  st.last = kNone;
+  st.token = -1;
+  st.kind = kind;
+  st.slot = slot;
+  return st;
+}
+
+__device__ __forceinline__ void write_token(const Args& a, int64_t slot, int32_t token, float prob, int32_t kept) {
+  a.tokens[slot] = token;
+  a.prob[slot] = prob;
+  if (a.kept) a.kept[slot] = kept;
+}
+
+__device__ __forceinline__ RowState state_of(int64_t slot, double base, double k2, double S, const Cut& cut,
+                                             int32_t eq_last) {
+  RowState st = empty_state(slot, kDistribution);
+  st.base = base;
+  st.k2 = k2;
+  st.exp_s = __builtin_amdgcn_frexp_exp(S);
+  st.inv_s = (float)(1.0 / __builtin_amdgcn_frexp_mant(S));
+  st.key = cut.key;
+  st.last = eq_last;
+  return st;
+}
+
+// p(v) in binary32: the exponent in binary64, its fraction alone through the binary32 exponential.
+template <class E>
+__device__ __forceinline__ float prob_of(const RowState& st, double d_min, float z, int32_t v) {
+  const uint32_t key = row_key<E>(z);
+  if (!(key > st.key || (key == st.key && v <= st.last))) return 0.0f;
+  const double d = fmax((double)z - st.base, d_min);
+  const double n = __builtin_rint(d * st.k2);
+  return __builtin_amdgcn_ldexpf(fast_exp2((float)fma(d, st.k2, -n)) * st.inv_s, (int)n - st.exp_s);
+}
+
+template <int P>
+__device__ __forceinline__ void write_probs(float* out, const float (&p)[P]) {
 #pragma unroll
-      for (int i = 0; i < kVpl; ++i) {
+  for (int q = 0; q < P; q += 4) {
+    u32x4 y;
+    y.x = __float_as_uint(p[q]);
+    y.y = __float_as_uint(p[q + 1]);
+    y.z = __float_as_uint(p[q + 2]);
+    y.w = __float_as_uint(p[q + 3]);
+    __builtin_nontemporal_store(y, reinterpret_cast<u32x4*>(out + q));
+  }
+}
+
+template <class E, int kVpl, bool kCut>
+__global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
+  constexpr int kWaves = kDrawThreads / kWave;
+  constexpr int kVecs = kVpl * kWave;  // vectors of a chunk
+  constexpr int P = E::kPerVec;
+  static_assert(kVecs <= kDrawThreads, "one vector of a chunk per thread");
+  __shared__ Shared<kDrawThreads> sh;
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int64_t row = blockIdx.x;
+  const int64_t slot = slot_of(a, row);
+  if (slot < 0) {
+    if (a.probs && t == 0) a.state[row] = empty_state(slot, kSkipped);
+    return;
+  }
+  const RowView<E> view(a, row);
+  const Profile f = profile_of(a, row);
+  Record* rec = a.rec + row * a.C;
+  const int32_t C = a.C;
+  const double u = f.greedy ? 0.0 : a.uniform[row];
+
+  // Every wave folds the chunks for itself, 64 at a time: no barrier, and the same result in each.
+  float m = -__builtin_inff();
+  bool any_near = false, any_high = false;
+  const double k2 = f.ok && !f.greedy ? kLog2e / f.T : 1.0;
+  for (int32_t c = lane; c < C; c += kWave) {
+    const Record r = rec[c];
+    if (r.far) {
+      m = fmaxf(m, r.m);
+      any_high = any_high || (double)r.m * k2 > 900.0;
+    } else {
+      any_near = true;
+    }
+  }
+  m = wave_max(m);
+  const bool plain = f.ok && !f.greedy && !(kCut && f.cut);
+  const bool near = plain && __any(any_near) && !__any(any_high);
+  const bool finite = near || (m > -__builtin_inff() && m < __builtin_inff());
+  if (!f.ok || !finite || !(u >= 0.0 && u < 1.0)) {
+    if (t == 0) {
+      write_token(a, slot, -1, 0.0f, 0);
+      if (a.probs) a.state[row] = empty_state(slot, kNothing);
+    }
+    return;
+  }
+
+  if (f.greedy) {  // the first chunk that holds the maximum, then its first element
+    int32_t chunk = 0;
+    for (int32_t c0 = 0; c0 < C; c0 += kWave) {
+      const uint64_t who = __ballot(c0 + lane < C && rec[c0 + lane < C ? c0 + lane : 0].m == m);
+      if (who) {
+        chunk = c0 + __ffsll((unsigned long long)who) - 1;
+        break;
+      }
+    }
+    const int32_t j = chunk * kVecs + t;
+    int32_t id = kNone;
+    if (t < kVecs) {
+      float z[P];
+      E::unpack(view.one(j), z);
+#pragma unroll
+      for (int e = P - 1; e >= 0; --e)
+        if (z[e] == m) id = j * P + e - view.lead;
+    }
+    const int32_t y = block_first<kWaves>(id, sh.wave_i[0]);
+    if (t == 0) {
+      write_token(a, slot, y, 1.0f, 1);
+      if (a.probs) {
+        RowState st = empty_state(slot, kOneToken);
+        st.token = y;
+        a.state[row] = st;
+      }
+    }
+    return;
+  }
+
+  const double base = near ? 0.0 : (double)m;
+  const Frame frame(base, k2);
+  // a chunk's mass in the row's frame
+  const double near_scale = near ? 1.0 : frame.weight(0.0f);
+  auto stats_mass = [&](const Record& r) { return r.far ? (r.s > 0.0 ? r.s * frame.weight(r.m) : 0.0) : r.s * near_scale; };
+
+  Cut cut;
+  cut.key = 0;
+  cut.copies = ~0ull;
+  int64_t n_kept = a.V;
+  int32_t eq_last = kNone;
+  if (kCut && f.cut) {
+    double S = 0.0;
+    if (f.top_p && !f.top_k) {
+      for (int32_t c = lane; c < C; c += kWave) S += stats_mass(rec[c]);
+      S = wave_sum(S);
+    }
+    const MemorySource<E, kDrawThreads> source{view};
+    cut = cut_of<E, kDrawThreads>(source, sh, a, f, frame, m, S);
+
+    // Each chunk's mass above the cut and its copies of the cut's key.  The logits above it are
+    // gathered in shared memory first, 64 to a weight: computing weights in place would
+    // cost every lane the exponential for the few that are kept.
+    __shared__ float gather_s[kWaves][kWave + P * kWave];
+    float* const list = gather_s[wave];
+    const float z_cut = row_key_logit<E>(cut.key);
+    uint32_t above = 0;
+    for (int32_t c = wave; c < C; c += kWaves) {
+      double s = 0.0;
+      uint32_t eq = 0, held = 0;
+      source.vectors(c * kVecs, (c + 1) * kVecs, kWave, [&](int32_t, u32x4 v, bool) {
         float z[P];
-        E::unpack(v[i], z);
+        E::unpack(v, z);
 #pragma unroll
         for (int e = 0; e < P; ++e) {
-          const int64_t at = (j0 + i * kWave) * P + e;
-          const uint32_t key = row_key<E>(z[e]);
-          if (key < cut_key || at < view.lead || at >= view.end) continue;
-          if (key == cut_key) {
-            ++eq;
-          } else {
-            ++above;
-            s += frame.weight(z[e]);
-          }
+          const bool more = z[e] > z_cut;
+          const uint64_t over = __ballot(more);
+          if (more)
+            list[held + __builtin_amdgcn_mbcnt_hi((uint32_t)(over >> 32),
+                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)over, 0))] = z[e];
+          held += __builtin_popcountll(over);
+          eq += fmaxf(z[e], -__builtin_inff()) == z_cut;
         }
-      }
+        while (held >= kWave) {
+          held -= kWave;
+          s += frame.weight(list[held + lane]);
+          above += kWave;
+        }
+      });
+      if (lane < held) s += frame.weight(list[lane]);
+      above += held;
       s = wave_sum(s);
       eq = wave_sum_u32(eq);
+      if (z_cut == -__builtin_inff()) {  // what the chunk holds beside the row came as -inf
+        const int32_t lo = c * kVecs * P, hi = lo + kVecs * P;
+        eq -= (view.lead > lo ? view.lead - lo : 0) + (view.end < hi ? hi - view.end : 0);
+      }
       if (lane == 0) {
         rec[c].s = s;
-        rec[c].eq = eq;
+        rec[c].far = eq;
       }
     }
     uint64_t n_above;
-    (void)block_scan((uint64_t)above, sh.wave_u, n_above);
+    (void)block_scan<kWaves>((uint64_t)(lane == 0 ? above : 0), sh.wave_u, n_above);
     __syncthreads();
     // the kept copies, first chunk first
-    const double one = frame.weight(row_key_logit<E>(cut_key));
+    const double one = frame.weight(z_cut);
     uint64_t seen = 0;
     for (int32_t c0 = 0; c0 < C; c0 += kDrawThreads) {
       const int32_t c = c0 + t;
-      const uint64_t eq = c < C ? rec[c].eq : 0;
+      const uint64_t eq = c < C ? rec[c].far : 0;
       uint64_t total;
-      const uint64_t pre = seen + block_scan(eq, sh.wave_u, total);
-      const uint64_t take = pre >= cut_copies ? 0 : (cut_copies - pre < eq ? cut_copies - pre : eq);
+      const uint64_t pre = seen + block_scan<kWaves>(eq, sh.wave_u, total);
+      const uint64_t take = pre >= cut.copies ? 0 : (cut.copies - pre < eq ? cut.copies - pre : eq);
       if (c < C) rec[c].s += (double)take * one;
-      if (take > 0 && take < eq) {  // the cut runs through this chunk's copies
-        sh.chunk = c;
-        sh.found_before = take;
-      } else if (take == eq && eq > 0 && pre + eq == cut_copies) {  // or behind its last one
+      if (take > 0 && pre + take == cut.copies) {  // the last kept copy is in this chunk
         sh.chunk = c;
         sh.found_before = take;
       }
       seen += total;
     }
     __syncthreads();
-    n_kept = (int64_t)(n_above + (cut_copies < seen ? cut_copies : seen));
-    if (cut_copies < seen) {
-      const int64_t j = (int64_t)sh.chunk * kVecs + t;
+    n_kept = (int64_t)(n_above + (cut.copies < seen ? cut.copies : seen));
+    if (cut.copies < seen) {
+      const int32_t j = sh.chunk * kVecs + t;
       const uint64_t want = sh.found_before;
       uint64_t eq = 0;
       float z[P];
-      E::unpack(view.vec_edge(t < kVecs ? j : 0), z);
+      E::unpack(view.one(t < kVecs ? j : 0), z);
       auto is = [&](int e) {
-        const int64_t at = j * P + e;
-        return t < kVecs && at >= view.lead && at < view.end && row_key<E>(z[e]) == cut_key;
+        const int32_t at = j * P + e;
+        return t < kVecs && at >= view.lead && at < view.end && row_key<E>(z[e]) == cut.key;
       };
 #pragma unroll
       for (int e = 0; e < P; ++e) eq += is(e);
       uint64_t total;
-      uint64_t pre = block_scan(eq, sh.wave_u, total);
+      uint64_t pre = block_scan<kWaves>(eq, sh.wave_u, total);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        if (!is(e)) continue;
-        if (++pre == want) sh.eq_last = (int32_t)(j * P + e - view.lead);
+        if (is(e) && ++pre == want) sh.eq_last = j * P + e - view.lead;
       }
       __syncthreads();
+      eq_last = sh.eq_last;
     }
   }
-  const int32_t eq_last = sh.eq_last;
 
   // S, and the chunk the uniform lands in
-  auto mass_of = [&](int32_t c) {
-    return c < C ? (f.cut ? rec[c].s : rec[c].s * frame.weight(rec[c].m)) : 0.0;
-  };
+  auto mass_of = [&](int32_t c) { return c < C ? (kCut && f.cut ? rec[c].s : stats_mass(rec[c])) : 0.0; };
   double S = 0.0;
-  for (int32_t c0 = 0; c0 < C; c0 += kDrawThreads) {
-    double total;
-    (void)block_scan(mass_of(c0 + t), sh.wave_d, total);
-    S += total;
-  }
+  for (int32_t c0 = 0; c0 < C; c0 += kWave) S += mass_of(c0 + lane);
+  S = wave_sum(S);
   const double target = u * S;
-  if (t == 0) sh.chunk = 0x7fffffff;
-  double carry = 0.0;
-  for (int32_t c0 = 0; c0 < C; c0 += kDrawThreads) {
-    double total;
-    const double x = mass_of(c0 + t);
-    const double pre = carry + block_scan(x, sh.wave_d, total);
-    if (x > 0.0 && pre + x > target) atomicMin(&sh.chunk, c0 + t);
-    if (x > 0.0) atomicMax(&sh.last, c0 + t);
-    __syncthreads();
-    if (sh.chunk == c0 + t) sh.before = pre;
-    carry += total;
+  double carry = 0.0, before = 0.0;
+  int32_t chunk = -1, last_chunk = 0;
+  for (int32_t c0 = 0; c0 < C && chunk < 0; c0 += kWave) {
+    const double x = mass_of(c0 + lane);
+    const double inc = carry + wave_detail::inclusive_scan(x);
+    const uint64_t hit = __ballot(x > 0.0 && inc > target), some = __ballot(x > 0.0);
+    if (some) last_chunk = c0 + 63 - __builtin_clzll(some);
+    if (hit) {
+      const int who = __ffsll((unsigned long long)hit) - 1;
+      chunk = c0 + who;
+      before = lane_value(inc - x, who);
+    }
+    carry = lane_value(inc, kWave - 1);
   }
-  __syncthreads();
   // u S within rounding of S: the last chunk with a kept weight, and its last kept token
-  const bool past = sh.chunk == 0x7fffffff;
-  const int32_t chunk = past ? sh.last : sh.chunk;
-  const double before = past ? 0.0 : sh.before;
-  __syncthreads();
-  if (t == 0) sh.last = -1;
-  const int64_t j = (int64_t)chunk * kVecs + t;
+  const bool past = chunk < 0;
+  if (past) chunk = last_chunk;
+  const int32_t j = chunk * kVecs + t;
   double w[P], sum = 0.0;
   {
     float z[P];
-    E::unpack(view.vec_edge(t < kVecs ? j : 0), z);
+    E::unpack(view.one(t < kVecs ? j : 0), z);
 #pragma unroll
     for (int e = 0; e < P; ++e) {
-      const int64_t at = j * P + e;
+      const int32_t at = j * P + e;
       bool keep = t < kVecs && at >= view.lead && at < view.end;
-      if (f.cut) {
+      if (kCut && f.cut) {
         const uint32_t key = row_key<E>(z[e]);
-        keep = keep && (key > cut_key || (key == cut_key && at - view.lead <= eq_last));
+        keep = keep && (key > cut.key || (key == cut.key && at - view.lead <= eq_last));
       }
       w[e] = keep ? frame.weight(z[e]) : 0.0;
       sum += w[e];
     }
   }
   double total;
-  double run = before + block_scan(sum, sh.wave_d, total);
+  double run = before + block_scan<kWaves>(sum, sh.wave_d, total);
+  int32_t first = kNone, last = kNone;
+  float first_p = 0.0f, last_p = 0.0f;
 #pragma unroll
   for (int e = 0; e < P; ++e) {
     if (!(w[e] > 0.0)) continue;
     run += w[e];
-    const int32_t id = (int32_t)(j * P + e - view.lead);
-    if (!past && run > target) atomicMin(&sh.first, id);
-    atomicMax(&sh.last, id);
-  }
-  __syncthreads();
-  const int32_t y = sh.first != 0x7fffffff ? sh.first : sh.last;
-#pragma unroll
-  for (int e = 0; e < P; ++e) {
-    if (t < kVecs && w[e] > 0.0 && (int32_t)(j * P + e - view.lead) == y) {
-      a.tokens[slot] = y;
-      a.prob[slot] = (float)(w[e] / S);
-      if (a.kept) a.kept[slot] = (int32_t)n_kept;
+    const int32_t id = j * P + e - view.lead;
+    last = id;
+    last_p = (float)(w[e] / S);
+    if (!past && run > target && first == kNone) {
+      first = id;
+      first_p = last_p;
     }
   }
-  if (a.probs && t == 0) {
-    st.m = (double)m;
-    st.k2 = frame.k2;
-    st.inv_s = 1.0 / S;
-    st.key = cut_key;
-    st.last = eq_last;
-    st.kind = kDistribution;
-    a.state[row] = st;
+  const int32_t y = block_first<kWaves>(first, sh.wave_i[0]);
+  const int32_t y_last = block_last<kWaves>(last, sh.wave_i[1]);
+  if (y != kNone ? first == y : last == y_last && last != kNone)
+    write_token(a, slot, y != kNone ? y : y_last, y != kNone ? first_p : last_p, (int32_t)n_kept);
+  if (a.probs && t == 0) a.state[row] = state_of(slot, base, k2, S, cut, eq_last);
+}
+
+// A row of at most kThreads x kVecs vectors, in one launch: it stays in shared memory.  Sums per
+// vector go to shared memory too, and each thread takes kVecs neighbouring ones, so prefix sums over the
+// threads are prefix sums over the ids.
+template <class E, int kThreads, int kVecs, bool kCut>
+__global__ __launch_bounds__(kThreads) void row_whole(Args a) {
+  constexpr int kWaves = kThreads / kWave, P = E::kPerVec;
+  __shared__ Shared<kThreads> sh;
+  __shared__ u32x4 row_s[kThreads * kVecs];
+  static_assert(kThreads * kVecs <= kWindow, "the sums take the histogram's place");
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int64_t row = blockIdx.x;
+  const int64_t slot = slot_of(a, row);
+  if (slot < 0) return;
+  const RowView<E> view(a, row);
+  const SharedSource<E, kThreads> x{row_s, (view.end + P - 1) / P, view.lead, a.V};
+  float m = -__builtin_inff();
+  {
+    u32x4 v[kVecs];
+    view.template edge<kVecs>(t, kThreads, v);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      float z[P];
+      E::unpack(v[i], z);
+#pragma unroll
+      for (int e = 0; e < P; ++e) m = fmaxf(m, z[e]);
+      row_s[i * kThreads + t] = v[i];  // read back by this thread alone, but for the draw's last step
+    }
   }
+  const Profile f = profile_of(a, row);
+  const double u = f.greedy ? 0.0 : a.uniform[row];
+  m = wave_max(m);
+  if (lane == 0) sh.wave_f[wave] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sh.wave_f[w]);
+
+  RowState st = empty_state(slot, kNothing);
+  if (f.ok && m > -__builtin_inff() && m < __builtin_inff() && u >= 0.0 && u < 1.0) {
+    if (f.greedy) {
+      if (t == 0) sh.chunk = kNone;
+      __syncthreads();
+      int32_t id = kNone;
+      x.vectors([&](int32_t, int32_t id0, u32x4 v) {
+        float z[P];
+        E::unpack(v, z);
+#pragma unroll
+        for (int e = P - 1; e >= 0; --e) id = z[e] == m && id0 + e < id ? id0 + e : id;
+      });
+      if (id != kNone) atomicMin(&sh.chunk, id);
+      __syncthreads();
+      st.kind = kOneToken;
+      st.token = sh.chunk;
+      if (t == 0) write_token(a, slot, st.token, 1.0f, 1);
+    } else {
+      const Frame frame(m, kLog2e / f.T);
+      double* const sums = reinterpret_cast<double*>(sh.hist);
+      Cut cut;
+      cut.key = 0;
+      cut.copies = ~0ull;
+      int32_t eq_last = kNone;
+      int64_t n_kept = a.V;
+      if (kCut && f.cut) {
+        double S = 0.0;
+        if (f.top_p && !f.top_k) {
+          double s = 0.0;
+          x.each([&](float z) { s += frame.weight(z); });
+          (void)block_scan<kWaves>(s, sh.wave_d, S);
+        }
+        cut = cut_of<E, kThreads>(x, sh, a, f, frame, m, S);
+        uint64_t n = 0;  // kept above the cut in the high half, copies of its key in the low one
+        x.each([&](float z) {
+          const uint32_t key = row_key<E>(z);
+          n += (key > cut.key ? 1ull << 32 : 0) + (key == cut.key ? 1ull : 0);
+        });
+        uint64_t all;
+        (void)block_scan<kWaves>(n, sh.wave_u, all);
+        const uint64_t n_eq = all & 0xffffffffu;
+        n_kept = (int64_t)((all >> 32) + (cut.copies < n_eq ? cut.copies : n_eq));
+        if (cut.copies < n_eq) {  // the id of the last kept copy
+          auto copies = [&](int32_t j, auto found) {
+            float z[P];
+            E::unpack(row_s[j], z);
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+              const int32_t id = j * P - view.lead + e;
+              if ((uint32_t)id < (uint32_t)a.V && row_key<E>(z[e]) == cut.key) found(id);
+            }
+          };
+          __syncthreads();
+          uint64_t eq = 0;
+          for (int i = 0; i < kVecs; ++i) {
+            const int32_t j = t * kVecs + i;
+            if (j < x.n) copies(j, [&](int32_t) { ++eq; });
+          }
+          uint64_t total;
+          uint64_t pre = block_scan<kWaves>(eq, sh.wave_u, total);
+          if (pre < cut.copies && pre + eq >= cut.copies) {
+            for (int i = 0; i < kVecs; ++i) {
+              const int32_t j = t * kVecs + i;
+              if (j < x.n)
+                copies(j, [&](int32_t id) {
+                  if (++pre == cut.copies) sh.eq_last = id;
+                });
+            }
+          }
+          __syncthreads();
+          eq_last = sh.eq_last;
+        }
+      }
+      auto weight_at = [&](int32_t id, float z) {  // -inf beside the row weighs 0
+        const uint32_t key = row_key<E>(z);
+        const bool keep = !kCut || !f.cut || key > cut.key || (key == cut.key && id <= eq_last);
+        return keep ? frame.weight(z) : 0.0;
+      };
+      __syncthreads();
+      x.vectors([&](int32_t j, int32_t id0, u32x4 v) {
+        float z[P];
+        E::unpack(v, z);
+        double s = 0.0;
+#pragma unroll
+        for (int e = 0; e < P; ++e) s += weight_at(id0 + e, z[e]);
+        sums[j] = s;
+      });
+      __syncthreads();
+      double own[kVecs], s = 0.0;
+      int32_t last = kNone;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int32_t j = t * kVecs + i;
+        own[i] = j < x.n ? sums[j] : 0.0;
+        s += own[i];
+        last = own[i] > 0.0 ? j : last;
+      }
+      double S;
+      const double pre = block_scan<kWaves>(s, sh.wave_d, S);
+      const double target = u * S;
+      int32_t first = kNone;
+      double run = pre, before = 0.0;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        if (first == kNone && own[i] > 0.0 && run + own[i] > target) {
+          first = t * kVecs + i;
+          before = run;
+        }
+        run += own[i];
+      }
+      // the first vector whose sums pass the target; else (u S within rounding of S) the last one with a kept value
+      const int32_t j_last = block_last<kWaves>(last, sh.wave_i[1]);
+      const int32_t j_first = block_first<kWaves>(first, sh.wave_i[0]);
+      const bool past = j_first == kNone;
+      if (past ? last == j_last && last != kNone : first == j_first) {
+        const int32_t j = past ? last : first;
+        float z[P];
+        E::unpack(row_s[j], z);
+        int32_t y = kNone;
+        double w_y = 0.0;
+        run = before;
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+          const int32_t id = j * P - view.lead + e;
+          const double w = weight_at(id, z[e]);
+          // the first value past the target, or the last kept one
+          if (w > 0.0 && (past || y == kNone || !(run > target))) {
+            y = id;
+            w_y = w;
+          }
+          run += w;
+        }
+        write_token(a, slot, y, (float)(w_y / S), (int32_t)n_kept);
+      }
+      st = state_of(slot, frame.base, frame.k2, S, cut, eq_last);
+    }
+  } else if (t == 0) {
+    write_token(a, slot, -1, 0.0f, 0);
+  }
+  if (!a.probs) return;
+  float* out = a.probs + slot * a.V;
+  const double d_min = st.kind == kDistribution ? -1100.0 / st.k2 : 0.0;
+  const bool grid = ((reinterpret_cast<uintptr_t>(out) - view.lead * 4) & 15) == 0;
+  x.vectors([&](int32_t, int32_t id0, u32x4 v) {
+    float z[P], p[P];
+    E::unpack(v, z);
+#pragma unroll
+    for (int e = 0; e < P; ++e)
+      p[e] = st.kind == kDistribution ? prob_of<E>(st, d_min, z[e], id0 + e) : (id0 + e == st.token ? 1.0f : 0.0f);
+    if (grid && id0 >= 0 && id0 + P <= a.V) {
+      write_probs<P>(out + id0, p);
+    } else {
+#pragma unroll
+      for (int e = 0; e < P; ++e)
+        if ((uint32_t)(id0 + e) < (uint32_t)a.V) out[id0 + e] = p[e];
+    }
+  });
 }
 
 constexpr int kProbThreads = 256;
-constexpr int kProbTile = 2048;
 
+// The probability rows: a thread reads one vector of logits and writes its P values; on the 16-byte grid of
+// both as whole vectors.
 template <class E>
 __global__ __launch_bounds__(kProbThreads) void row_probs(Args a, int32_t tiles) {
+  constexpr int P = E::kPerVec, kTile = kProbThreads * P;
   const int64_t row = blockIdx.x / tiles;
-  const int32_t v0 = (int32_t)(blockIdx.x - row * tiles) * kProbTile;
   const RowState st = a.state[row];
   if (st.kind == kSkipped) return;
+  const int64_t v0 = (int64_t)(blockIdx.x - row * tiles) * kTile;
   float* out = a.probs + st.slot * a.V;
   const char* in = row_ptr_strided<E>(a, row);
-  const float scale = (float)st.inv_s;
-  for (int32_t v = v0 + threadIdx.x; v < v0 + kProbTile && v < a.V; v += kProbThreads) {
-    float p = 0.0f;
-    if (st.kind == kOneToken) {
-      p = v == st.token ? 1.0f : 0.0f;
-    } else if (st.kind == kDistribution) {
-      const float z = E::at(in, v);
-      const uint32_t key = row_key<E>(z);
-      if (key > st.key || (key == st.key && v <= st.last)) {
-        // the exponent in binary64, its fraction alone through the binary32 exponential
-        const double d = fmax((double)z - st.m, -1100.0 / st.k2) * st.k2;
-        const double n = __builtin_rint(d);
-        p = __builtin_amdgcn_ldexpf(fast_exp2((float)(d - n)) * scale, (int)n);
-      }
-    }
-    out[v] = p;
+  const double d_min = st.kind == kDistribution ? -1100.0 / st.k2 : 0.0;
+  const int t = threadIdx.x;
+  const bool grid = ((reinterpret_cast<uintptr_t>(in) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
+  if (grid && v0 + kTile <= a.V) {
+    const int32_t v = (int32_t)v0 + t * P;
+    float z[P], p[P];
+    u32x4 x;
+    x.x = x.y = x.z = x.w = 0;
+    if (st.kind == kDistribution) x = *reinterpret_cast<const u32x4*>(in + (int64_t)v * E::kBytes);
+    E::unpack(x, z);
+#pragma unroll
+    for (int e = 0; e < P; ++e)
+      p[e] = st.kind == kDistribution ? prob_of<E>(st, d_min, z[e], v + e) : (v + e == st.token ? 1.0f : 0.0f);
+    write_probs<P>(out + v, p);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    const int64_t v = v0 + e * kProbThreads + t;
+    if (v >= a.V) break;
+    out[v] = st.kind == kDistribution ? prob_of<E>(st, d_min, E::at(in, v), (int32_t)v) : (v == st.token ? 1.0f : 0.0f);
   }
 }
 
 // Units below which the chunks are a quarter as long, so that a small batch spreads over the card.
 constexpr int64_t kFullUnits = 1024;
-
-template <class E>
-constexpr int32_t chunk_elems(int vpl) {
-  return vpl * kWave * E::kPerVec;
-}
+constexpr int32_t kMostChunks = 256;  // a wave folds a row's chunks 64 at a time
 
 struct Plan {
-  int vpl;
+  int vpl;           // 16 or 4: chunks; 0: the row in one workgroup
+  int threads, vecs; // then its shape
   int32_t C;
   size_t rec_bytes, bytes;
 };
@@ -691,23 +1228,51 @@ inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Chunks of a row of V elements that may begin anywhere in its first 16-byte block.
 inline Plan plan_of(int64_t n, int32_t V, int32_t dtype) {
   const int64_t per = dtype == SDV_BF16 ? 8 : 4, vecs = ((int64_t)V + 2 * per - 2) / per;
-  Plan p;
-  p.vpl = n * ((vecs + 16 * kWave - 1) / (16 * kWave)) >= kFullUnits ? 16 : 4;
+  Plan p = {};
+  if (vecs <= 4 * kDrawThreads) {
+    p.threads = vecs <= 256 ? 256 : kDrawThreads;
+    p.vecs = vecs <= kDrawThreads ? 1 : 4;
+    p.C = 1;
+    p.bytes = 256;
+    return p;
+  }
+  p.vpl = 16;
+  if (n * ((vecs + 16 * kWave - 1) / (16 * kWave)) < kFullUnits && vecs <= 4 * kWave * kMostChunks) p.vpl = 4;
   p.C = (int32_t)((vecs + p.vpl * kWave - 1) / (p.vpl * kWave));
   p.rec_bytes = up256((size_t)n * p.C * sizeof(Record));
   p.bytes = p.rec_bytes + up256((size_t)n * sizeof(RowState));
   return p;
 }
 
-template <class E, int kVpl>
-int launch(const Args& a, hipStream_t stream) {
+template <class E>
+constexpr int64_t prob_tiles(int32_t V) {
+  return ((int64_t)V + kProbThreads * E::kPerVec - 1) / (kProbThreads * E::kPerVec);
+}
+
+template <class E, int kVpl, bool kCut>
+int launch_chunks(const Args& a, hipStream_t stream) {
   const int64_t groups = (a.n * a.C + kStatsWaves - 1) / kStatsWaves;
   hipLaunchKernelGGL((row_stats<E, kVpl>), dim3((unsigned)groups), dim3(kStatsWaves * kWave), 0, stream, a);
-  hipLaunchKernelGGL((row_draw<E, kVpl>), dim3((unsigned)a.n), dim3(kDrawThreads), 0, stream, a);
+  hipLaunchKernelGGL((row_draw<E, kVpl, kCut>), dim3((unsigned)a.n), dim3(kDrawThreads), 0, stream, a);
   if (a.probs) {
-    const int32_t tiles = (int32_t)(((int64_t)a.V + kProbTile - 1) / kProbTile);
+    const int32_t tiles = (int32_t)prob_tiles<E>(a.V);
     hipLaunchKernelGGL((row_probs<E>), dim3((unsigned)(a.n * tiles)), dim3(kProbThreads), 0, stream, a, tiles);
   }
+  return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
+}
+
+// kCut: the call carries a truncation.  Calls without take kernels that hold no code for one.
+template <class E, bool kCut>
+int launch(const Args& a, const Plan& p, hipStream_t stream) {
+  if (p.vpl == 16) return launch_chunks<E, 16, kCut>(a, stream);
+  if (p.vpl == 4) return launch_chunks<E, 4, kCut>(a, stream);
+  const dim3 grid((unsigned)a.n), block((unsigned)p.threads);
+  if (p.threads == 256)
+    hipLaunchKernelGGL((row_whole<E, 256, 1, kCut>), grid, block, 0, stream, a);
+  else if (p.vecs == 1)
+    hipLaunchKernelGGL((row_whole<E, kDrawThreads, 1, kCut>), grid, block, 0, stream, a);
+  else
+    hipLaunchKernelGGL((row_whole<E, kDrawThreads, 4, kCut>), grid, block, 0, stream, a);
   return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
 }
 
@@ -734,7 +1299,7 @@ extern "C" int sdv_sample(const void* logits, int64_t n_rows, int64_t row_stride
   if (o.slots ? o.n_slots < 0 || o.n_slots > INT32_MAX : o.n_slots != 0) return SDV_ERR_INVALID_ARG;
   const Plan p = n_rows <= INT32_MAX ? plan_of(n_rows, V, dtype) : Plan();
   if (n_rows > INT32_MAX || V > INT32_MAX - 64 || row_stride > ((int64_t)1 << 40) ||
-      n_rows * p.C > (int64_t)INT32_MAX || (o.probs && n_rows * (((int64_t)V + kProbTile - 1) / kProbTile) > INT32_MAX))
+      n_rows * p.C > (int64_t)INT32_MAX || (o.probs && n_rows * prob_tiles<F32>(V) > INT32_MAX))
     return SDV_ERR_LIMIT;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < p.bytes) return SDV_ERR_WORKSPACE;
   Args a = {};
@@ -758,6 +1323,7 @@ extern "C" int sdv_sample(const void* logits, int64_t n_rows, int64_t row_stride
   a.rec = static_cast<Record*>(workspace);
   a.state = reinterpret_cast<RowState*>(static_cast<char*>(workspace) + p.rec_bytes);
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (dtype == SDV_BF16) return p.vpl == 16 ? launch<Bf16, 16>(a, s) : launch<Bf16, 4>(a, s);
-  return p.vpl == 16 ? launch<F32, 16>(a, s) : launch<F32, 4>(a, s);
+  if (a.top_k || a.top_p || a.min_p)
+    return dtype == SDV_BF16 ? launch<Bf16, true>(a, p, s) : launch<F32, true>(a, p, s);
+  return dtype == SDV_BF16 ? launch<Bf16, false>(a, p, s) : launch<F32, false>(a, p, s);
 }
