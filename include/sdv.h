@@ -522,8 +522,9 @@ int sdv_sample(const void* logits, int64_t n_rows, int64_t row_stride, int32_t V
  * A page number outside [0, n_pages) is no page: slots there, and slots beyond max_pages *
  * page_size, are neither written nor seen (a serving engine frees the pages that left a window and
  * leaves -1).  Rows that no request names by valid offsets are left as they were.  A request with
- * cache_len < 0, or of a tree with more than 64 nodes or a parent outside [-1, n - 1], is passed
- * over: sdv_kv_append writes nothing of it, sdv_attend writes zeros for its rows.
+ * cache_len outside [0, INT32_MAX - 1024 - K), or of a tree with more than 64 nodes or a parent
+ * outside [-1, n - 1], is passed over: sdv_kv_append writes nothing of it, sdv_attend writes zeros
+ * for its rows.
  * page_size is a power of two in [1, 1024]; head_dim is 64, 128 or 256.
  */
 typedef struct sdv_cache {

@@ -415,14 +415,45 @@ def repad(offsets: torch.Tensor, accepted_len: torch.Tensor, out_tokens: torch.T
     return res
 
 
-def _scratch(nbytes: int, device: torch.device) -> torch.Tensor | None:
-    """Device scratch of a call: the stream's cached workspace, or, while a graph is captured, memory of
-    that graph's own (two graphs captured on one stream may be replayed on two)."""
+# The calls below take a few microseconds on the GPU for a small batch, so their checks are kept
+# short on the host: each tensor's fields are read once, and the device guard is entered only off the current device.
+_GET_DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_CAPTURING = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+_SCRATCH: dict = {}
+
+
+def _stream(index: int) -> int:
+    return _RAW_STREAM(index) if _RAW_STREAM is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _scratch(nbytes: int, device: torch.device, index: int, stream: int) -> torch.Tensor | None:
+    """Device scratch of a call on the current device: one buffer per stream, which the stream's order protects; or, while
+    a graph is captured, memory of that graph's own (two graphs captured on one stream may be
+    replayed on two)."""
     if nbytes == 0:
         return None
-    if torch.cuda.is_current_stream_capturing():
+    if _CAPTURING():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return _workspace(nbytes, device)
+    ws = _SCRATCH.get((index, stream))
+    if ws is None or ws.numel() < nbytes:
+        ws = _SCRATCH[index, stream] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws
+
+
+def _vector(t, dtype, n: int, index: int, name: str) -> int:
+    """The address of a contiguous vector of n values on device `index`."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (n,) and t.get_device() == index \
+            and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} values on the call's device")
+
+
+def _on(index: int, call):
+    """call(stream) with device `index` current."""
+    if _GET_DEVICE() == index:
+        return call(_stream(index))
+    with torch.cuda.device(index):
+        return call(_stream(index))
 
 
 def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, *, top_k: torch.Tensor | None = None,
@@ -436,99 +467,109 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, *, top_
     tensor to fill), "probs", the rows that verify_ex takes as draft_probs.  With slots (int32 [n]) row r's outputs
     go to index slots[r] of ``out`` = (tokens, prob), which is then given (kept_tokens and probs of as many rows); a
     slot outside it skips the row."""
-    if not logits.is_cuda:
-        raise ValueError("logits must be on the GPU")
-    if logits.dtype not in _DTYPES:
+    dt = _DTYPES.get(logits.dtype)
+    if dt is None:
         raise TypeError("logits must be bfloat16 or float32")
-    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
-        raise ValueError("logits must be an [n, V] tensor with neighbouring tokens next to each other")
-    dev = logits.device
+    index = logits.get_device()
+    if index < 0:
+        raise ValueError("logits must be on the GPU")
+    if logits.dim() != 2:
+        raise ValueError("logits must be an [n, V] tensor")
     n, V = logits.shape
-    stride = logits.stride(0) if n > 1 else max(V, logits.stride(0))
-    if n < 1 or V < 1 or stride < V:
-        raise ValueError("logits must be an [n, V] tensor of rows that do not overlap")
-    _device_vector(uniform, torch.float64, n, dev, "uniform")
+    stride, step = logits.stride()
+    if n < 1 or V < 1 or (step != 1 and V > 1) or (stride < V and n > 1):
+        raise ValueError("logits must be an [n, V] tensor of rows that do not overlap, neighbouring tokens next to each other")
+    dev = logits.device
     opt = _native.SdvSampleOptions()
     if isinstance(temperature, torch.Tensor):
-        opt.temperature = _device_vector(temperature, torch.float32, n, dev, "temperature").data_ptr()
+        opt.temperature = _vector(temperature, torch.float32, n, index, "temperature")
         temperature = 0.0
     if top_k is not None:
-        opt.top_k = _device_vector(top_k, torch.int32, n, dev, "top_k").data_ptr()
+        opt.top_k = _vector(top_k, torch.int32, n, index, "top_k")
     if top_p_milli is not None:
-        opt.top_p_milli = _device_vector(top_p_milli, torch.int32, n, dev, "top_p_milli").data_ptr()
+        opt.top_p_milli = _vector(top_p_milli, torch.int32, n, index, "top_p_milli")
     if min_p is not None:
-        opt.min_p = _device_vector(min_p, torch.float32, n, dev, "min_p").data_ptr()
-    n_out = n
+        opt.min_p = _vector(min_p, torch.float32, n, index, "min_p")
+    n_out, fresh = n, torch.empty
+    if slots is not None:
+        if out is None:
+            raise ValueError("slots place rows in given tensors: out is needed")
+        n_out, fresh = out[0].shape[0], torch.zeros
+        opt.slots = _vector(slots, torch.int32, n, index, "slots")
+        opt.n_slots = n_out
     if out is not None:
         tokens, prob = out
-        n_out = tokens.shape[0] if slots is not None else n
-        _device_vector(tokens, torch.int32, n_out, dev, "out[0]")
-        _device_vector(prob, torch.float32, n_out, dev, "out[1]")
-    elif slots is not None:
-        raise ValueError("slots place rows in given tensors: out is needed")
     else:
         tokens = torch.empty(n, dtype=torch.int32, device=dev)
         prob = torch.empty(n, dtype=torch.float32, device=dev)
-    if slots is not None:
-        opt.slots = _device_vector(slots, torch.int32, n, dev, "slots").data_ptr()
-        opt.n_slots = n_out
-    fresh = torch.empty if slots is None else torch.zeros
     if kept_tokens is None:
         kept_tokens = fresh(n_out, dtype=torch.int32, device=dev)
-    opt.kept_tokens = _device_vector(kept_tokens, torch.int32, n_out, dev, "kept_tokens").data_ptr()
+    opt.kept_tokens = _vector(kept_tokens, torch.int32, n_out, index, "kept_tokens")
     extra = {"kept_tokens": kept_tokens}
     if probs is not False and probs is not None:
         if probs is True:
             probs = fresh((n_out, V), dtype=torch.float32, device=dev)
-        elif probs.dtype != torch.float32 or probs.device != dev or probs.shape != (n_out, V) or not probs.is_contiguous():
+        elif probs.dtype is not torch.float32 or probs.get_device() != index or probs.shape != (n_out, V) \
+                or not probs.is_contiguous():
             raise ValueError("probs must be a contiguous float32 [n_out, V] tensor on the logits' device")
         opt.probs = probs.data_ptr()
         extra["probs"] = probs
-    dt = _DTYPES[logits.dtype]
+    p_u = _vector(uniform, torch.float64, n, index, "uniform")
+    p_tokens = _vector(tokens, torch.int32, n_out, index, "out[0]")
+    p_prob = _vector(prob, torch.float32, n_out, index, "out[1]")
     lib = _native.lib()
-    ctx, stream = _launch_on(dev)
-    with ctx:
-        ws = _scratch(lib.sdv_sample_workspace_bytes(n, V, dt), dev) if workspace is None else workspace
-        rc = lib.sdv_sample(logits.data_ptr(), n, stride, V, dt, float(temperature), uniform.data_ptr(),
-                            ctypes.byref(opt), tokens.data_ptr(), prob.data_ptr(), _ptr(ws),
-                            0 if ws is None else ws.numel() * ws.element_size(), stream)
+
+    def call(stream):
+        ws = workspace
+        if ws is None:
+            ws = _scratch(lib.sdv_sample_workspace_bytes(n, V, dt), dev, index, stream)
+        return lib.sdv_sample(logits.data_ptr(), n, stride if n > 1 else V, V, dt, float(temperature), p_u,
+                              ctypes.byref(opt), p_tokens, p_prob, _ptr(ws),
+                              0 if ws is None else ws.numel() * ws.element_size(), stream)
+
+    rc = _on(index, call)
     if rc != 0:
         raise SdvError(rc, "sdv_sample")
     return tokens, prob, extra
 
 
 def _cache(key_cache, value_cache, page_table, cache_len, offsets, layers=False):
-    """Checks one layer's cache (or, with layers, [L, ...] of them) and marshals it: (sdv_cache, B, dims)."""
-    dev = key_cache.device
-    if not key_cache.is_cuda:
-        raise ValueError("the cache must be on the GPU")
-    if key_cache.dtype not in _DTYPES:
+    """Checks one layer's cache (or, with layers, [L, ...] of them) and marshals it: (sdv_cache, device
+    index, B, address of the offsets, n_kv_heads, head_dim)."""
+    dt = _DTYPES.get(key_cache.dtype)
+    if dt is None:
         raise TypeError("the cache must be bfloat16 or float32")
-    if key_cache.dim() != (5 if layers and key_cache.dim() == 5 else 4) or not key_cache.is_contiguous():
+    index = key_cache.get_device()
+    if index < 0:
+        raise ValueError("the cache must be on the GPU")
+    shape = key_cache.shape
+    if len(shape) != 4 and not (layers and len(shape) == 5) or not key_cache.is_contiguous():
         raise ValueError("key_cache must be a contiguous [n_pages, n_kv_heads, page_size, head_dim] tensor")
-    if value_cache.dtype != key_cache.dtype or value_cache.device != dev or value_cache.shape != key_cache.shape \
+    if value_cache.dtype is not key_cache.dtype or value_cache.get_device() != index or value_cache.shape != shape \
             or not value_cache.is_contiguous():
         raise ValueError("value_cache must be like key_cache")
     B = offsets.shape[0] - 1
-    _device_vector(offsets, torch.int32, B + 1, dev, "offsets")
-    _device_vector(cache_len, torch.int32, B, dev, "cache_len")
-    if page_table.dtype != torch.int32 or page_table.device != dev or page_table.dim() != 2 \
-            or page_table.shape[0] != B or not page_table.is_contiguous():
+    p_offsets = _vector(offsets, torch.int32, B + 1, index, "offsets")
+    p_len = _vector(cache_len, torch.int32, B, index, "cache_len")
+    table = page_table.shape
+    if page_table.dtype is not torch.int32 or page_table.get_device() != index or len(table) != 2 or table[0] != B \
+            or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 [B, max_pages] tensor on the cache's device")
-    n_pages, heads, page_size, head_dim = key_cache.shape[-4:]
-    c = _native.SdvCache(key_cache.data_ptr(), value_cache.data_ptr(), page_table.data_ptr(), cache_len.data_ptr(),
-                         n_pages, page_table.shape[1], page_size, heads, head_dim, _DTYPES[key_cache.dtype])
-    return c, B, heads, head_dim
+    n_pages, heads, page_size, head_dim = shape[-4:]
+    return (_native.SdvCache(key_cache.data_ptr(), value_cache.data_ptr(), page_table.data_ptr(), p_len, n_pages,
+                             table[1], page_size, heads, head_dim, dt), index, B, p_offsets, heads, head_dim)
 
 
-def _rows(t, name, rows, heads, head_dim, like):
+def _rows(t, name, rows, heads, head_dim, dtype, index):
     """The row stride of a [rows, heads, head_dim] tensor whose heads lie next to each other."""
-    if t.dtype != like.dtype or t.device != like.device or t.dim() != 3 or (rows is not None and t.shape[0] != rows) \
-            or (heads is not None and t.shape[1] != heads) or t.shape[2] != head_dim or t.stride(2) != 1 \
-            or (t.shape[1] > 1 and t.stride(1) != head_dim):
-        raise ValueError(f"{name} must be a [rows, heads, head_dim] tensor of the cache's dtype and device, "
-                         "each row contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * head_dim
+    shape = t.shape
+    if t.dtype is dtype and t.get_device() == index and len(shape) == 3 and shape[0] == rows \
+            and (heads is None or shape[1] == heads) and shape[2] == head_dim:
+        row, head, step = t.stride()
+        if step == 1 and (head == head_dim or shape[1] == 1):
+            return row if rows > 1 else shape[1] * head_dim
+    raise ValueError(f"{name} must be a [n_draft_rows + B, heads, head_dim] tensor of the cache's dtype and device, "
+                     "each row contiguous")
 
 
 def kv_append(keys: torch.Tensor, values: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
@@ -541,33 +582,32 @@ def kv_append(keys: torch.Tensor, values: torch.Tensor, key_cache: torch.Tensor,
     (float32 [rotary / 2]; pairs half a rotation apart, or neighbours when interleaved).  page_table is
     int32 [B, max_pages], parents (int32 [n_draft_rows]) the tree of verify_tree.  Returns the queries
     rotated the same way (queries_out, or a new contiguous tensor), or None without queries."""
-    c, B, heads, head_dim = _cache(key_cache, value_cache, page_table, cache_len, offsets)
-    dev = key_cache.device
-    rows = keys.shape[0]
-    ks = _rows(keys, "keys", None, heads, head_dim, key_cache)
-    vs = _rows(values, "values", rows, heads, head_dim, key_cache)
+    c, index, B, p_offsets, heads, head_dim = _cache(key_cache, value_cache, page_table, cache_len, offsets)
+    dtype, rows = key_cache.dtype, keys.shape[0]
     if rows < B:
         raise ValueError("keys must have n_draft_rows + B rows")
-    _device_vector(parents, torch.int32, rows - B, dev, "parents")
-    rotary = 0
+    ks = _rows(keys, "keys", rows, heads, head_dim, dtype, index)
+    vs = _rows(values, "values", rows, heads, head_dim, dtype, index)
+    p_parents = None if parents is None else _vector(parents, torch.int32, rows - B, index, "parents")
+    rotary, p_freq = 0, None
     if inv_freq is not None:
-        rotary = 2 * _device_vector(inv_freq, torch.float32, inv_freq.numel(), dev, "inv_freq").shape[0]
-    n_q = qs = 0
+        rotary = 2 * inv_freq.numel()
+        p_freq = _vector(inv_freq, torch.float32, rotary // 2, index, "inv_freq")
+    n_q, qs, p_q, p_qo = 0, 0, None, None
     if queries is not None:
-        n_q = queries.shape[1] if queries.dim() == 3 else 0
-        qs = _rows(queries, "queries", rows, n_q, head_dim, key_cache)
+        qs = _rows(queries, "queries", rows, None, head_dim, dtype, index)
+        n_q, p_q = queries.shape[1], queries.data_ptr()
         if queries_out is None:
-            queries_out = torch.empty((rows, n_q, head_dim), dtype=queries.dtype, device=dev)
-        elif queries_out.dtype != queries.dtype or queries_out.device != dev or queries_out.shape != queries.shape \
+            queries_out = torch.empty((rows, n_q, head_dim), dtype=dtype, device=keys.device)
+        elif queries_out.dtype is not dtype or queries_out.get_device() != index or queries_out.shape != queries.shape \
                 or not queries_out.is_contiguous():
             raise ValueError("queries_out must be a contiguous tensor like queries")
+        p_qo = queries_out.data_ptr()
     elif queries_out is not None:
         raise ValueError("queries_out without queries")
-    ctx, stream = _launch_on(dev)
-    with ctx:
-        rc = _native.lib().sdv_kv_append(ctypes.byref(c), B, rows - B, offsets.data_ptr(), _ptr(parents),
-                                         keys.data_ptr(), ks, values.data_ptr(), vs, _ptr(inv_freq), rotary,
-                                         int(bool(interleaved)), _ptr(queries), qs, n_q, _ptr(queries_out), stream)
+    rc = _on(index, lambda stream: _native.lib().sdv_kv_append(
+        ctypes.byref(c), B, rows - B, p_offsets, p_parents, keys.data_ptr(), ks, values.data_ptr(), vs, p_freq, rotary,
+        1 if interleaved else 0, p_q, qs, n_q, p_qo, stream))
     if rc != 0:
         raise SdvError(rc, "sdv_kv_append")
     return queries_out
@@ -581,28 +621,32 @@ def attend(queries: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Te
     that kv_append wrote (arguments as there), each row over the slots before it (in a tree, the cached
     slots and its ancestors) within window positions (0: all) or among the first ``sinks`` slots.  scale
     defaults to head_dim ** -0.5.  Returns [n_draft_rows + B, n_q_heads, head_dim]."""
-    c, B, heads, head_dim = _cache(key_cache, value_cache, page_table, cache_len, offsets)
-    dev = key_cache.device
-    qs = _rows(queries, "queries", None, None, head_dim, key_cache)
-    rows, n_q = queries.shape[:2]
+    c, index, B, p_offsets, heads, head_dim = _cache(key_cache, value_cache, page_table, cache_len, offsets)
+    dtype, rows = key_cache.dtype, queries.shape[0]
+    qs = _rows(queries, "queries", rows, None, head_dim, dtype, index)
+    n_q = queries.shape[1]
     if rows < B:
         raise ValueError("queries must have n_draft_rows + B rows")
     if n_q < 1 or n_q % heads:
         raise ValueError("the number of query heads must be a multiple of the cache's heads")
-    _device_vector(parents, torch.int32, rows - B, dev, "parents")
+    p_parents = None if parents is None else _vector(parents, torch.int32, rows - B, index, "parents")
+    dev = key_cache.device
     if out is None:
-        out = torch.empty((rows, n_q, head_dim), dtype=queries.dtype, device=dev)
-    elif out.dtype != queries.dtype or out.device != dev or out.shape != queries.shape or not out.is_contiguous():
+        out = torch.empty((rows, n_q, head_dim), dtype=dtype, device=dev)
+    elif out.dtype is not dtype or out.get_device() != index or out.shape != queries.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor like queries")
     lib = _native.lib()
-    ctx, stream = _launch_on(dev)
-    with ctx:
+    p_c = ctypes.byref(c)
+    scale = head_dim ** -0.5 if scale is None else float(scale)
+
+    def call(stream):
         ws = workspace
         if ws is None:
-            ws = _scratch(lib.sdv_attend_workspace_bytes(ctypes.byref(c), B, rows - B, n_q, int(window), int(sinks)), dev)
-        rc = lib.sdv_attend(ctypes.byref(c), B, rows - B, offsets.data_ptr(), _ptr(parents), queries.data_ptr(), qs, n_q,
-                            head_dim ** -0.5 if scale is None else float(scale), int(window), int(sinks),
-                            out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), stream)
+            ws = _scratch(lib.sdv_attend_workspace_bytes(p_c, B, rows - B, n_q, window, sinks), dev, index, stream)
+        return lib.sdv_attend(p_c, B, rows - B, p_offsets, p_parents, queries.data_ptr(), qs, n_q, scale, window, sinks,
+                              out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), stream)
+
+    rc = _on(index, call)
     if rc != 0:
         raise SdvError(rc, "sdv_attend")
     return out
@@ -613,17 +657,14 @@ def kv_settle(key_cache: torch.Tensor, value_cache: torch.Tensor, page_table: to
     """sdv_kv_settle: moves the accepted path of verified token trees (accepted_len and accepted_nodes of
     verify_tree) to the slots where the sequences continue, in one layer's cache or in all of
     [n_layers, n_pages, n_kv_heads, page_size, head_dim].  Returns the new cache lengths, int32 [B]."""
-    c, B, _, _ = _cache(key_cache, value_cache, page_table, cache_len, offsets, layers=True)
-    dev = key_cache.device
+    c, index, B, p_offsets, _, _ = _cache(key_cache, value_cache, page_table, cache_len, offsets, layers=True)
     n_d = accepted_nodes.numel()
-    _device_vector(accepted_len, torch.int32, B, dev, "accepted_len")
-    _device_vector(accepted_nodes, torch.int32, n_d, dev, "accepted_nodes")
-    new_len = torch.empty(B, dtype=torch.int32, device=dev)
-    ctx, stream = _launch_on(dev)
-    with ctx:
-        rc = _native.lib().sdv_kv_settle(ctypes.byref(c), key_cache.shape[0] if key_cache.dim() == 5 else 1, B, n_d,
-                                         offsets.data_ptr(), accepted_len.data_ptr(), _ptr(accepted_nodes) if n_d else None,
-                                         new_len.data_ptr(), stream)
+    p_acc = _vector(accepted_len, torch.int32, B, index, "accepted_len")
+    p_nodes = _vector(accepted_nodes, torch.int32, n_d, index, "accepted_nodes")
+    new_len = torch.empty(B, dtype=torch.int32, device=key_cache.device)
+    layers = key_cache.shape[0] if key_cache.dim() == 5 else 1
+    rc = _on(index, lambda stream: _native.lib().sdv_kv_settle(
+        ctypes.byref(c), layers, B, n_d, p_offsets, p_acc, p_nodes if n_d else None, new_len.data_ptr(), stream))
     if rc != 0:
         raise SdvError(rc, "sdv_kv_settle")
     return new_len

@@ -20,8 +20,6 @@ namespace attend_impl {
 
 using namespace sdv;
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
 constexpr int kTile = 32;  // tokens a wave takes at a time
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -30,15 +28,17 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
 struct AttendArgs {
   CacheView cache;
-  int32_t B, n_q, G, splits, window, sinks;
+  int32_t B, n_q, G, window, sinks;
+  int32_t ranges;      // the ranges that the batch's work is cut into
+  int32_t part_tiles;  // > 0: a range is a part of one unit, of at most so many token tiles; 0: ranges of equal work
   int64_t n_d, query_stride, tiles;
   float scale2;  // scale * log2(e)
   const int32_t* cu;
   const int32_t* parents;
   const char* queries;
   char* out;
-  float* part;   // [unit][column][D] sums of a split, in the frame of its maxima
-  float* stats;  // [unit][column][2] maximum and sum of weights
+  float* part;   // [2 ranges][columns][D] sums of a piece of a unit, in the frame of its maxima
+  float* stats;  // [2 ranges][columns][2] maximum and sum of weights
 };
 
 // First tile number of request i: its columns take at most ceil((K + 1) G / columns) tiles from there.
@@ -64,6 +64,105 @@ __device__ __forceinline__ TileOf tile_of(const AttendArgs& a, int64_t tile) {
   return t;
 }
 
+// Workgroups go to the 8 XCDs in turn.  Each XCD takes a run of neighbouring units instead: the heads of one page
+// lie next to each other, so an XCD then reads whole pages (paged reads 5.0 -> 6.0 TB/s), and tiles
+// of one request share its L2.
+__device__ __forceinline__ int64_t unit_of_block(int64_t block, int64_t n) {
+  const int64_t x = block & 7, q = n >> 3, r = n & 7;
+  return x * q + (x < r ? x : r) + (block >> 3);
+}
+
+// The token tiles that rows j_lo .. j_hi of a request see: [0, near_end) and [lo, hi).
+struct Span {
+  int32_t lo, hi, near_end, t_lo, n_near, n;
+};
+__device__ __forceinline__ Span span_of(int32_t len, int32_t pos_lo, int32_t pos_hi, int32_t window, int32_t sinks) {
+  Span s;
+  s.hi = len + pos_hi + 1;
+  s.lo = window && len + pos_lo >= window ? len + pos_lo - window + 1 : 0;
+  s.near_end = s.lo < sinks ? s.lo : sinks;
+  s.t_lo = s.lo / kTile;
+  s.n_near = (s.near_end + kTile - 1) / kTile;
+  if (s.t_lo <= s.n_near) {  // the first tokens' tiles run into the window's
+    s.t_lo = 0;
+    s.n_near = 0;
+  }
+  s.n = s.n_near + (s.hi + kTile - 1) / kTile - s.t_lo;
+  return s;
+}
+
+// The batch's work is the list of its units (tile of columns, head), request by request, each of `parts` items.
+// Long work: an item is a token tile, and the list is cut into equal ranges, one per workgroup.  Lengths
+// differ between requests, and one workgroup per unit leaves the card half empty at the end (1136 units of 64
+// requests in 512 places: 3 rounds for 2.2).  Short work: an item is a part of part_tiles tiles, and a range is one
+// item, so that no workgroup sets up two units (8 to 25 us each) for a few tiles.
+struct Work {
+  int32_t first, k, len;      // the request
+  int32_t tiles, n, parts;    // column tiles; token tiles of a unit (those of all its rows), its items
+  __device__ int64_t units(const AttendArgs& a) const { return (int64_t)tiles * a.cache.n_heads; }
+};
+__device__ __forceinline__ Work work_of(const AttendArgs& a, int32_t i, int32_t columns) {
+  Work w;
+  w.tiles = w.n = w.parts = 0;
+  w.len = a.cache.len[i];
+  const Request r = request_at(a.cu, i, a.n_d);
+  w.first = r.first;
+  w.k = r.k;
+  if (r.index < 0) return w;
+  w.tiles = (int32_t)((((int64_t)r.k + 1) * a.G + columns - 1) / columns);
+  w.n = !len_fits(w.len, r.k) ? 1 : span_of(w.len, 0, r.k, a.window, a.sinks).n;
+  w.parts = a.part_tiles ? (w.n + a.part_tiles - 1) / a.part_tiles : w.n;
+  return w;
+}
+struct Stream {
+  int32_t per;                   // requests per lane
+  Work own;                      // of the lane's first
+  int64_t before, units_before;  // items, and units, before the lane's requests
+  int64_t total;                 // items of the batch
+  int64_t length;                // of a range
+};
+__device__ __forceinline__ Stream stream_of(const AttendArgs& a, int32_t columns) {
+  const int lane = threadIdx.x & (kWave - 1);
+  Stream s;
+  s.per = (a.B + kWave - 1) / kWave;
+  s.own.first = s.own.k = s.own.len = s.own.tiles = s.own.n = s.own.parts = 0;
+  uint64_t items = 0, units = 0;
+  for (int32_t k = 0; k < s.per; ++k) {
+    const int32_t i = lane * s.per + k;
+    if (i >= a.B) break;
+    const Work w = work_of(a, i, columns);
+    if (k == 0) s.own = w;
+    items += (uint64_t)(w.units(a) * w.parts);
+    units += (uint64_t)w.units(a);
+  }
+  const uint64_t inc = wave_inclusive_scan(items);
+  s.before = (int64_t)(inc - items);
+  s.units_before = (int64_t)(wave_inclusive_scan(units) - units);
+  s.total = (int64_t)lane_value(inc, kWave - 1);
+  s.length = a.part_tiles ? 1 : (s.total + a.ranges - 1) / a.ranges;
+  return s;
+}
+// The work of request i: from the lanes where they hold one request each.
+__device__ __forceinline__ Work work_at(const AttendArgs& a, const Stream& s, int32_t i, int32_t columns) {
+  if (s.per > 1) return work_of(a, i, columns);
+  Work w;
+  w.first = lane_value(s.own.first, i);
+  w.k = lane_value(s.own.k, i);
+  w.len = lane_value(s.own.len, i);
+  w.tiles = lane_value(s.own.tiles, i);
+  w.n = lane_value(s.own.n, i);
+  w.parts = lane_value(s.own.parts, i);
+  return w;
+}
+__device__ __forceinline__ Request request_with(const Work& w, int32_t i) {
+  Request r;
+  r.index = i;
+  r.first = w.first;
+  r.k = w.k;
+  r.row0 = (int64_t)w.first + i;
+  return r;
+}
+
 __device__ __forceinline__ float both_max16_32(float v) {
   float x, y;
   wave_detail::both<16>(v, x, y);
@@ -85,43 +184,55 @@ struct TreeSight {
   bool root;
 };
 
-template <class E, int D, int QB>
+template <class E, int D, int QB, int kWaves>
 struct Shape {
   static constexpr int kColumns = 16 * QB;
   static constexpr bool kBf16 = E::kBytes == 2;
   static constexpr int kValueStride = D * 2 + 32;  // bytes; rows 8 banks apart for the transposing reads
   static constexpr int kValueBytes = kBf16 ? kWaves * kTile * kValueStride : 0;
   static constexpr int kMergeStride = D + 4;
-  static constexpr int kMergeBytes = 2 * kColumns * kMergeStride * 4;
+  static constexpr int kMergeBytes = kWaves / 2 * kColumns * kMergeStride * 4;
   static constexpr int kBytes = kValueBytes > kMergeBytes ? kValueBytes : kMergeBytes;
 };
 
-template <class E, int D, int QB>
-__global__ __launch_bounds__(kThreads) void attend(AttendArgs a) {
-  using S = Shape<E, D, QB>;
+template <class E, int D, int QB, int kWaves>
+struct Scratch {
+  using S = Shape<E, D, QB, kWaves>;
+  __align__(16) char smem[S::kBytes];
+  float m_s[kWaves][S::kColumns], l_s[kWaves][S::kColumns];
+  int32_t parent_s[kWave], depth_s[kMaxNodes + 1];
+  uint64_t sight_s[kMaxNodes + 1];
+  int32_t root_s[kMaxNodes + 1];
+};
+
+// One unit (a tile of a request's columns, one key/value head), or of its token tiles [w_lo, w_hi) when
+// pos_all (then the tiles are those of all of the request's rows).  slot: where the sums go that another
+// workgroup's are joined with; -1: the unit is whole and its result is written.
+//
+// kWholePages: pages hold 16 slots or more, so 16 tokens lie in one page and its address is a scalar; smaller
+// pages take an address per token.
+template <class E, int D, int QB, int kWaves, bool kWholePages>
+__device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, QB, kWaves>& sh, const TileOf& at,
+                                            int32_t len, int32_t head, bool pos_all, int32_t w_lo, int32_t w_hi, int64_t slot) {
+  using S = Shape<E, D, QB, kWaves>;
   constexpr bool kBf16 = S::kBf16;
   constexpr int kSteps = kBf16 ? D / 32 : D / 16;  // 16-byte pieces of a key row per lane
   constexpr int kDB = D / 16;                       // blocks of 16 output values
-  __shared__ __align__(16) char smem[S::kBytes];
-  __shared__ float m_s[kWaves][S::kColumns], l_s[kWaves][S::kColumns];
-  __shared__ int32_t parent_s[kWave], depth_s[kMaxNodes + 1];
-  __shared__ uint64_t sight_s[kMaxNodes + 1];
-  __shared__ int32_t root_s[kMaxNodes + 1];
+  char* const smem = sh.smem;
+  auto& m_s = sh.m_s;
+  auto& l_s = sh.l_s;
+  auto& parent_s = sh.parent_s;
+  auto& depth_s = sh.depth_s;
+  auto& sight_s = sh.sight_s;
+  auto& root_s = sh.root_s;
 
   const int t = threadIdx.x, lane = t & (kWave - 1), col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
-  const int32_t head = (int32_t)(blockIdx.x % a.cache.n_heads);
-  const int64_t rest = blockIdx.x / a.cache.n_heads;
-  const int32_t split = (int32_t)(rest % a.splits);
-  const int64_t tile = rest / a.splits;
-  const TileOf at = tile_of<S::kColumns>(a, tile);
-  if (at.r.index < 0) return;
   const int32_t i = at.r.index, K = at.r.k;
-  const int64_t len = a.cache.len[i];
   const int64_t columns = ((int64_t)K + 1) * a.G;
   const int64_t c_last = at.c0 + S::kColumns < columns ? at.c0 + S::kColumns - 1 : columns - 1;
-  const int64_t j_lo = at.c0 / a.G, j_hi = c_last / a.G;  // rows of this tile
-  bool ok = len >= 0;
+  const int32_t j_lo = (int32_t)(at.c0 / a.G), j_hi = (int32_t)(c_last / a.G);  // rows of this tile
+  bool ok = len_fits(len, K);
   if (a.parents && ok) {
     ok = tree_depths(a.parents, at.r, parent_s, depth_s);
     if (ok) {
@@ -137,7 +248,7 @@ __global__ __launch_bounds__(kThreads) void attend(AttendArgs a) {
   }
 
   // this lane's columns: their rows, positions and queries
-  int64_t pos[QB];
+  int32_t pos[QB];
   int32_t jrow[QB];
   bool live[QB];
   TreeSight sight[QB];
@@ -161,21 +272,19 @@ __global__ __launch_bounds__(kThreads) void attend(AttendArgs a) {
     }
   }
 
-  // The slots that any row of the tile sees: [0, near_end) and [lo, hi).
-  const int64_t tail_lo = a.parents ? 0 : j_lo, tail_hi = a.parents ? K : j_hi;
-  const int64_t hi = len + tail_hi + 1;
-  const int64_t lo = a.window && len + tail_lo - a.window + 1 > 0 ? len + tail_lo - a.window + 1 : 0;
-  const int64_t near_end = lo < a.sinks ? lo : a.sinks;
-  int64_t t_lo = lo / kTile, n_near = (near_end + kTile - 1) / kTile;
-  if (t_lo <= n_near) {  // the first tokens' tiles run into the window's
-    t_lo = 0;
-    n_near = 0;
+  // the tiles are those of the rows, or of all the request's rows; what this tile's rows see of them is the same
+  const int32_t tail_lo = a.parents ? 0 : j_lo, tail_hi = a.parents ? K : j_hi;
+  const Span own = span_of(len, tail_lo, tail_hi, a.window, a.sinks);
+  const Span span = pos_all ? span_of(len, 0, K, a.window, a.sinks) : own;
+  const int32_t lo = own.lo, hi = own.hi, near_end = own.near_end, n_near = span.n_near, t_lo = span.t_lo;
+  if (!pos_all) {
+    w_lo = 0;
+    w_hi = span.n;
   }
-  const int64_t n_tiles = ok ? n_near + (hi + kTile - 1) / kTile - t_lo : 0;
-  const int64_t w_lo = n_tiles * split / a.splits, w_hi = n_tiles * (split + 1) / a.splits;
-  const int64_t far = len + tail_hi;  // the largest position
-  auto start = [&](int64_t n) { return (n < n_near ? n : n - n_near + t_lo) * kTile; };
-  auto held = [&](int64_t s) { return (s >= lo && s < hi) || s < near_end; };
+  if (!ok) w_hi = w_lo;
+  const int32_t far = len + tail_hi;  // the largest position
+  auto start = [&](int32_t n) { return (n < n_near ? n : n - n_near + t_lo) * kTile; };
+  auto held = [&](int32_t s) { return (s >= lo && s < hi) || s < near_end; };
 
   f32x4 acc[QB][kDB];
   float m[QB], l[QB];
@@ -190,51 +299,81 @@ __global__ __launch_bounds__(kThreads) void attend(AttendArgs a) {
   char* const v_lds = smem + wave * kTile * S::kValueStride;
   u32x4 kreg[2][kSteps];
   u32x4 vreg[kBf16 ? D / 16 : 1];
-  auto page_at = [&](int64_t n) -> int32_t {  // of token lane & 31
-    const int64_t s = start(n) + (lane & (kTile - 1));
-    return n < w_hi && held(s) ? a.cache.page(i, s) : -1;
+  float vf[kBf16 ? 1 : 8][kDB];
+  auto page_at = [&](int32_t n) -> int32_t {  // of token lane & 31
+    const int32_t s = start(n) + (lane & (kTile - 1));
+    return n < w_hi && (kWholePages || held(s)) ? a.cache.page(i, s) : -1;
   };
-  auto load = [&](int64_t n, int32_t page) {
-    const int64_t s0 = start(n);
+  constexpr int kLine = D * E::kBytes;
+  // the lane's byte offsets within 16 tokens' rows
+  const uint32_t k_off = col * kLine + 16 * g;
+  constexpr int kLanes = D / 8, kRows = kWave / kLanes;  // lanes of a bf16 value row, rows of one load
+  const uint32_t v_off = (lane / kLanes) * kLine + (lane % kLanes) * 16;
+  // Keys and values of a tile are asked for separately, each as soon as the registers of the tile before are free.
+  auto load_keys = [&](int32_t n, int32_t page) {
+    const int32_t s0 = start(n);
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
-      const int k = 16 * blk + col;
-      const int32_t p = __shfl(page, k);
-      const char* src = a.cache.keys + a.cache.row(p < 0 ? 0 : p, head, s0 + k) * (D * E::kBytes) + 16 * g;
+      const char* src;
+      if constexpr (kWholePages) {
+        const int32_t p = lane_value(page, 16 * blk);
+        src = a.cache.keys + a.cache.row(p < 0 ? 0 : p, head, s0 + 16 * blk) * kLine + k_off;
+      } else {
+        const int32_t p = __shfl(page, 16 * blk + col);
+        src = a.cache.keys + a.cache.row(p < 0 ? 0 : p, head, s0 + 16 * blk + col) * kLine + 16 * g;
+      }
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) kreg[blk][s] = *reinterpret_cast<const u32x4*>(src + 64 * s);
     }
+  };
+  auto load_values = [&](int32_t n, int32_t page) {
+    const int32_t s0 = start(n);
     if constexpr (kBf16) {
-      constexpr int kLanes = D / 8, kRows = kWave / kLanes;  // lanes of a value row, rows of one load
+      if constexpr (kWholePages) {
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        const int k = x * kRows + lane / kLanes;
+        for (int blk = 0; blk < 2; ++blk) {
+          const int32_t p = lane_value(page, 16 * blk);
+          const char* vs = a.cache.values + a.cache.row(p < 0 ? 0 : p, head, s0 + 16 * blk) * kLine + v_off;
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x)
+            vreg[blk * (D / 32) + x] = *reinterpret_cast<const u32x4*>(vs + x * kRows * kLine);
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const int k = x * kRows + lane / kLanes;
+          const int32_t p = __shfl(page, k);
+          vreg[x] = *reinterpret_cast<const u32x4*>(a.cache.values +
+                                                    a.cache.row(p < 0 ? 0 : p, head, s0 + k) * kLine +
+                                                    (lane % kLanes) * 16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int k = 16 * (e >> 2) + 4 * g + (e & 3);
         const int32_t p = __shfl(page, k);
-        const u32x4 v = *reinterpret_cast<const u32x4*>(
-            a.cache.values + a.cache.row(p < 0 ? 0 : p, head, s0 + k) * (D * 2) + (lane % kLanes) * 16);
-        vreg[x] = v;
+        const char* src = a.cache.values + a.cache.row(p < 0 ? 0 : p, head, s0 + k) * kLine + col * 4;
+#pragma unroll
+        for (int d = 0; d < kDB; ++d) vf[e][d] = *reinterpret_cast<const float*>(src + d * 64);
       }
     }
   };
 
-  int64_t n = w_lo + wave;
-  int32_t page = page_at(n);
-  if (n < w_hi) load(n, page);
+  int32_t n = w_lo + wave;
+  // the pages of two tiles ahead: a page read behind a tile's loads would wait for them
+  int32_t page = page_at(n), page_1 = page_at(n + kWaves);
+  if (n < w_hi) {
+    load_keys(n, page);
+    load_values(n, page);
+  }
   for (; n < w_hi; n += kWaves) {
-    const int64_t s0 = start(n);
-    const int32_t page_next = page_at(n + kWaves);
+    const int32_t s0 = start(n);
+    const int32_t page_2 = page_at(n + 2 * kWaves);
     // a value no row sees is 0: what lies there may be NaN
-    const bool paged = __all(page >= 0);
-    if constexpr (kBf16) {
-      constexpr int kLanes = D / 8, kRows = kWave / kLanes;
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        const int k = x * kRows + lane / kLanes;
-        u32x4 v = vreg[x];
-        if (!paged && __shfl(page, k) < 0) v.x = v.y = v.z = v.w = 0;
-        *reinterpret_cast<u32x4*>(v_lds + k * S::kValueStride + (lane % kLanes) * 16) = v;
-      }
-    }
+    const int32_t page_now = held(s0 + (lane & (kTile - 1))) ? page : -1;
+    const bool paged = __all(page_now >= 0);
+    const bool more = n + kWaves < w_hi;
     f32x4 sc[QB][2];
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
@@ -255,9 +394,17 @@ __global__ __launch_bounds__(kThreads) void attend(AttendArgs a) {
         }
       }
     }
-    const int32_t page_now = page;
-    page = page_next;
-    if (n + kWaves < w_hi) load(n + kWaves, page);
+    if (more) load_keys(n + kWaves, page_1);
+    if constexpr (kBf16) {
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) {
+        const int k = x * kRows + lane / kLanes;
+        u32x4 v = vreg[x];
+        if (!paged && __shfl(page_now, k) < 0) v.x = v.y = v.z = v.w = 0;
+        *reinterpret_cast<u32x4*>(v_lds + k * S::kValueStride + (lane % kLanes) * 16) = v;
+      }
+      if (more) load_values(n + kWaves, page_1);
+    }
 
     // every row sees every token of the tile: no masks
     const bool whole = paged && s0 + kTile <= (a.parents ? len : len + j_lo + 1) &&
@@ -273,10 +420,10 @@ __global__ __launch_bounds__(kThreads) void attend(AttendArgs a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int k = 16 * (e >> 2) + 4 * g + (e & 3);
-          const int64_t s = s0 + k;
+          const int32_t s = s0 + k;
           const bool there = __shfl(page_now, k) >= 0;  // by every lane: before the tests that part them
           const bool near = a.window == 0 || pos[b] - s < a.window || s < a.sinks;
-          const int64_t node = s - len;  // row index behind the cached slots
+          const int32_t node = s - len;  // row index behind the cached slots
           bool see;
           if (node < 0)
             see = near;
@@ -327,19 +474,19 @@ __global__ __launch_bounds__(kThreads) void attend(AttendArgs a) {
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int k = 16 * (e >> 2) + 4 * g + (e & 3);
-        const int32_t p = __shfl(page_now, k);
-        const char* src = a.cache.values + a.cache.row(p < 0 ? 0 : p, head, s0 + k) * (D * 4) + col * 4;
+        const bool there = paged || __shfl(page_now, 16 * (e >> 2) + 4 * g + (e & 3)) >= 0;
 #pragma unroll
         for (int d = 0; d < kDB; ++d) {
-          float v = *reinterpret_cast<const float*>(src + d * 64);
-          if (p < 0) v = 0.0f;
+          const float v = there ? vf[e][d] : 0.0f;
 #pragma unroll
           for (int b = 0; b < QB; ++b)
             acc[b][d] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, pf[b][e], acc[b][d], 0, 0, 0);
         }
       }
+      if (more) load_values(n + kWaves, page_1);
     }
+    page = page_1;
+    page_1 = page_2;
   }
 
   // the four waves' sums in one frame
@@ -389,22 +536,19 @@ __global__ __launch_bounds__(kThreads) void attend(AttendArgs a) {
     __syncthreads();
   }
   if (wave != 0) return;
-  const int64_t unit = (tile * a.cache.n_heads + head) * a.splits + split;
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
     const int64_t c = at.c0 + 16 * b + col;
     if (c >= columns) continue;
     const int64_t j = c / a.G;
-    if (a.splits > 1) {
-      const int64_t u = unit * S::kColumns + 16 * b + col;
+    if (slot >= 0) {
+      const int64_t u = slot * S::kColumns + 16 * b + col;
       if (g == 0) {
         a.stats[2 * u] = top[b];
         a.stats[2 * u + 1] = sum[b];
       }
-      if (sum[b] > 0.0f) {
 #pragma unroll
-        for (int d = 0; d < kDB; ++d) *reinterpret_cast<f32x4*>(a.part + u * D + 16 * d + 4 * g) = acc[b][d];
-      }
+      for (int d = 0; d < kDB; ++d) *reinterpret_cast<f32x4*>(a.part + u * D + 16 * d + 4 * g) = acc[b][d];
     } else {
       const int64_t h = (int64_t)head * a.G + (c - j * a.G);
       const float inv = sum[b] > 0.0f ? 1.0f / sum[b] : 0.0f;
@@ -424,48 +568,172 @@ __global__ __launch_bounds__(kThreads) void attend(AttendArgs a) {
   }
 }
 
-// Joins the splits of a tile's columns: D / 4 lanes per column.
+// Two waves per SIMD hide each other's loads; sums of 64 columns, or of 256 values, take the registers of both.
 template <class E, int D, int QB>
-__global__ __launch_bounds__(kThreads) void join(AttendArgs a) {
-  constexpr int kColumns = 16 * QB, kLanes = D / 4, kPer = kThreads / kLanes;
-  const int t = threadIdx.x;
-  const int32_t head = (int32_t)(blockIdx.x % a.cache.n_heads);
-  const int64_t tile = blockIdx.x / a.cache.n_heads;
-  const TileOf at = tile_of<kColumns>(a, tile);
+constexpr int kMinWaves = D * QB <= 256 ? 2 : 1;
+
+// A workgroup per unit.
+template <class E, int D, int QB, int kWaves, bool kWholePages>
+__global__ __launch_bounds__(kWaves* kWave, (kMinWaves<E, D, QB>)) void attend_units(AttendArgs a) {
+  __shared__ Scratch<E, D, QB, kWaves> sh;
+  const int64_t block = unit_of_block(blockIdx.x, gridDim.x);
+  const TileOf at = tile_of<16 * QB>(a, block / a.cache.n_heads);
   if (at.r.index < 0) return;
-  const int64_t columns = ((int64_t)at.r.k + 1) * a.G;
-  const int64_t unit = (tile * a.cache.n_heads + head) * a.splits;
-  for (int x = t / kLanes; x < kColumns; x += kPer) {
-    const int64_t c = at.c0 + x;
-    if (c >= columns) break;
-    float top = -__builtin_inff();
-    for (int s = 0; s < a.splits; ++s) top = fmaxf(top, a.stats[2 * ((unit + s) * kColumns + x)]);
-    f32x4 o = f32x4{0, 0, 0, 0};
-    float sum = 0.0f;
-    for (int s = 0; s < a.splits; ++s) {
-      const int64_t u = (unit + s) * kColumns + x;
-      const float w = a.stats[2 * u + 1];
-      if (!(w > 0.0f)) continue;
-      const float fade = fast_exp2(a.stats[2 * u] - top);
-      sum += w * fade;
-      o += *reinterpret_cast<const f32x4*>(a.part + u * D + (t % kLanes) * 4) * fade;
+  attend_unit<E, D, QB, kWaves, kWholePages>(a, sh, at, a.cache.len[at.r.index], (int32_t)(block % a.cache.n_heads),
+                                             false, 0, 0, -1);
+}
+
+// A workgroup per range of the batch's work.
+constexpr int kStreamWaves = 4;
+template <class E, int D, int QB>
+__global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void attend_ranges(AttendArgs a) {
+  constexpr int kColumns = 16 * QB;
+  __shared__ Scratch<E, D, QB, kStreamWaves> sh;
+  const Stream s = stream_of(a, kColumns);
+  const int64_t range = unit_of_block(blockIdx.x, gridDim.x);
+  const int64_t end = (range + 1) * s.length < s.total ? (range + 1) * s.length : s.total;
+  int64_t p = range * s.length;
+  if (p >= end) return;
+  // the request of p, then on from one to the next
+  const int who = 63 - __builtin_clzll(__ballot(s.before <= p));
+  int32_t i = who * s.per;
+  int64_t base = (int64_t)lane_value((uint64_t)s.before, who);
+  while (p < end && i < a.B) {
+    const Work w = work_at(a, s, i, kColumns);
+    const int64_t items = w.units(a) * w.parts;
+    if (p >= base + items) {
+      base += items;
+      ++i;
+      continue;
     }
+    const int64_t unit = (p - base) / w.parts;
+    const int32_t q_lo = (int32_t)(p - base - unit * w.parts);
+    const int32_t q_hi = q_lo + (end - p) < w.parts ? (int32_t)(q_lo + (end - p)) : w.parts;
+    TileOf at;
+    at.r = request_with(w, i);
+    at.c0 = unit / a.cache.n_heads * kColumns;
+    const bool first = q_lo == 0, whole = first && q_hi == w.parts;
+    attend_unit<E, D, QB, kStreamWaves, true>(a, sh, at, w.len, (int32_t)(unit % a.cache.n_heads), true,
+                                              (int32_t)((int64_t)w.n * q_lo / w.parts),
+                                              (int32_t)((int64_t)w.n * q_hi / w.parts),
+                                              whole ? -1 : 2 * range + (first ? 1 : 0));
+    p += q_hi - q_lo;
+    __syncthreads();
+  }
+}
+
+// Joins the pieces of the units that ranges cut.  A workgroup takes kJoin columns of a unit, or, where a
+// unit is cut into many pieces (few units, long caches), one column whose pieces its waves share.  Lane k of
+// D / 4 holds four values of a column; the wave's other lanes hold the same of further pieces.
+constexpr int kJoinWaves = 4;
+constexpr int kJoin = 8;
+
+template <class E, int D, int QB, bool kMany>
+__global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
+  constexpr int kColumns = 16 * QB, kLanes = D / 4, kRows = kWave / kLanes;  // pieces a wave reads at once
+  __shared__ float o_s[kJoinWaves][D], stat_s[kJoinWaves][2];
+  const int t = threadIdx.x, lane = t & (kWave - 1), k = lane % kLanes;
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const Stream s = stream_of(a, kColumns);
+  const int64_t u = blockIdx.x;
+  const int who = 63 - __builtin_clzll(__ballot(s.units_before <= u));
+  int64_t begin = (int64_t)lane_value((uint64_t)s.before, who);
+  int64_t unit = u - (int64_t)lane_value((uint64_t)s.units_before, who);
+  int32_t i = who * s.per;
+  Work w;
+  for (;; ++i) {
+    if (i >= a.B) return;
+    w = work_at(a, s, i, kColumns);
+    if (unit < w.units(a)) break;
+    unit -= w.units(a);
+    begin += w.units(a) * w.parts;
+  }
+  begin += unit * w.parts;
+  const int64_t r_lo = begin / s.length;
+  const int32_t pieces = (int32_t)((begin + w.parts - 1) / s.length - r_lo) + 1;
+  if (pieces == 1) return;
+  const Request r = request_with(w, i);
+  const int32_t head = (int32_t)(unit % a.cache.n_heads);
+  const int64_t c0 = unit / a.cache.n_heads * kColumns, columns = ((int64_t)r.k + 1) * a.G;
+  // the piece with the unit's first tile is its range's second, the others their ranges' first
+  auto at = [&](int32_t piece) { return (2 * (r_lo + piece) + (piece == 0 ? 1 : 0)) * kColumns; };
+  const int x_lo = blockIdx.y * (kMany ? 1 : kJoin), x_hi = x_lo + (kMany ? 1 : kJoin);
+  for (int x = x_lo + (kMany ? 0 : wave); x < x_hi; x += kMany ? 1 : kJoinWaves) {
+    const int64_t c = c0 + x;
+    if (c >= columns) break;
+    // this wave's pieces: all of them, or every kJoinWaves-th 64
+    float top = -__builtin_inff(), sum = 0.0f;
+    f32x4 o = f32x4{0, 0, 0, 0};
+    for (int32_t p0 = kMany ? wave * kWave : 0; p0 < pieces; p0 += kMany ? kJoinWaves * kWave : kWave) {
+      const int32_t p = p0 + lane;
+      float m = -__builtin_inff(), l = 0.0f;
+      if (p < pieces) {
+        m = a.stats[2 * (at(p) + x)];
+        l = a.stats[2 * (at(p) + x) + 1];
+      }
+      const float next = fmaxf(top, wave_max(m)), frame = next == -__builtin_inff() ? 0.0f : next;
+      const float fade = fast_exp2(top - frame), scale = fast_exp2(m - frame);
+      top = next;
+      sum = sum * fade + wave_sum(l * scale);
+      o *= fade;
+      const int32_t n = pieces - p0 < kWave ? pieces - p0 : kWave;
+#pragma unroll 4
+      for (int32_t q = 0; q < n; q += kRows) {
+        const int32_t mine = q + lane / kLanes;
+        const float f = __shfl(scale, mine & (kWave - 1));
+        if (mine < n) o += *reinterpret_cast<const f32x4*>(a.part + (at(p0 + mine) + x) * D + 4 * k) * f;
+      }
+    }
+    if constexpr (kRows > 1) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int step = kLanes; step < kWave; step *= 2) o[e] += __shfl_xor(o[e], step);
+      }
+    }
+    if constexpr (kMany) {
+      if (lane < kLanes) *reinterpret_cast<f32x4*>(&o_s[wave][4 * k]) = o;
+      if (lane == 0) {
+        stat_s[wave][0] = top;
+        stat_s[wave][1] = sum;
+      }
+      __syncthreads();
+      if (wave != 0) return;
+      top = -__builtin_inff();
+      for (int v = 0; v < kJoinWaves; ++v) top = fmaxf(top, stat_s[v][0]);
+      const float frame = top == -__builtin_inff() ? 0.0f : top;
+      sum = 0.0f;
+      o = f32x4{0, 0, 0, 0};
+      for (int v = 0; v < kJoinWaves; ++v) {
+        const float f = fast_exp2(stat_s[v][0] - frame);
+        sum += stat_s[v][1] * f;
+        o += *reinterpret_cast<const f32x4*>(&o_s[v][4 * k]) * f;
+      }
+    }
+    if (lane >= kLanes) continue;
     o *= sum > 0.0f ? 1.0f / sum : 0.0f;
     const int64_t j = c / a.G, h = (int64_t)head * a.G + (c - j * a.G);
-    char* dst = a.out + ((at.r.row0 + j) * a.n_q + h) * (D * E::kBytes) + (t % kLanes) * 4 * E::kBytes;
+    char* dst = a.out + ((r.row0 + j) * a.n_q + h) * (D * E::kBytes) + k * 4 * E::kBytes;
     if constexpr (E::kBytes == 2) {
-      bf16x4 w;
-      for (int e = 0; e < 4; ++e) w[e] = (__bf16)o[e];
-      *reinterpret_cast<bf16x4*>(dst) = w;
+      bf16x4 v;
+      for (int e = 0; e < 4; ++e) v[e] = (__bf16)o[e];
+      *reinterpret_cast<bf16x4*>(dst) = v;
     } else {
       *reinterpret_cast<f32x4*>(dst) = o;
     }
   }
 }
 
+enum Mode { kUnits, kRanges, kSmallPages };
+
+// Two workgroups per compute unit.
+constexpr int64_t kPlaces = 512;
+
 struct Plan {
   int qb;
-  int32_t splits;
+  Mode mode;
+  int32_t ranges, part_tiles;
+  int32_t pieces;  // of a unit, about
   int64_t tiles;
   size_t part_bytes, bytes;
 };
@@ -475,56 +743,79 @@ inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int32_t window, int32_t sinks) {
   const int64_t G = n_q / c->n_kv_heads, rows = n_d + B, mean = (rows * G + B - 1) / B;
   Plan p;
-  p.qb = mean <= 16 ? 1 : 2;
+  p.qb = mean <= 16 || (c->dtype == SDV_FP32 && c->head_dim > 64) ? 1 : 2;
   if (mean > 48 && c->dtype == SDV_BF16 && c->head_dim <= 128) p.qb = 4;
   const int64_t columns = 16 * p.qb;
   p.tiles = rows * G / columns + B;
-  // splits: enough workgroups to fill the card, each with two tiles per wave
-  const int64_t busy = (rows * G / columns > B ? rows * G / columns : B) * c->n_kv_heads;
+  const int64_t units = (rows * G / columns > B ? rows * G / columns : B) * c->n_kv_heads;
   int64_t seen = (int64_t)c->max_pages * c->page_size;
   if (window && (int64_t)window + sinks + rows / B < seen) seen = (int64_t)window + sinks + rows / B;
-  int64_t splits = (1024 + busy - 1) / busy;
-  const int64_t most = seen / (kWaves * kTile * 2);
-  if (splits > most) splits = most;
-  if (splits > 64) splits = 64;
-  p.splits = splits < 1 ? 1 : (int32_t)splits;
+  p.mode = kUnits;
+  p.ranges = p.part_tiles = p.pieces = 0;
   p.part_bytes = p.bytes = 0;
-  if (p.splits > 1) {
-    const int64_t units = p.tiles * c->n_kv_heads * p.splits * columns;
-    p.part_bytes = up256((size_t)units * c->head_dim * 4);
-    p.bytes = p.part_bytes + up256((size_t)units * 8);
+  if (c->page_size < 16) {
+    p.mode = kSmallPages;
+    if (p.qb > 2) p.qb = 2;
+    p.tiles = rows * G / (16 * p.qb) + B;
+  } else if (B <= 512 && rows <= 64 * (int64_t)B && units <= 4096 && seen > kStreamWaves * kTile) {
+    p.mode = kRanges;
+    const int64_t tokens = (seen + kTile - 1) / kTile;
+    if (units * tokens >= kPlaces * kStreamWaves * 8) {
+      p.ranges = kPlaces;
+      p.pieces = (int32_t)((kPlaces + units - 1) / units) + 1;
+    } else {  // a part per place, of a tile per wave at least
+      const int64_t part = (units * tokens + kPlaces - 1) / kPlaces;
+      p.part_tiles = part < kStreamWaves ? kStreamWaves : (int32_t)part;
+      p.pieces = (int32_t)((tokens + p.part_tiles) / p.part_tiles);
+      p.ranges = (int32_t)(p.tiles * c->n_kv_heads * p.pieces);
+    }
+    const size_t n = (size_t)2 * p.ranges * columns;
+    p.part_bytes = up256(n * c->head_dim * 4);
+    p.bytes = p.part_bytes + up256(n * 8);
   }
   return p;
 }
 
 template <class E, int D, int QB>
-int launch(const AttendArgs& a, hipStream_t s) {
-  const int64_t grid = a.tiles * a.cache.n_heads;
-  hipLaunchKernelGGL((attend<E, D, QB>), dim3((unsigned)(grid * a.splits)), dim3(kThreads), 0, s, a);
-  if (a.splits > 1) hipLaunchKernelGGL((join<E, D, QB>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+int launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
+  const Mode mode = p.mode;
+  const dim3 units((unsigned)(a.tiles * a.cache.n_heads));
+  if (mode == kSmallPages) {
+    if constexpr (QB <= 2) hipLaunchKernelGGL((attend_units<E, D, QB, 4, false>), units, dim3(4 * kWave), 0, s, a);
+    return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
+  }
+  if (mode == kRanges) {
+    hipLaunchKernelGGL((attend_ranges<E, D, QB>), dim3((unsigned)a.ranges), dim3(kStreamWaves * kWave), 0, s, a);
+    if (p.pieces > 16)
+      hipLaunchKernelGGL((join<E, D, QB, true>), dim3(units.x, 16 * QB), dim3(kJoinWaves * kWave), 0, s, a);
+    else
+      hipLaunchKernelGGL((join<E, D, QB, false>), dim3(units.x, 16 * QB / kJoin), dim3(kJoinWaves * kWave), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((attend_units<E, D, QB, 4, true>), units, dim3(4 * kWave), 0, s, a);
+  }
   return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
 }
 
 template <class E, int D>
-int launch_columns(const AttendArgs& a, int qb, hipStream_t s) {
-  if (qb == 1) return launch<E, D, 1>(a, s);
+int launch_columns(const AttendArgs& a, const Plan& p, hipStream_t s) {
+  if constexpr (E::kBytes == 4 && D > 64) return launch<E, D, 1>(a, p, s);
+  if (p.qb == 1) return launch<E, D, 1>(a, p, s);
   if constexpr (E::kBytes == 2 && D <= 128) {
-    if (qb == 4) return launch<E, D, 4>(a, s);
+    if (p.qb == 4) return launch<E, D, 4>(a, p, s);
   }
-  return launch<E, D, 2>(a, s);
+  return launch<E, D, 2>(a, p, s);
 }
 
 template <class E>
-int launch_dim(const AttendArgs& a, int32_t D, int qb, hipStream_t s) {
-  return D == 64 ? launch_columns<E, 64>(a, qb, s)
-                 : (D == 128 ? launch_columns<E, 128>(a, qb, s) : launch_columns<E, 256>(a, qb, s));
+int launch_dim(const AttendArgs& a, int32_t D, const Plan& p, hipStream_t s) {
+  return D == 64 ? launch_columns<E, 64>(a, p, s)
+                 : (D == 128 ? launch_columns<E, 128>(a, p, s) : launch_columns<E, 256>(a, p, s));
 }
 
 inline int check(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int32_t window, int32_t sinks) {
   if (n_q < 1 || n_q % c->n_kv_heads || window < 0 || sinks < 0) return SDV_ERR_INVALID_ARG;
   if (n_q > 1024) return SDV_ERR_LIMIT;
-  const Plan p = plan_of(c, B, n_d, n_q, window, sinks);
-  return p.tiles * c->n_kv_heads * p.splits > INT32_MAX ? SDV_ERR_LIMIT : SDV_OK;
+  return plan_of(c, B, n_d, n_q, window, sinks).tiles * c->n_kv_heads > INT32_MAX ? SDV_ERR_LIMIT : SDV_OK;
 }
 
 }  // namespace attend_impl
@@ -559,7 +850,8 @@ extern "C" int sdv_attend(const sdv_cache* cache, int32_t B, int64_t n_draft_row
   a.B = B;
   a.n_q = n_q_heads;
   a.G = n_q_heads / cache->n_kv_heads;
-  a.splits = p.splits;
+  a.ranges = p.ranges;
+  a.part_tiles = p.part_tiles;
   a.window = window;
   a.sinks = sinks;
   a.n_d = n_draft_rows;
@@ -573,6 +865,6 @@ extern "C" int sdv_attend(const sdv_cache* cache, int32_t B, int64_t n_draft_row
   a.part = static_cast<float*>(workspace);
   a.stats = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_bytes);
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  return cache->dtype == SDV_BF16 ? launch_dim<Bf16>(a, cache->head_dim, p.qb, s)
-                                  : launch_dim<F32>(a, cache->head_dim, p.qb, s);
+  return cache->dtype == SDV_BF16 ? launch_dim<Bf16>(a, cache->head_dim, p, s)
+                                  : launch_dim<F32>(a, cache->head_dim, p, s);
 }

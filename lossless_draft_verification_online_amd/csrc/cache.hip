@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kThreads) void append(AppendArgs a) {
   const int64_t j = row - r.row0;
   if (r.index < 0 || j > r.k) return;
   const int64_t len = a.cache.len[r.index];
-  if (len < 0) return;
+  if (!len_fits((int32_t)len, r.k)) return;
   int64_t depth = j;
   if (a.parents) {
     if (!tree_depths(a.parents, r, parent_s, depth_s)) return;
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(kThreads) void settle(SettleArgs a) {
   char* const base = ((rest & 1) ? a.cache.values : a.cache.keys) + (rest >> 1) * a.layer_bytes;
   const Request r = request_at(a.cu, i, a.n_d);
   const int32_t len = a.cache.len[i], acc = a.accepted_len[i];
-  bool ok = r.index >= 0 && len >= 0 && acc >= 0 && acc <= r.k && r.k <= kMaxNodes;
+  bool ok = r.index >= 0 && len_fits(len, r.k) && acc >= 0 && acc <= r.k && r.k <= kMaxNodes;
   if (t < kWave) {
     bool fine = true;
     int64_t from = -1, to = -1;

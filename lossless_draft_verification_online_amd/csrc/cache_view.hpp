@@ -52,6 +52,9 @@ __device__ __forceinline__ int32_t find_last(int32_t n, int64_t key, F f) {
   return (int32_t)lo;
 }
 
+// Whether the positions of a request of K + 1 rows behind len cached slots are 32-bit numbers, with room for a tile.
+__device__ __forceinline__ bool len_fits(int32_t len, int32_t k) { return len >= 0 && len < INT32_MAX - 1024 - k; }
+
 struct Request {
   int32_t index, first, k;  // its number, its first draft row cu[i], its K; index -1: offsets not valid
   int64_t row0;             // cu[i] + i
@@ -122,7 +125,7 @@ inline int check_cache(const sdv_cache* c, int32_t B, int64_t n_d, const int32_t
       (c->page_size & (c->page_size - 1)) || (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) ||
       !aligned16(c->keys) || !aligned16(c->values))
     return SDV_ERR_INVALID_ARG;
-  if (n_d + B > INT32_MAX || c->n_kv_heads > 1024 || c->n_pages > INT32_MAX) return SDV_ERR_LIMIT;
+  if (n_d + B > INT32_MAX - 1024 || c->n_kv_heads > 1024 || c->n_pages > INT32_MAX) return SDV_ERR_LIMIT;
   return SDV_OK;
 }
 
