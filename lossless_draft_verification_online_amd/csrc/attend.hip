@@ -724,7 +724,228 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
   }
 }
 
-enum Mode { kUnits, kRanges, kSmallPages };
+// Many rows per request (prompts), bf16, linear: products bound the call.  A workgroup takes 128 columns, a
+// wave 32 of them, and the waves share the keys and values of 64 tokens through shared memory, where direct loads
+// put the next 64 meanwhile.  Matrix instructions of 32 x 32 x 16; per tile and wave 32 of them (1024
+// cycles at D = 128) against 32 KiB of shared-memory reads, so two waves per SIMD keep both busy, one's
+// softmax under the other's products.
+//
+// A row of a tile keeps its 16-byte pieces in the order p ^ 2 (token mod 8) (for D = 64, of 8 pieces, p ^ 2 (token
+// / 2 mod 4)): the 32 rows that a key read takes, and the 8 that a transposing value read takes, then lie in
+// different banks.  A direct load writes its lanes' 16 bytes in lane order, so the permutation is in the addresses
+// that the lanes read from.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+constexpr int kRowsWaves = 4;
+constexpr int kRowsTile = 64;
+constexpr int kRowsColumns = 32 * kRowsWaves;
+
+template <int D>
+__device__ __forceinline__ int piece_of(int token, int p) {
+  return D == 128 ? p ^ (2 * (token & 7)) : p ^ (2 * ((token >> 1) & 3));
+}
+
+template <int D>
+__global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a) {
+  constexpr int kLine = D * 2, kPieces = D / 8, kSteps = D / 16, kDB = D / 32;
+  constexpr int kLoadRows = kWave / kPieces;       // rows of one direct load
+  constexpr int kLoads = 16 / kLoadRows;           // of a wave's 16 rows
+  // arrays of their own: reads of one tile do not wait for the loads into the other
+  __shared__ __align__(16) char k_0[kRowsTile * kLine], k_1[kRowsTile * kLine];
+  __shared__ __align__(16) char v_0[kRowsTile * kLine], v_1[kRowsTile * kLine];
+  const int t = threadIdx.x, lane = t & (kWave - 1), col = lane & 31, half = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  // head by head, the last tiles (of the longest rows) first
+  const int64_t unit = unit_of_block(blockIdx.x, gridDim.x);
+  const int32_t head = (int32_t)(unit / a.tiles);
+  const TileOf at = tile_of<kRowsColumns>(a, a.tiles - 1 - (unit - head * a.tiles));
+  if (at.r.index < 0) return;
+  const int32_t i = at.r.index, len = a.cache.len[i];
+  const bool ok = len_fits(len, at.r.k);
+  const int64_t columns = ((int64_t)at.r.k + 1) * a.G;
+  const int64_t c_end = at.c0 + kRowsColumns < columns ? at.c0 + kRowsColumns : columns;
+  const Span span = span_of(len, (int32_t)(at.c0 / a.G), (int32_t)((c_end - 1) / a.G), a.window, a.sinks);
+  // tiles of 64 tokens over [0, near_end) and [lo, hi)
+  int32_t t_lo = span.lo / kRowsTile, n_near = (span.near_end + kRowsTile - 1) / kRowsTile;
+  if (t_lo <= n_near) t_lo = n_near = 0;
+  const int32_t n_tiles = ok ? n_near + (span.hi + kRowsTile - 1) / kRowsTile - t_lo : 0;
+  auto start = [&](int32_t n) { return (n < n_near ? n : n - n_near + t_lo) * kRowsTile; };
+
+  // the wave's columns
+  const int64_t c = at.c0 + 32 * wave + col;
+  const bool live = c < columns;
+  const int32_t j = live ? (int32_t)(c / a.G) : (int32_t)((columns - 1) / a.G);
+  const int32_t h = head * a.G + (live ? (int32_t)(c - (int64_t)j * a.G) : 0);
+  const int32_t pos = len + j;
+  const bool wave_live = at.c0 + 32 * wave < columns;
+  const int32_t pos_lo = lane_value(pos, 0), pos_hi = lane_value(pos, 31);  // ascending over the columns
+  bf16x8 q[kSteps];
+  {
+    const char* src = a.queries + ((at.r.row0 + j) * a.query_stride + (int64_t)h * D) * 2 + 16 * half;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const bf16x8*>(src + 32 * s);
+  }
+
+  // Rows 16 wave .. of a tile are the wave's to load: one page.
+  typedef __attribute__((address_space(3))) void* Lds;
+  typedef const __attribute__((address_space(1))) void* Global;
+  uint32_t off[kLoads];
+#pragma unroll
+  for (int x = 0; x < kLoads; ++x) {
+    const int row = x * kLoadRows + lane / kPieces;
+    off[x] = row * kLine + piece_of<D>(row, lane % kPieces) * 16;
+  }
+  auto page_at = [&](int32_t n) { return n < n_tiles ? a.cache.page(i, start(n) + 16 * wave) : -1; };
+  auto load = [&](int32_t n, int32_t page, char* k_to, char* v_to) {
+    const int64_t at_row = a.cache.row(page < 0 ? 0 : page, head, start(n) + 16 * wave) * kLine;
+    k_to += 16 * wave * kLine;
+    v_to += 16 * wave * kLine;
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x)
+      __builtin_amdgcn_global_load_lds((Global)(a.cache.keys + at_row + off[x]), (Lds)(k_to + x * 1024), 16, 0, 0);
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x)
+      __builtin_amdgcn_global_load_lds((Global)(a.cache.values + at_row + off[x]), (Lds)(v_to + x * 1024), 16, 0, 0);
+  };
+
+  f32x16 acc[kDB];
+#pragma unroll
+  for (int d = 0; d < kDB; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[d][e] = 0.0f;
+  float m = -__builtin_inff(), l = 0.0f;
+  __shared__ int32_t page_s[2][kRowsWaves];
+
+  int32_t page = __builtin_amdgcn_readfirstlane(page_at(0)), page_1 = page_at(1);
+  auto tile = [&](int32_t n, int buffer, char* k_s, char* v_s, char* k_next, char* v_next) {
+    const int32_t s0 = start(n);
+    // a value no row sees is 0: what lies there may be NaN
+    const int32_t first = s0 + 16 * wave;
+    const bool held = page >= 0 && (first + 16 <= span.near_end || (first >= span.lo && first + 16 <= span.hi));
+    if (!held) {
+      __builtin_amdgcn_s_waitcnt(0);
+      const int row = lane >> 2;  // 4 lanes of a row
+      const int32_t s = first + row;
+      if (page < 0 || !(s < span.near_end || (s >= span.lo && s < span.hi))) {
+        u32x4 z;
+        z.x = z.y = z.z = z.w = 0;
+        char* const to = v_s + (16 * wave + row) * kLine;
+#pragma unroll
+        for (int x = 0; x < kPieces / 4; ++x) *reinterpret_cast<u32x4*>(to + ((lane & 3) + 4 * x) * 16) = z;
+      }
+    }
+    if (lane == 0) page_s[buffer][wave] = page;
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // this wave's direct loads
+    __syncthreads();  // the tile is there, and every wave is done with the other one
+    page = __builtin_amdgcn_readfirstlane(page_1);
+    if (n + 1 < n_tiles) load(n + 1, page, k_next, v_next);
+    page_1 = page_at(n + 2);
+    // tiles that no column of the wave sees
+    if (!wave_live || s0 > pos_hi || (a.window && s0 + kRowsTile <= pos_lo - a.window + 1 && s0 >= a.sinks)) return;
+    bool whole = s0 + kRowsTile <= pos_lo + 1 && (a.window == 0 || s0 > pos_hi - a.window || s0 + kRowsTile <= a.sinks);
+#pragma unroll
+    for (int w = 0; w < kRowsWaves; ++w) whole = whole && page_s[buffer][w] >= 0;
+
+    f32x16 sc[2];
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sc[blk][e] = 0.0f;
+      const int token = 32 * blk + col;
+      const char* const row = k_s + token * kLine;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const bf16x8 k = *reinterpret_cast<const bf16x8*>(row + piece_of<D>(token, 2 * s + half) * 16);
+        sc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[s], sc[blk], 0, 0, 0);
+      }
+    }
+    // element e of a block: token 8 (e / 4) + 4 half + e mod 4
+    if (!whole) {
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int k = 32 * blk + 8 * (e >> 2) + 4 * half + (e & 3);
+          const int32_t s = s0 + k;
+          const bool see = s <= pos && (a.window == 0 || pos - s < a.window || s < a.sinks) &&
+                           page_s[buffer][2 * blk + (e >> 3)] >= 0;
+          sc[blk][e] = see ? sc[blk][e] : -__builtin_inff();
+        }
+      }
+    }
+    float top = sc[0][0];
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[blk][e]);
+    {
+      float x, y;
+      wave_detail::both<32>(top, x, y);
+      top = fmaxf(x, y) * a.scale2;
+    }
+    const float m_new = fmaxf(m, top);
+    const float frame = m_new == -__builtin_inff() ? 0.0f : m_new;
+    const float fade = fast_exp2(m - frame);
+    m = m_new;
+    float sum = 0.0f;
+    bf16x8 p[4];
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float x = fast_exp2(fmaf(sc[blk][e], a.scale2, -frame));
+        sum += x;
+        p[2 * blk + (e >> 3)][e & 7] = (__bf16)x;
+      }
+    l = l * fade + sum;
+    if (!__all(fade == 1.0f)) {
+#pragma unroll
+      for (int d = 0; d < kDB; ++d) acc[d] *= fade;
+    }
+    // step s: tokens 16 s + 4 half + 0 .. 3 and 8 further; a 16-lane group reads 4 tokens x 16 values
+    const int g = (lane >> 4) & 1, in = lane & 15;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      const int token = 16 * s + 4 * half + (in >> 2);
+#pragma unroll
+      for (int d = 0; d < kDB; ++d) {
+        typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+        const int pc = 4 * d + 2 * g + ((in >> 1) & 1);
+        const char* const r0 = v_s + token * kLine + piece_of<D>(token, pc) * 16 + (in & 1) * 8;
+        const char* const r1 = v_s + (token + 8) * kLine + piece_of<D>(token + 8, pc) * 16 + (in & 1) * 8;
+        const bf16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)r0);
+        const bf16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)r1);
+        const bf16x8 v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[s], acc[d], 0, 0, 0);
+      }
+    }
+  };
+  if (n_tiles > 0) load(0, page, k_0, v_0);
+  for (int32_t n = 0; n < n_tiles; n += 2) {
+    tile(n, 0, k_0, v_0, k_1, v_1);
+    if (n + 1 < n_tiles) tile(n + 1, 1, k_1, v_1, k_0, v_0);
+  }
+  {
+    float x, y;
+    wave_detail::both<32>(l, x, y);
+    l = x + y;
+  }
+  if (!live) return;
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  char* const dst = a.out + ((at.r.row0 + j) * a.n_q + h) * kLine + 8 * half;
+#pragma unroll
+  for (int d = 0; d < kDB; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; e += 4) {
+      bf16x4 w;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) w[x] = (__bf16)(acc[d][e + x] * inv);
+      *reinterpret_cast<bf16x4*>(dst + d * 64 + e * 4) = w;
+    }
+}
+
+enum Mode { kUnits, kRanges, kSmallPages, kRows };
+
+constexpr int64_t kManyColumns = 96;
 
 // Two workgroups per compute unit.
 constexpr int64_t kPlaces = 512;
@@ -740,7 +961,8 @@ struct Plan {
 
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int32_t window, int32_t sinks) {
+inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int32_t window, int32_t sinks,
+                    bool tree) {
   const int64_t G = n_q / c->n_kv_heads, rows = n_d + B, mean = (rows * G + B - 1) / B;
   Plan p;
   p.qb = mean <= 16 || (c->dtype == SDV_FP32 && c->head_dim > 64) ? 1 : 2;
@@ -750,9 +972,16 @@ inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int
   const int64_t units = (rows * G / columns > B ? rows * G / columns : B) * c->n_kv_heads;
   int64_t seen = (int64_t)c->max_pages * c->page_size;
   if (window && (int64_t)window + sinks + rows / B < seen) seen = (int64_t)window + sinks + rows / B;
+  const bool many_rows =
+      !tree && c->dtype == SDV_BF16 && c->head_dim <= 128 && c->page_size >= 16 && mean >= kManyColumns;
   p.mode = kUnits;
+  if (many_rows) {
+    p.mode = kRows;
+    p.tiles = rows * G / kRowsColumns + B;
+  }
   p.ranges = p.part_tiles = p.pieces = 0;
   p.part_bytes = p.bytes = 0;
+  if (many_rows) return p;
   if (c->page_size < 16) {
     p.mode = kSmallPages;
     if (p.qb > 2) p.qb = 2;
@@ -780,6 +1009,11 @@ template <class E, int D, int QB>
 int launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
   const Mode mode = p.mode;
   const dim3 units((unsigned)(a.tiles * a.cache.n_heads));
+  if (mode == kRows) {
+    if constexpr (E::kBytes == 2 && D <= 128 && QB == 4)
+      hipLaunchKernelGGL((attend_rows<D>), units, dim3(kRowsWaves * kWave), 0, s, a);
+    return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
+  }
   if (mode == kSmallPages) {
     if constexpr (QB <= 2) hipLaunchKernelGGL((attend_units<E, D, QB, 4, false>), units, dim3(4 * kWave), 0, s, a);
     return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
@@ -815,7 +1049,7 @@ int launch_dim(const AttendArgs& a, int32_t D, const Plan& p, hipStream_t s) {
 inline int check(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int32_t window, int32_t sinks) {
   if (n_q < 1 || n_q % c->n_kv_heads || window < 0 || sinks < 0) return SDV_ERR_INVALID_ARG;
   if (n_q > 1024) return SDV_ERR_LIMIT;
-  return plan_of(c, B, n_d, n_q, window, sinks).tiles * c->n_kv_heads > INT32_MAX ? SDV_ERR_LIMIT : SDV_OK;
+  return plan_of(c, B, n_d, n_q, window, sinks, true).tiles * c->n_kv_heads > INT32_MAX ? SDV_ERR_LIMIT : SDV_OK;
 }
 
 }  // namespace attend_impl
@@ -826,7 +1060,7 @@ extern "C" size_t sdv_attend_workspace_bytes(const sdv_cache* cache, int32_t B, 
   if (!cache || B < 1 || n_draft_rows < 0 || cache->n_kv_heads < 1 || cache->max_pages < 1 || cache->page_size < 1 ||
       n_draft_rows + B > INT32_MAX || check(cache, B, n_draft_rows, n_q_heads, window, sinks) != SDV_OK)
     return 0;
-  return plan_of(cache, B, n_draft_rows, n_q_heads, window, sinks).bytes;
+  return plan_of(cache, B, n_draft_rows, n_q_heads, window, sinks, true).bytes;  // without a tree: that or less
 }
 
 extern "C" int sdv_attend(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, const int32_t* ragged_offsets,
@@ -843,7 +1077,7 @@ extern "C" int sdv_attend(const sdv_cache* cache, int32_t B, int64_t n_draft_row
       query_stride < (int64_t)n_q_heads * cache->head_dim || !(scale - scale == 0.0f))
     return SDV_ERR_INVALID_ARG;
   if (query_stride > ((int64_t)1 << 31)) return SDV_ERR_LIMIT;
-  const Plan p = plan_of(cache, B, n_draft_rows, n_q_heads, window, sinks);
+  const Plan p = plan_of(cache, B, n_draft_rows, n_q_heads, window, sinks, parents != nullptr);
   if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return SDV_ERR_WORKSPACE;
   AttendArgs a;
   a.cache = view_of(cache);
