@@ -573,7 +573,9 @@ int sdv_kv_append(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, const
  * product with the values (relative 2^-9 each).  The same call gives the same bits.
  * workspace: sdv_attend_workspace_bytes(...), 16-byte aligned, not initialised.
  * Errors as sdv_kv_append, plus n_q_heads not a multiple of n_kv_heads, window < 0, sinks < 0 or a
- * scale that is not finite -> SDV_ERR_INVALID_ARG; a small workspace -> SDV_ERR_WORKSPACE.
+ * scale that is not finite -> SDV_ERR_INVALID_ARG; more than INT32_MAX - 1024 rows times n_q_heads /
+ * n_kv_heads, or more than INT32_MAX units of work -> SDV_ERR_LIMIT; a small workspace ->
+ * SDV_ERR_WORKSPACE.
  */
 size_t sdv_attend_workspace_bytes(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, int32_t n_q_heads,
                                   int32_t window, int32_t sinks);

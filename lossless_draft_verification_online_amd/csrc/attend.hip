@@ -32,7 +32,8 @@ struct AttendArgs {
   int32_t ranges;      // the ranges that the batch's work is cut into
   int32_t part_tiles;  // > 0: a range is a part of one unit, of at most so many token tiles; 0: ranges of equal work
   int64_t n_d, query_stride, tiles;
-  float scale2;  // scale * log2(e)
+  float scale2;  // |scale| log2(e), at least 2^-126: a masked -inf stays one; the sign goes to the queries
+  uint32_t flip;  // sign bits of a word of queries, set for a negative scale
   const int32_t* cu;
   const int32_t* parents;
   const char* queries;
@@ -43,12 +44,12 @@ struct AttendArgs {
 
 // First tile number of request i: its columns take at most ceil((K + 1) G / columns) tiles from there.
 __device__ __forceinline__ int64_t first_tile(const int32_t* cu, int32_t i, int32_t G, int32_t columns) {
-  return ((int64_t)cu[i] + i) * G / columns + i;
+  return (uint32_t)(cu[i] + i) * (uint32_t)G / (uint32_t)columns + i;  // below 2^31, as n_draft_rows + B times G is
 }
 
 struct TileOf {
   Request r;
-  int64_t c0;  // its first column within the request
+  int32_t c0;  // its first column within the request
 };
 
 template <int kColumns>
@@ -59,8 +60,9 @@ __device__ __forceinline__ TileOf tile_of(const AttendArgs& a, int64_t tile) {
   t.r = request_at(a.cu, i, a.n_d);
   t.c0 = 0;
   if (t.r.index < 0) return t;
-  t.c0 = (tile - first_tile(a.cu, i, a.G, kColumns)) * kColumns;
-  if (t.c0 >= ((int64_t)t.r.k + 1) * a.G) t.r.index = -1;
+  const int64_t c0 = (tile - first_tile(a.cu, i, a.G, kColumns)) * kColumns;
+  if (c0 >= (int64_t)(t.r.k + 1) * a.G) t.r.index = -1;
+  t.c0 = (int32_t)c0;
   return t;
 }
 
@@ -109,7 +111,7 @@ __device__ __forceinline__ Work work_of(const AttendArgs& a, int32_t i, int32_t 
   w.first = r.first;
   w.k = r.k;
   if (r.index < 0) return w;
-  w.tiles = (int32_t)((((int64_t)r.k + 1) * a.G + columns - 1) / columns);
+  w.tiles = (int32_t)(((uint32_t)(r.k + 1) * a.G + columns - 1) / (uint32_t)columns);
   w.n = !len_fits(w.len, r.k) ? 1 : span_of(w.len, 0, r.k, a.window, a.sinks).n;
   w.parts = a.part_tiles ? (w.n + a.part_tiles - 1) / a.part_tiles : w.n;
   return w;
@@ -178,10 +180,10 @@ __device__ __forceinline__ float both_sum16_32(float v) {
   return x + y;
 }
 
-// Which rows of a tree a row sees: bit n of nodes for node n's slot, root for row 0's.
+// Which rows of a tree a row sees: bit t of rows for row t < 64, last for row 64.
 struct TreeSight {
-  uint64_t nodes;
-  bool root;
+  uint64_t rows;
+  bool last;
 };
 
 template <class E, int D, int QB, int kWaves>
@@ -202,7 +204,7 @@ struct Scratch {
   float m_s[kWaves][S::kColumns], l_s[kWaves][S::kColumns];
   int32_t parent_s[kWave], depth_s[kMaxNodes + 1];
   uint64_t sight_s[kMaxNodes + 1];
-  int32_t root_s[kMaxNodes + 1];
+  int32_t last_s[kMaxNodes + 1];
 };
 
 // One unit (a tile of a request's columns, one key/value head), or of its token tiles [w_lo, w_hi) when
@@ -224,24 +226,30 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   auto& parent_s = sh.parent_s;
   auto& depth_s = sh.depth_s;
   auto& sight_s = sh.sight_s;
-  auto& root_s = sh.root_s;
+  auto& last_s = sh.last_s;
 
   const int t = threadIdx.x, lane = t & (kWave - 1), col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int32_t i = at.r.index, K = at.r.k;
-  const int64_t columns = ((int64_t)K + 1) * a.G;
-  const int64_t c_last = at.c0 + S::kColumns < columns ? at.c0 + S::kColumns - 1 : columns - 1;
-  const int32_t j_lo = (int32_t)(at.c0 / a.G), j_hi = (int32_t)(c_last / a.G);  // rows of this tile
+  const int32_t columns = (K + 1) * a.G;
+  const int32_t c_last = at.c0 + S::kColumns < columns ? at.c0 + S::kColumns - 1 : columns - 1;
+  const int32_t j_lo = (uint32_t)at.c0 / (uint32_t)a.G, j_hi = (uint32_t)c_last / (uint32_t)a.G;  // rows of this tile
   bool ok = len_fits(len, K);
   if (a.parents && ok) {
     ok = tree_depths(a.parents, at.r, parent_s, depth_s);
     if (ok) {
       if (t <= K) {
-        uint64_t nodes = 0;
-        for (int32_t n = t - 1; n >= 0; n = parent_s[n])
-          if (a.window == 0 || depth_s[t] - depth_s[n + 1] < a.window || len + n + 1 < a.sinks) nodes |= 1ull << n;
-        sight_s[t] = nodes;
-        root_s[t] = a.window == 0 || depth_s[t] < a.window || len < a.sinks;
+        uint64_t rows = a.window == 0 || depth_s[t] < a.window || len < a.sinks;
+        bool last = false;
+        for (int32_t n = t - 1; n >= 0; n = parent_s[n]) {
+          if (!(a.window == 0 || depth_s[t] - depth_s[n + 1] < a.window || len + n + 1 < a.sinks)) continue;
+          if (n < 63)
+            rows |= 2ull << n;
+          else
+            last = true;
+        }
+        sight_s[t] = rows;
+        last_s[t] = last;
       }
       __syncthreads();
     }
@@ -255,19 +263,19 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   u32x4 q[QB][kSteps];
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
-    const int64_t c = at.c0 + 16 * b + col;
+    const int32_t c = at.c0 + 16 * b + col;
     live[b] = ok && c < columns;
-    jrow[b] = live[b] ? (int32_t)(c / a.G) : 0;
+    jrow[b] = live[b] ? (uint32_t)c / (uint32_t)a.G : 0;
     pos[b] = len + (a.parents && live[b] ? depth_s[jrow[b]] : jrow[b]);
-    sight[b].nodes = a.parents && live[b] ? sight_s[jrow[b]] : 0;
-    sight[b].root = a.parents && live[b] ? root_s[jrow[b]] != 0 : false;
-    const int64_t h = (int64_t)head * a.G + (c - (int64_t)jrow[b] * a.G);
+    sight[b].rows = a.parents && live[b] ? sight_s[jrow[b]] : 0;
+    sight[b].last = a.parents && live[b] ? last_s[jrow[b]] != 0 : false;
+    const int32_t h = head * a.G + (c - jrow[b] * a.G);
     const char* src = a.queries + ((at.r.row0 + jrow[b]) * a.query_stride + h * D) * E::kBytes + 16 * g;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       u32x4 z;
       z.x = z.y = z.z = z.w = 0;
-      if (live[b]) z = *reinterpret_cast<const u32x4*>(src + 64 * s);
+      if (live[b]) z = *reinterpret_cast<const u32x4*>(src + 64 * s) ^ a.flip;
       q[b][s] = z;
     }
   }
@@ -300,10 +308,14 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   u32x4 kreg[2][kSteps];
   u32x4 vreg[kBf16 ? D / 16 : 1];
   float vf[kBf16 ? 1 : 8][kDB];
-  auto page_at = [&](int32_t n) -> int32_t {  // of token lane & 31
-    const int32_t s = start(n) + (lane & (kTile - 1));
-    return n < w_hi && (kWholePages || held(s)) ? a.cache.page(i, s) : -1;
+  // The table's entry of token lane & 31 as it is, checked when it is used: a check would wait for it, and for
+  // the keys and values asked for before it.
+  const int32_t* const table = a.cache.table + (int64_t)i * a.cache.max_pages;
+  auto entry_at = [&](int32_t n) -> int32_t {
+    const int32_t s = start(n) + (lane & (kTile - 1)), k = s >> a.cache.page_log2;
+    return n < w_hi && (kWholePages || held(s)) && k < a.cache.max_pages ? table[k] : -1;
   };
+  auto page_of = [&](int32_t entry) { return entry >= 0 && entry < a.cache.n_pages ? entry : -1; };
   constexpr int kLine = D * E::kBytes;
   // the lane's byte offsets within 16 tokens' rows
   const uint32_t k_off = col * kLine + 16 * g;
@@ -362,17 +374,18 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
 
   int32_t n = w_lo + wave;
   // the pages of two tiles ahead: a page read behind a tile's loads would wait for them
-  int32_t page = page_at(n), page_1 = page_at(n + kWaves);
+  int32_t page = page_of(entry_at(n)), entry_1 = entry_at(n + kWaves);
   if (n < w_hi) {
     load_keys(n, page);
     load_values(n, page);
   }
   for (; n < w_hi; n += kWaves) {
     const int32_t s0 = start(n);
-    const int32_t page_2 = page_at(n + 2 * kWaves);
+    const int32_t page_1 = page_of(entry_1);
+    entry_1 = entry_at(n + 2 * kWaves);
     // a value no row sees is 0: what lies there may be NaN
-    const int32_t page_now = held(s0 + (lane & (kTile - 1))) ? page : -1;
-    const bool paged = __all(page_now >= 0);
+    const uint32_t there = (uint32_t)__ballot(page >= 0 && held(s0 + (lane & (kTile - 1))));  // bit k: token s0 + k
+    const bool paged = there == ~0u;
     const bool more = n + kWaves < w_hi;
     f32x4 sc[QB][2];
 #pragma unroll
@@ -396,13 +409,14 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
     }
     if (more) load_keys(n + kWaves, page_1);
     if constexpr (kBf16) {
+      if (!paged) {
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        const int k = x * kRows + lane / kLanes;
-        u32x4 v = vreg[x];
-        if (!paged && __shfl(page_now, k) < 0) v.x = v.y = v.z = v.w = 0;
-        *reinterpret_cast<u32x4*>(v_lds + k * S::kValueStride + (lane % kLanes) * 16) = v;
+        for (int x = 0; x < D / 16; ++x)
+          if (!((there >> (x * kRows + lane / kLanes)) & 1)) vreg[x].x = vreg[x].y = vreg[x].z = vreg[x].w = 0;
       }
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x)
+        *reinterpret_cast<u32x4*>(v_lds + (x * kRows + lane / kLanes) * S::kValueStride + (lane % kLanes) * 16) = vreg[x];
       if (more) load_values(n + kWaves, page_1);
     }
 
@@ -413,48 +427,50 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
     float pf[QB][8];
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = sc[b][e >> 2][e & 3] * a.scale2;
       if (!whole) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int k = 16 * (e >> 2) + 4 * g + (e & 3);
-          const int32_t s = s0 + k;
-          const bool there = __shfl(page_now, k) >= 0;  // by every lane: before the tests that part them
-          const bool near = a.window == 0 || pos[b] - s < a.window || s < a.sinks;
-          const int32_t node = s - len;  // row index behind the cached slots
-          bool see;
-          if (node < 0)
-            see = near;
-          else if (!a.parents)
-            see = near && node <= jrow[b];
-          else
-            see = node == 0 ? sight[b].root : (node <= K && ((sight[b].nodes >> ((node - 1) & 63)) & 1));
-          if (!see || !live[b] || !there) x[e] = -__builtin_inff();
+        // bit k: the column sees token s0 + k
+        auto below = [&](int32_t s) { return s - s0 >= kTile ? ~0u : (s > s0 ? (1u << (s - s0)) - 1 : 0u); };
+        uint32_t see = a.window ? ~below(pos[b] - a.window + 1) | below(a.sinks) : ~0u;
+        if (!a.parents) {
+          see &= below(pos[b] + 1);
+        } else {  // the cached slots, then the row's own path
+          const int32_t d = len - s0;  // the tile's token of row 0
+          see &= below(len);
+          if (d < kTile)
+            see |= d >= 0 ? (uint32_t)(sight[b].rows << d)
+                          : (d > -64 ? (uint32_t)(sight[b].rows >> -d) : 0u) |
+                                (sight[b].last && -d > 32 && -d <= 64 ? 1u << (64 + d) : 0u);
         }
+        see = live[b] ? (see & there) >> (4 * g) : 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (!((see >> (16 * (e >> 2) + (e & 3))) & 1)) sc[b][e >> 2][e & 3] = -__builtin_inff();
       }
-      float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-      top = both_max16_32(top);
-      const float m_new = fmaxf(m[b], top);
-      const float frame = m_new == -__builtin_inff() ? 0.0f : m_new;
-      const float fade = fast_exp2(m[b] - frame);
-      m[b] = m_new;
+      const f32x4 y = sc[b][0], z = sc[b][1];
+      float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
+      top = both_max16_32(top) * a.scale2;
+      // The frame follows the maximum only when a weight would pass 2^8: the sums have room for that, and they
+      // are not rescaled for each small step up.
+      if (__any(top > m[b] + 8.0f)) {
+        const float next = fmaxf(m[b], top);
+        const float keep = next == -__builtin_inff() ? 1.0f : fast_exp2(m[b] - next);
+        m[b] = next;
+        l[b] *= keep;
+#pragma unroll
+        for (int d = 0; d < kDB; ++d) acc[b][d] *= keep;
+      }
+      const float frame = m[b] == -__builtin_inff() ? 0.0f : m[b];
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float p = fast_exp2(x[e] - frame);
+        const float p = fast_exp2(fmaf(sc[b][e >> 2][e & 3], a.scale2, -frame));
         sum += p;
         if constexpr (kBf16)
           pb[b][e] = (__bf16)p;
         else
           pf[b][e] = p;
       }
-      l[b] = l[b] * fade + sum;
-      if (!__all(fade == 1.0f)) {
-#pragma unroll
-        for (int d = 0; d < kDB; ++d) acc[b][d] *= fade;
-      }
+      l[b] += sum;
     }
     if constexpr (kBf16) {
       __builtin_amdgcn_wave_barrier();
@@ -474,10 +490,10 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const bool there = paged || __shfl(page_now, 16 * (e >> 2) + 4 * g + (e & 3)) >= 0;
+        const bool held_e = (there >> (16 * (e >> 2) + 4 * g + (e & 3))) & 1;
 #pragma unroll
         for (int d = 0; d < kDB; ++d) {
-          const float v = there ? vf[e][d] : 0.0f;
+          const float v = held_e ? vf[e][d] : 0.0f;
 #pragma unroll
           for (int b = 0; b < QB; ++b)
             acc[b][d] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, pf[b][e], acc[b][d], 0, 0, 0);
@@ -486,7 +502,6 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
       if (more) load_values(n + kWaves, page_1);
     }
     page = page_1;
-    page_1 = page_2;
   }
 
   // the four waves' sums in one frame
@@ -538,9 +553,9 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   if (wave != 0) return;
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
-    const int64_t c = at.c0 + 16 * b + col;
+    const int32_t c = at.c0 + 16 * b + col;
     if (c >= columns) continue;
-    const int64_t j = c / a.G;
+    const int32_t j = (uint32_t)c / (uint32_t)a.G;
     if (slot >= 0) {
       const int64_t u = slot * S::kColumns + 16 * b + col;
       if (g == 0) {
@@ -550,7 +565,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
 #pragma unroll
       for (int d = 0; d < kDB; ++d) *reinterpret_cast<f32x4*>(a.part + u * D + 16 * d + 4 * g) = acc[b][d];
     } else {
-      const int64_t h = (int64_t)head * a.G + (c - j * a.G);
+      const int32_t h = head * a.G + (c - j * a.G);
       const float inv = sum[b] > 0.0f ? 1.0f / sum[b] : 0.0f;
       char* dst = a.out + ((at.r.row0 + j) * a.n_q + h) * (D * E::kBytes) + 4 * g * E::kBytes;
 #pragma unroll
@@ -606,14 +621,14 @@ __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void at
       ++i;
       continue;
     }
-    const int64_t unit = (p - base) / w.parts;
+    const uint32_t unit = (uint32_t)((p - base) / w.parts);
     const int32_t q_lo = (int32_t)(p - base - unit * w.parts);
     const int32_t q_hi = q_lo + (end - p) < w.parts ? (int32_t)(q_lo + (end - p)) : w.parts;
     TileOf at;
     at.r = request_with(w, i);
-    at.c0 = unit / a.cache.n_heads * kColumns;
+    at.c0 = (int32_t)(unit / (uint32_t)a.cache.n_heads) * kColumns;
     const bool first = q_lo == 0, whole = first && q_hi == w.parts;
-    attend_unit<E, D, QB, kStreamWaves, true>(a, sh, at, w.len, (int32_t)(unit % a.cache.n_heads), true,
+    attend_unit<E, D, QB, kStreamWaves, true>(a, sh, at, w.len, (int32_t)(unit % (uint32_t)a.cache.n_heads), true,
                                               (int32_t)((int64_t)w.n * q_lo / w.parts),
                                               (int32_t)((int64_t)w.n * q_hi / w.parts),
                                               whole ? -1 : 2 * range + (first ? 1 : 0));
@@ -653,13 +668,13 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
   const int32_t pieces = (int32_t)((begin + w.parts - 1) / s.length - r_lo) + 1;
   if (pieces == 1) return;
   const Request r = request_with(w, i);
-  const int32_t head = (int32_t)(unit % a.cache.n_heads);
-  const int64_t c0 = unit / a.cache.n_heads * kColumns, columns = ((int64_t)r.k + 1) * a.G;
+  const int32_t head = (uint32_t)unit % (uint32_t)a.cache.n_heads;
+  const int32_t c0 = (int32_t)((uint32_t)unit / (uint32_t)a.cache.n_heads) * kColumns, columns = (r.k + 1) * a.G;
   // the piece with the unit's first tile is its range's second, the others their ranges' first
   auto at = [&](int32_t piece) { return (2 * (r_lo + piece) + (piece == 0 ? 1 : 0)) * kColumns; };
   const int x_lo = blockIdx.y * (kMany ? 1 : kJoin), x_hi = x_lo + (kMany ? 1 : kJoin);
   for (int x = x_lo + (kMany ? 0 : wave); x < x_hi; x += kMany ? 1 : kJoinWaves) {
-    const int64_t c = c0 + x;
+    const int32_t c = c0 + x;
     if (c >= columns) break;
     // this wave's pieces: all of them, or every kJoinWaves-th 64
     float top = -__builtin_inff(), sum = 0.0f;
@@ -712,7 +727,7 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
     }
     if (lane >= kLanes) continue;
     o *= sum > 0.0f ? 1.0f / sum : 0.0f;
-    const int64_t j = c / a.G, h = (int64_t)head * a.G + (c - j * a.G);
+    const int32_t j = (uint32_t)c / (uint32_t)a.G, h = head * a.G + (c - j * a.G);
     char* dst = a.out + ((r.row0 + j) * a.n_q + h) * (D * E::kBytes) + k * 4 * E::kBytes;
     if constexpr (E::kBytes == 2) {
       bf16x4 v;
@@ -761,9 +776,9 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   if (at.r.index < 0) return;
   const int32_t i = at.r.index, len = a.cache.len[i];
   const bool ok = len_fits(len, at.r.k);
-  const int64_t columns = ((int64_t)at.r.k + 1) * a.G;
-  const int64_t c_end = at.c0 + kRowsColumns < columns ? at.c0 + kRowsColumns : columns;
-  const Span span = span_of(len, (int32_t)(at.c0 / a.G), (int32_t)((c_end - 1) / a.G), a.window, a.sinks);
+  const int32_t columns = (at.r.k + 1) * a.G;
+  const int32_t c_end = at.c0 + kRowsColumns < columns ? at.c0 + kRowsColumns : columns;
+  const Span span = span_of(len, (uint32_t)at.c0 / (uint32_t)a.G, (uint32_t)(c_end - 1) / (uint32_t)a.G, a.window, a.sinks);
   // tiles of 64 tokens over [0, near_end) and [lo, hi)
   int32_t t_lo = span.lo / kRowsTile, n_near = (span.near_end + kRowsTile - 1) / kRowsTile;
   if (t_lo <= n_near) t_lo = n_near = 0;
@@ -771,10 +786,10 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   auto start = [&](int32_t n) { return (n < n_near ? n : n - n_near + t_lo) * kRowsTile; };
 
   // the wave's columns
-  const int64_t c = at.c0 + 32 * wave + col;
+  const int32_t c = at.c0 + 32 * wave + col;
   const bool live = c < columns;
-  const int32_t j = live ? (int32_t)(c / a.G) : (int32_t)((columns - 1) / a.G);
-  const int32_t h = head * a.G + (live ? (int32_t)(c - (int64_t)j * a.G) : 0);
+  const int32_t j = (uint32_t)(live ? c : columns - 1) / (uint32_t)a.G;
+  const int32_t h = head * a.G + (live ? c - j * a.G : 0);
   const int32_t pos = len + j;
   const bool wave_live = at.c0 + 32 * wave < columns;
   const int32_t pos_lo = lane_value(pos, 0), pos_hi = lane_value(pos, 31);  // ascending over the columns
@@ -782,7 +797,8 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   {
     const char* src = a.queries + ((at.r.row0 + j) * a.query_stride + (int64_t)h * D) * 2 + 16 * half;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) q[s] = *reinterpret_cast<const bf16x8*>(src + 32 * s);
+    for (int s = 0; s < kSteps; ++s)
+      q[s] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(src + 32 * s) ^ a.flip);
   }
 
   // Rows 16 wave .. of a tile are the wave's to load: one page.
@@ -794,7 +810,16 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     const int row = x * kLoadRows + lane / kPieces;
     off[x] = row * kLine + piece_of<D>(row, lane % kPieces) * 16;
   }
-  auto page_at = [&](int32_t n) { return n < n_tiles ? a.cache.page(i, start(n) + 16 * wave) : -1; };
+  // The table's entry as it is, checked when it is used: a check would wait for it, and for the direct loads before it.
+  const int32_t* const table = a.cache.table + (int64_t)i * a.cache.max_pages;
+  auto entry_at = [&](int32_t n) {
+    const int32_t k = (start(n) + 16 * wave) >> a.cache.page_log2;
+    return n < n_tiles && k < a.cache.max_pages ? table[k] : -1;
+  };
+  auto page_of = [&](int32_t entry) {
+    const int32_t p = __builtin_amdgcn_readfirstlane(entry);
+    return p >= 0 && p < a.cache.n_pages ? p : -1;
+  };
   auto load = [&](int32_t n, int32_t page, char* k_to, char* v_to) {
     const int64_t at_row = a.cache.row(page < 0 ? 0 : page, head, start(n) + 16 * wave) * kLine;
     k_to += 16 * wave * kLine;
@@ -813,9 +838,9 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[d][e] = 0.0f;
   float m = -__builtin_inff(), l = 0.0f;
-  __shared__ int32_t page_s[2][kRowsWaves];
+  __shared__ __align__(16) int32_t page_s[2][kRowsWaves];
 
-  int32_t page = __builtin_amdgcn_readfirstlane(page_at(0)), page_1 = page_at(1);
+  int32_t page = page_of(entry_at(0)), entry_1 = entry_at(1);
   auto tile = [&](int32_t n, int buffer, char* k_s, char* v_s, char* k_next, char* v_next) {
     const int32_t s0 = start(n);
     // a value no row sees is 0: what lies there may be NaN
@@ -836,38 +861,64 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     if (lane == 0) page_s[buffer][wave] = page;
     __builtin_amdgcn_s_waitcnt(0x0f70);  // this wave's direct loads
     __syncthreads();  // the tile is there, and every wave is done with the other one
-    page = __builtin_amdgcn_readfirstlane(page_1);
+    const int4 pages = *reinterpret_cast<const int4*>(page_s[buffer]);
+    page = page_of(entry_1);
     if (n + 1 < n_tiles) load(n + 1, page, k_next, v_next);
-    page_1 = page_at(n + 2);
+    entry_1 = entry_at(n + 2);
     // tiles that no column of the wave sees
     if (!wave_live || s0 > pos_hi || (a.window && s0 + kRowsTile <= pos_lo - a.window + 1 && s0 >= a.sinks)) return;
     bool whole = s0 + kRowsTile <= pos_lo + 1 && (a.window == 0 || s0 > pos_hi - a.window || s0 + kRowsTile <= a.sinks);
-#pragma unroll
-    for (int w = 0; w < kRowsWaves; ++w) whole = whole && page_s[buffer][w] >= 0;
+    const int missing = pages.x | pages.y | pages.z | pages.w;  // negative: one of the four pages is none
+    whole = whole && missing >= 0;
 
+    // Products in the order written: the next operands are read under the products of the last ones.
     f32x16 sc[2];
+    bf16x8 kf[2][kSteps];
+    auto key = [&](int blk, int s) {
+      const int token = 32 * blk + col;
+      return *reinterpret_cast<const bf16x8*>(k_s + token * kLine + piece_of<D>(token, 2 * s + half) * 16);
+    };
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk) {
+    for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
       for (int e = 0; e < 16; ++e) sc[blk][e] = 0.0f;
-      const int token = 32 * blk + col;
-      const char* const row = k_s + token * kLine;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        const bf16x8 k = *reinterpret_cast<const bf16x8*>(row + piece_of<D>(token, 2 * s + half) * 16);
-        sc[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[s], sc[blk], 0, 0, 0);
-      }
+    for (int s = 0; s < kSteps; ++s) kf[0][s] = key(0, s);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      kf[1][s] = key(1, s);
+      sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[0][s], q[s], sc[0], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
+    // values of step s: tokens 16 s + 4 half + 0 .. 3 and 8 further; a 16-lane group reads 4 tokens x 16 values
+    bf16x4 vf[2][kDB][2];
+    auto value = [&](int s, bf16x4 (&v)[kDB][2]) {
+      typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+      const int g = (lane >> 4) & 1, in = lane & 15, token = 16 * s + 4 * half + (in >> 2);
+#pragma unroll
+      for (int d = 0; d < kDB; ++d) {
+        const int pc = 4 * d + 2 * g + ((in >> 1) & 1);
+        char* const r0 = v_s + token * kLine + piece_of<D>(token, pc) * 16 + (in & 1) * 8;
+        char* const r1 = v_s + (token + 8) * kLine + piece_of<D>(token + 8, pc) * 16 + (in & 1) * 8;
+        v[d][0] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)r0);
+        v[d][1] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)r1);
+      }
+    };
+    value(0, vf[0]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) sc[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[1][s], q[s], sc[1], 0, 0, 0);
     // element e of a block: token 8 (e / 4) + 4 half + e mod 4
     if (!whole) {
+      const int32_t none = (pages.x < 0 ? 1 : 0) | (pages.y < 0 ? 2 : 0) | (pages.z < 0 ? 4 : 0) | (pages.w < 0 ? 8 : 0);
+      const int32_t near = a.window ? pos - a.window : -1;  // slots above it, and the first `sinks`
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int k = 32 * blk + 8 * (e >> 2) + 4 * half + (e & 3);
-          const int32_t s = s0 + k;
-          const bool see = s <= pos && (a.window == 0 || pos - s < a.window || s < a.sinks) &&
-                           page_s[buffer][2 * blk + (e >> 3)] >= 0;
+          const int32_t s = s0 + 32 * blk + 8 * (e >> 2) + 4 * half + (e & 3);
+          const bool see = (s <= pos) & ((s > near) | (s < a.sinks)) & !((none >> (2 * blk + (e >> 3))) & 1);
           sc[blk][e] = see ? sc[blk][e] : -__builtin_inff();
         }
       }
@@ -882,10 +933,18 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
       wave_detail::both<32>(top, x, y);
       top = fmaxf(x, y) * a.scale2;
     }
-    const float m_new = fmaxf(m, top);
-    const float frame = m_new == -__builtin_inff() ? 0.0f : m_new;
-    const float fade = fast_exp2(m - frame);
-    m = m_new;
+    // The frame follows the maximum only when a weight would pass 2^8: the sums have room for that, and 64 of them
+    // are not rescaled for each small step up.
+    if (__any(top > m + 8.0f)) {
+      const float next = fmaxf(m, top);
+      const float fade = fast_exp2(m - next);  // 0 from -inf; a column that saw nothing yet keeps -inf
+      const float keep = next == -__builtin_inff() ? 1.0f : fade;
+      m = next;
+      l *= keep;
+#pragma unroll
+      for (int d = 0; d < kDB; ++d) acc[d] *= keep;
+    }
+    const float frame = m == -__builtin_inff() ? 0.0f : m;
     float sum = 0.0f;
     bf16x8 p[4];
 #pragma unroll
@@ -896,27 +955,16 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
         sum += x;
         p[2 * blk + (e >> 3)][e & 7] = (__bf16)x;
       }
-    l = l * fade + sum;
-    if (!__all(fade == 1.0f)) {
-#pragma unroll
-      for (int d = 0; d < kDB; ++d) acc[d] *= fade;
-    }
-    // step s: tokens 16 s + 4 half + 0 .. 3 and 8 further; a 16-lane group reads 4 tokens x 16 values
-    const int g = (lane >> 4) & 1, in = lane & 15;
+    l += sum;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int token = 16 * s + 4 * half + (in >> 2);
+      __builtin_amdgcn_sched_barrier(0);
+      if (s < 3) value(s + 1, vf[(s + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int d = 0; d < kDB; ++d) {
-        typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
-        const int pc = 4 * d + 2 * g + ((in >> 1) & 1);
-        const char* const r0 = v_s + token * kLine + piece_of<D>(token, pc) * 16 + (in & 1) * 8;
-        const char* const r1 = v_s + (token + 8) * kLine + piece_of<D>(token + 8, pc) * 16 + (in & 1) * 8;
-        const bf16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)r0);
-        const bf16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)r1);
-        const bf16x8 v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p[s], acc[d], 0, 0, 0);
-      }
+      for (int d = 0; d < kDB; ++d)
+        acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            __builtin_shufflevector(vf[s & 1][d][0], vf[s & 1][d][1], 0, 1, 2, 3, 4, 5, 6, 7), p[s], acc[d], 0, 0, 0);
     }
   };
   if (n_tiles > 0) load(0, page, k_0, v_0);
@@ -1048,7 +1096,7 @@ int launch_dim(const AttendArgs& a, int32_t D, const Plan& p, hipStream_t s) {
 
 inline int check(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int32_t window, int32_t sinks) {
   if (n_q < 1 || n_q % c->n_kv_heads || window < 0 || sinks < 0) return SDV_ERR_INVALID_ARG;
-  if (n_q > 1024) return SDV_ERR_LIMIT;
+  if (n_q > 1024 || (n_d + B) * (n_q / c->n_kv_heads) > INT32_MAX - 1024) return SDV_ERR_LIMIT;
   return plan_of(c, B, n_d, n_q, window, sinks, true).tiles * c->n_kv_heads > INT32_MAX ? SDV_ERR_LIMIT : SDV_OK;
 }
 
@@ -1091,7 +1139,8 @@ extern "C" int sdv_attend(const sdv_cache* cache, int32_t B, int64_t n_draft_row
   a.n_d = n_draft_rows;
   a.query_stride = query_stride;
   a.tiles = p.tiles;
-  a.scale2 = scale * 1.4426950408889634f;
+  a.scale2 = fmaxf(fabsf(scale) * 1.4426950408889634f, 0x1p-126f);
+  a.flip = scale < 0 ? (cache->dtype == SDV_BF16 ? 0x80008000u : 0x80000000u) : 0u;
   a.cu = ragged_offsets;
   a.parents = parents;
   a.queries = static_cast<const char*>(queries);

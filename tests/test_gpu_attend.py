@@ -69,6 +69,34 @@ def test_prompts(dtype):
     check(Batch([258, 130], [0, 77], 1, 256, 16, dtype, 3, Hq=2), dtype, 50, 0)
 
 
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 3), (64, 0), (100, 40), (90, 200), (5000, 3)])
+def test_prompts_under_windows(window, sinks):
+    check(Batch([127, 300, 64], [33, 500, 0], 1, 128, 16, "bf16", window, Hq=8), "bf16", window, sinks)
+    b = Batch([127, 300, 64], [33, 500, 0], 2, 64, 64, "bf16", window, Hq=6)
+    b.table[1, 2:4] = [-1, b.n_pages]  # pages that are missing
+    check(b, "bf16", window, sinks)
+
+
+def test_what_no_row_of_a_prompt_sees_may_hold_anything():
+    b = Batch([200, 100], [300, 9], 2, 128, 16, "bf16", 20, Hq=4)
+    window, sinks = 64, 3
+    want = check(b, "bf16", window, sinks)
+    seen = np.zeros((b.n_pages, 16), dtype=bool)
+    for i, _, K, L, _, _ in oracle.requests(b.cu, b.len, b.n_d):
+        for s in range(L + K + 1):
+            if s < sinks or s > L - window:
+                seen[oracle.place(b.table[i], b.n_pages, 16, s)] = True
+    for c in (b.kc, b.vc):
+        c[torch.from_numpy(~seen)[:, None, :, None].expand(c.shape)] = float("nan")
+    table, length, cu = b.index_args()
+    out = sdv.attend(b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), table, length, cu, window=window, sinks=sinks)
+    assert torch.equal(out, want)
+    b.len[0] = -1
+    length = torch.from_numpy(b.len).to(DEV)
+    out = sdv.attend(b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), table, length, cu, window=window, sinks=sinks)
+    assert not out[:201].any() and torch.equal(out[201:], want[201:])
+
+
 def test_long_caches_are_split():
     check(Batch([0], [9000], 1, 128, 16, "bf16", 4, Hq=8), "bf16")
     check(Batch([4, 0], [5000, 20], 1, 64, 16, "fp32", 5, Hq=4), "fp32", 4096, 4)
@@ -85,8 +113,10 @@ def test_strided_queries_and_scales():
     wide = torch.randn((b.rows, 9, 64)).to(torch.bfloat16)
     wide[:, :4] = b.q
     check(b, "bf16", q=wide.to(DEV)[:, :4])
+    prompt = Batch([130, 70], [50, 20], 2, 64, 16, "bf16", 9, Hq=4)
     for scale in (0.0, 1.0, -0.5):
         check(b, "bf16", scale=scale)
+        check(prompt, "bf16", 60, 3, scale=scale)
     b = Batch([3, 1], [500, 20], 2, 64, 16, "fp32", 10, Hq=4)
     b.q *= 30  # far apart scores: most weights vanish
     check(b, "fp32", scale=1.0)
