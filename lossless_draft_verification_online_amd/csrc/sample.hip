@@ -386,17 +386,24 @@ __device__ __forceinline__ int32_t block_last(int32_t id, int32_t* wave_ids) {
   return last;
 }
 
-// A row's elements for the passes of a cut.  Each pass is a loop over single vectors, small enough
+// A row's vectors for the passes over it.  Each pass is a loop over single vectors, small enough
 // to stay in the instruction cache: unrolled over a thread's whole share (32 logits) the passes of a row are
 // 160 KiB of code that each workgroup fetches to run once, and that fetch set their time (56 us against 20 us for
-// one row of 32000 under top-k).
+// one row of 32000 under top-k).  A row is C chunks of vecs neighbouring vectors, a chunk at most one vector per
+// thread; what a vector holds beside the row is -inf.
+//
 // In memory, a wave's vectors interleaved by lane and kAhead of them loaded ahead ...
 constexpr int kAhead = 4;
 
-template <class E, int kThreads>
+template <class E, int kThreads, int kVpl>
 struct MemorySource {
+  static constexpr int P = E::kPerVec, vecs = kVpl * kWave;
   const RowView<E>& view;
-  // f(id of the vector's first value, vector, whole: every value is the row's)
+  int32_t C;
+  __device__ int32_t lead() const { return view.lead; }
+  __device__ int32_t values() const { return view.end - view.lead; }
+  __device__ __forceinline__ u32x4 one(int32_t j) const { return view.one(j); }
+  // f(index of this lane's vector, vector)
   template <class F>
   __device__ __forceinline__ void vectors(int32_t j0, int32_t j1, int32_t step, F f) const {
     const int lane = threadIdx.x & (kWave - 1);
@@ -416,43 +423,67 @@ struct MemorySource {
 #pragma unroll
       for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
       load(j + kAhead * step, ahead[kAhead - 1]);
-      f((j + lane) * E::kPerVec - view.lead, v, view.inside(j, kWave));
+      f(j + lane, v);
     }
   }
+  // Every vector once, by the whole workgroup.
   template <class F>
-  __device__ __forceinline__ void each(F f) const {
+  __device__ __forceinline__ void all(F f) const {
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x / kWave));
-    vectors(wave * kWave, (view.end + E::kPerVec - 1) / E::kPerVec, kThreads, [&](int32_t id, u32x4 v, bool whole) {
-      float z[E::kPerVec];
-      E::unpack(v, z);
-#pragma unroll
-      for (int e = 0; e < E::kPerVec; ++e)
-        if (whole || (uint32_t)(id + e) < (uint32_t)(view.end - view.lead)) f(z[e]);
-    });
+    vectors(wave * kWave, (view.end + P - 1) / P, kThreads, f);
+  }
+  // The vectors of a chunk, by one wave (lanes past the row's end get -inf).
+  template <class F>
+  __device__ __forceinline__ void chunk(int32_t c, F f) const {
+    vectors(c * vecs, (c + 1) * vecs, kWave, f);
   }
 };
 
-// ... or in shared memory.
+// ... or in shared memory, a chunk per wave.
 template <class E, int kThreads>
 struct SharedSource {
+  static constexpr int P = E::kPerVec;
+  static constexpr int32_t C = kThreads / kWave;
   const u32x4* v;
-  int32_t n, lead, V;  // vectors; values beside the row's in the first; the row's
-  template <class F>
-  __device__ __forceinline__ void vectors(F f) const {
-#pragma unroll 1
-    for (int32_t j = threadIdx.x; j < n; j += kThreads) f(j, j * E::kPerVec - lead, v[j]);
+  int32_t n, vecs;  // vectors of the row, of a chunk
+  int32_t lead_, V;
+  __device__ int32_t lead() const { return lead_; }
+  __device__ int32_t values() const { return V; }
+  __device__ __forceinline__ u32x4 one(int32_t j) const {
+    u32x4 x = RowView<E>::nothing();
+    if (j < n) x = v[j];
+    return x;
   }
   template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    vectors([&](int32_t, int32_t id, u32x4 x) {
-      float z[E::kPerVec];
-      E::unpack(x, z);
-#pragma unroll
-      for (int e = 0; e < E::kPerVec; ++e)
-        if ((uint32_t)(id + e) < (uint32_t)V) f(z[e]);
-    });
+  __device__ __forceinline__ void all(F f) const {
+#pragma unroll 1
+    for (int32_t j = threadIdx.x; j < n; j += kThreads) f(j, v[j]);
+  }
+  template <class F>
+  __device__ __forceinline__ void chunk(int32_t c, F f) const {
+    const int lane = threadIdx.x & (kWave - 1);
+    const int32_t end = (c + 1) * vecs;
+#pragma unroll 1
+    for (int32_t j = c * vecs; j < end; j += kWave) {
+      u32x4 x = RowView<E>::nothing();
+      if (j + lane < end && j + lane < n) x = v[j + lane];
+      f(j + lane, x);
+    }
   }
 };
+
+// Every logit of the row once: f(z).
+template <class E, class Source, class F>
+__device__ __forceinline__ void each(const Source& source, F f) {
+  const int32_t V = source.values(), lead = source.lead();
+  source.all([&](int32_t j, u32x4 v) {
+    float z[E::kPerVec];
+    E::unpack(v, z);
+#pragma unroll
+    for (int e = 0; e < E::kPerVec; ++e)
+      if ((uint32_t)(j * E::kPerVec + e - lead) < (uint32_t)V) f(z[e]);
+  });
+}
 
 struct Selected {
   uint32_t key;
@@ -478,7 +509,7 @@ __device__ Selected radix_select(const Source& source, Shared<kThreads>& sh, Val
     __syncthreads();
     for (int b = t; b < kBins; b += kThreads) sh.hist[b] = 0;
     __syncthreads();
-    source.each([&](float z) {
+    each<E>(source, [&](float z) {
       const uint32_t key = order_key(z);
       if (level > 0 && ((key ^ r.key) >> (shift + width)) != 0) return;
       const uint64_t x = value(z);
@@ -525,7 +556,7 @@ struct Cut {
 // other logit's weight is computed.  False if a cut lies below the window.  S: the whole row's mass
 // in the frame (used without top-k).
 template <class E, int kThreads, class Source>
-__device__ bool window_cut(const Source& source, Shared<kThreads>& sh, const Profile& f, const Frame& frame,
+__device__ __forceinline__ bool window_cut(const Source& source, Shared<kThreads>& sh, const Profile& f, const Frame& frame,
                            uint32_t top, double S, Cut& cut) {
   constexpr int kPer = kWindow / kThreads, kWaves = kThreads / kWave;
   const int t = threadIdx.x;
@@ -535,10 +566,24 @@ __device__ bool window_cut(const Source& source, Shared<kThreads>& sh, const Pro
   if (t == 0) sh.found_bin = kWindow;
   __syncthreads();
   const uint32_t top16 = top >> 16;
-  source.each([&](float z) {
-    const uint32_t d = top16 - (order_key(z) >> 16);
-    if (d < kWindow) atomicAdd(&count[d], 1u);
-  });
+  if (top16 >= 0x8000u + kWindow) {
+    // a maximum above the window's width over 0: the window holds positive logits alone, whose bits are their
+    // order; zeros, negative ones, NaN and what lies beside the row wrap to a large distance
+    const uint32_t max16 = top16 & 0x7fffu;
+    source.all([&](int32_t, u32x4 v) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t lo = max16 - (v[w] & 0xffffu), hi = max16 - (v[w] >> 16);
+        if (lo < kWindow) atomicAdd(&count[lo], 1u);
+        if (hi < kWindow) atomicAdd(&count[hi], 1u);
+      }
+    });
+  } else {
+    each<E>(source, [&](float z) {
+      const uint32_t d = top16 - (order_key(z) >> 16);
+      if (d < kWindow) atomicAdd(&count[d], 1u);
+    });
+  }
   __syncthreads();
   uint64_t c[kPer], own = 0;
 #pragma unroll
@@ -617,7 +662,7 @@ __device__ bool window_cut(const Source& source, Shared<kThreads>& sh, const Pro
 
 // The cut of a row's profile.  S: the whole row's mass in the frame (of a row with top-p, without top-k).
 template <class E, int kThreads, class Source>
-__device__ Cut cut_of(const Source& source, Shared<kThreads>& sh, const Args& a, const Profile& f, const Frame& frame,
+__device__ __forceinline__ Cut cut_of(const Source& source, Shared<kThreads>& sh, const Args& a, const Profile& f, const Frame& frame,
                       float m, double S) {
   Cut cut;
   cut.key = 0;
@@ -734,15 +779,180 @@ __device__ __forceinline__ void write_probs(float* out, const float (&p)[P]) {
   }
 }
 
-template <class E, int kVpl, bool kCut>
-__global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
-  constexpr int kWaves = kDrawThreads / kWave;
-  constexpr int kVecs = kVpl * kWave;  // vectors of a chunk
-  constexpr int P = E::kPerVec;
-  static_assert(kVecs <= kDrawThreads, "one vector of a chunk per thread");
-  __shared__ Shared<kDrawThreads> sh;
+// Each chunk's kept mass of a cut row, into rec[c].s; the tokens kept, and the id of the cut key's last kept copy
+// where some of its copies are not (kNone otherwise).  The logits above the cut are gathered in shared memory
+// first, 64 to a weight: computing weights in place would cost every lane the exponential for the few that are kept.
+template <class E, int kThreads, class Source>
+__device__ __forceinline__ int64_t cut_masses(const Source& source, Shared<kThreads>& sh, const Frame& frame,
+                                              const Cut& cut, Record* rec, int32_t& eq_last) {
+  constexpr int P = E::kPerVec, kWaves = kThreads / kWave, kPart = 4, kList = (1 + kPart) * kWave;
+  static_assert(kWaves * kList * sizeof(float) <= sizeof(sh.hist), "the lists take the histogram's place");
   const int t = threadIdx.x, lane = t & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  float* const list = reinterpret_cast<float*>(sh.hist) + wave * kList;
+  const float z_cut = row_key_logit<E>(cut.key);
+  const int32_t C = source.C, lead = source.lead(), end = lead + source.values();
+  uint32_t above = 0;
+  __syncthreads();
+  for (int32_t c = wave; c < C; c += kWaves) {
+    double s = 0.0;
+    uint32_t eq = 0, held = 0;
+    source.chunk(c, [&](int32_t, u32x4 v) {
+      float z[P];
+      E::unpack(v, z);
+#pragma unroll
+      for (int e0 = 0; e0 < P; e0 += kPart) {
+#pragma unroll
+        for (int e = e0; e < e0 + kPart; ++e) {
+          const bool more = z[e] > z_cut;
+          const uint64_t over = __ballot(more);
+          if (more)
+            list[held + __builtin_amdgcn_mbcnt_hi((uint32_t)(over >> 32),
+                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)over, 0))] = z[e];
+          held += __builtin_popcountll(over);
+          eq += fmaxf(z[e], -__builtin_inff()) == z_cut;  // NaN counts as -inf
+        }
+        while (held >= kWave) {
+          held -= kWave;
+          s += frame.weight(list[held + lane]);
+          above += kWave;
+        }
+      }
+    });
+    if (lane < held) s += frame.weight(list[lane]);
+    above += held;
+    s = wave_sum(s);
+    eq = wave_sum_u32(eq);
+    if (z_cut == -__builtin_inff()) {  // what the chunk's loop saw beside the row came as -inf
+      const int32_t rounds = (source.vecs + kWave - 1) / kWave;
+      const int32_t lo = c * source.vecs * P, hi = lo + source.vecs * P;
+      const int32_t own = (end < hi ? end : hi) - (lead > lo ? lead : lo);
+      eq -= rounds * kWave * P - (own > 0 ? own : 0);
+    }
+    if (lane == 0) {
+      rec[c].s = s;
+      rec[c].far = eq;
+    }
+  }
+  uint64_t n_above;
+  (void)block_scan<kWaves>((uint64_t)(lane == 0 ? above : 0), sh.wave_u, n_above);
+  __syncthreads();
+  // the kept copies, first chunk first
+  const double one = frame.weight(z_cut);
+  uint64_t seen = 0;
+  for (int32_t c0 = 0; c0 < C; c0 += kThreads) {
+    const int32_t c = c0 + t;
+    const uint64_t eq = c < C ? rec[c].far : 0;
+    uint64_t total;
+    const uint64_t pre = seen + block_scan<kWaves>(eq, sh.wave_u, total);
+    const uint64_t take = pre >= cut.copies ? 0 : (cut.copies - pre < eq ? cut.copies - pre : eq);
+    if (c < C) rec[c].s += (double)take * one;
+    if (take > 0 && pre + take == cut.copies) {  // the last kept copy is in this chunk
+      sh.chunk = c;
+      sh.found_before = take;
+    }
+    seen += total;
+  }
+  __syncthreads();
+  if (cut.copies < seen) {
+    const int32_t j = sh.chunk * source.vecs + t;
+    const uint64_t want = sh.found_before;
+    uint64_t eq = 0;
+    float z[P];
+    E::unpack(source.one(t < source.vecs ? j : 0), z);
+    auto is = [&](int e) {
+      const int32_t at = j * P + e;
+      return t < source.vecs && at >= lead && at < end && row_key<E>(z[e]) == cut.key;
+    };
+#pragma unroll
+    for (int e = 0; e < P; ++e) eq += is(e);
+    uint64_t total;
+    uint64_t pre = block_scan<kWaves>(eq, sh.wave_u, total);
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      if (is(e) && ++pre == want) sh.eq_last = j * P + e - lead;
+    }
+    __syncthreads();
+    eq_last = sh.eq_last;
+  }
+  return (int64_t)(n_above + (cut.copies < seen ? cut.copies : seen));
+}
+
+// The draw: S, the chunk the uniform lands in (every wave for itself, 64 chunks at a time: no barrier, the same
+// result in each), and the token in it.  mass_of(c): a chunk's mass in the frame.  Returns S.
+template <class E, int kThreads, bool kCut, class Source, class Mass>
+__device__ __forceinline__ double draw(const Args& a, const Source& source, Shared<kThreads>& sh, const Frame& frame,
+                                       bool is_cut, const Cut& cut, int32_t eq_last, double u, int64_t slot,
+                                       int64_t n_kept, Mass mass_of) {
+  constexpr int P = E::kPerVec, kWaves = kThreads / kWave;
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  const int32_t C = source.C, lead = source.lead(), end = lead + source.values();
+  double S = 0.0;
+  for (int32_t c0 = 0; c0 < C; c0 += kWave) S += mass_of(c0 + lane);
+  S = wave_sum(S);
+  const double target = u * S;
+  double carry = 0.0, before = 0.0;
+  int32_t chunk = -1, last_chunk = 0;
+  for (int32_t c0 = 0; c0 < C && chunk < 0; c0 += kWave) {
+    const double x = mass_of(c0 + lane);
+    const double inc = carry + wave_detail::inclusive_scan(x);
+    const uint64_t hit = __ballot(x > 0.0 && inc > target), some = __ballot(x > 0.0);
+    if (some) last_chunk = c0 + 63 - __builtin_clzll(some);
+    if (hit) {
+      const int who = __ffsll((unsigned long long)hit) - 1;
+      chunk = c0 + who;
+      before = lane_value(inc - x, who);
+    }
+    carry = lane_value(inc, kWave - 1);
+  }
+  // u S within rounding of S: the last chunk with a kept weight, and its last kept token
+  const bool past = chunk < 0;
+  if (past) chunk = last_chunk;
+  const int32_t j = chunk * source.vecs + t;
+  double w[P], sum = 0.0;
+  {
+    float z[P];
+    E::unpack(source.one(t < source.vecs ? j : 0), z);
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      const int32_t at = j * P + e;
+      bool keep = t < source.vecs && at >= lead && at < end;
+      if (kCut && is_cut) {
+        const uint32_t key = row_key<E>(z[e]);
+        keep = keep && (key > cut.key || (key == cut.key && at - lead <= eq_last));
+      }
+      w[e] = keep ? frame.weight(z[e]) : 0.0;
+      sum += w[e];
+    }
+  }
+  double total;
+  double run = before + block_scan<kWaves>(sum, sh.wave_d, total);
+  int32_t first = kNone, last = kNone;
+  double first_w = 0.0, last_w = 0.0;
+#pragma unroll
+  for (int e = 0; e < P; ++e) {
+    if (!(w[e] > 0.0)) continue;
+    run += w[e];
+    last = j * P + e - lead;
+    last_w = w[e];
+    if (!past && run > target && first == kNone) {
+      first = last;
+      first_w = w[e];
+    }
+  }
+  const int32_t y = block_first<kWaves>(first, sh.wave_i[0]);
+  const int32_t y_last = block_last<kWaves>(last, sh.wave_i[1]);
+  if (y != kNone ? first == y : last == y_last && last != kNone)
+    write_token(a, slot, y != kNone ? y : y_last, (float)((y != kNone ? first_w : last_w) / S), (int32_t)n_kept);
+  return S;
+}
+
+template <class E, int kVpl, bool kCut>
+__global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
+  constexpr int kWaves = kDrawThreads / kWave, P = E::kPerVec;
+  static_assert(kVpl * kWave <= kDrawThreads, "one vector of a chunk per thread");
+  __shared__ Shared<kDrawThreads> sh;
+  const int t = threadIdx.x, lane = t & (kWave - 1);
   const int64_t row = blockIdx.x;
   const int64_t slot = slot_of(a, row);
   if (slot < 0) {
@@ -780,6 +990,7 @@ __global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
     return;
   }
 
+  const MemorySource<E, kDrawThreads, kVpl> source{view, C};
   if (f.greedy) {  // the first chunk that holds the maximum, then its first element
     int32_t chunk = 0;
     for (int32_t c0 = 0; c0 < C; c0 += kWave) {
@@ -789,9 +1000,9 @@ __global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
         break;
       }
     }
-    const int32_t j = chunk * kVecs + t;
+    const int32_t j = chunk * source.vecs + t;
     int32_t id = kNone;
-    if (t < kVecs) {
+    if (t < source.vecs) {
       float z[P];
       E::unpack(view.one(j), z);
 #pragma unroll
@@ -815,7 +1026,6 @@ __global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
   // a chunk's mass in the row's frame
   const double near_scale = near ? 1.0 : frame.weight(0.0f);
   auto stats_mass = [&](const Record& r) { return r.far ? (r.s > 0.0 ? r.s * frame.weight(r.m) : 0.0) : r.s * near_scale; };
-
   Cut cut;
   cut.key = 0;
   cut.copies = ~0ull;
@@ -827,191 +1037,53 @@ __global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
       for (int32_t c = lane; c < C; c += kWave) S += stats_mass(rec[c]);
       S = wave_sum(S);
     }
-    const MemorySource<E, kDrawThreads> source{view};
     cut = cut_of<E, kDrawThreads>(source, sh, a, f, frame, m, S);
-
-    // Each chunk's mass above the cut and its copies of the cut's key.  The logits above it are
-    // gathered in shared memory first, 64 to a weight: computing weights in place would
-    // cost every lane the exponential for the few that are kept.
-    __shared__ float gather_s[kWaves][kWave + P * kWave];
-    float* const list = gather_s[wave];
-    const float z_cut = row_key_logit<E>(cut.key);
-    uint32_t above = 0;
-    for (int32_t c = wave; c < C; c += kWaves) {
-      double s = 0.0;
-      uint32_t eq = 0, held = 0;
-      source.vectors(c * kVecs, (c + 1) * kVecs, kWave, [&](int32_t, u32x4 v, bool) {
-        float z[P];
-        E::unpack(v, z);
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const bool more = z[e] > z_cut;
-          const uint64_t over = __ballot(more);
-          if (more)
-            list[held + __builtin_amdgcn_mbcnt_hi((uint32_t)(over >> 32),
-                                                  __builtin_amdgcn_mbcnt_lo((uint32_t)over, 0))] = z[e];
-          held += __builtin_popcountll(over);
-          eq += fmaxf(z[e], -__builtin_inff()) == z_cut;
-        }
-        while (held >= kWave) {
-          held -= kWave;
-          s += frame.weight(list[held + lane]);
-          above += kWave;
-        }
-      });
-      if (lane < held) s += frame.weight(list[lane]);
-      above += held;
-      s = wave_sum(s);
-      eq = wave_sum_u32(eq);
-      if (z_cut == -__builtin_inff()) {  // what the chunk holds beside the row came as -inf
-        const int32_t lo = c * kVecs * P, hi = lo + kVecs * P;
-        eq -= (view.lead > lo ? view.lead - lo : 0) + (view.end < hi ? hi - view.end : 0);
-      }
-      if (lane == 0) {
-        rec[c].s = s;
-        rec[c].far = eq;
-      }
-    }
-    uint64_t n_above;
-    (void)block_scan<kWaves>((uint64_t)(lane == 0 ? above : 0), sh.wave_u, n_above);
-    __syncthreads();
-    // the kept copies, first chunk first
-    const double one = frame.weight(z_cut);
-    uint64_t seen = 0;
-    for (int32_t c0 = 0; c0 < C; c0 += kDrawThreads) {
-      const int32_t c = c0 + t;
-      const uint64_t eq = c < C ? rec[c].far : 0;
-      uint64_t total;
-      const uint64_t pre = seen + block_scan<kWaves>(eq, sh.wave_u, total);
-      const uint64_t take = pre >= cut.copies ? 0 : (cut.copies - pre < eq ? cut.copies - pre : eq);
-      if (c < C) rec[c].s += (double)take * one;
-      if (take > 0 && pre + take == cut.copies) {  // the last kept copy is in this chunk
-        sh.chunk = c;
-        sh.found_before = take;
-      }
-      seen += total;
-    }
-    __syncthreads();
-    n_kept = (int64_t)(n_above + (cut.copies < seen ? cut.copies : seen));
-    if (cut.copies < seen) {
-      const int32_t j = sh.chunk * kVecs + t;
-      const uint64_t want = sh.found_before;
-      uint64_t eq = 0;
-      float z[P];
-      E::unpack(view.one(t < kVecs ? j : 0), z);
-      auto is = [&](int e) {
-        const int32_t at = j * P + e;
-        return t < kVecs && at >= view.lead && at < view.end && row_key<E>(z[e]) == cut.key;
-      };
-#pragma unroll
-      for (int e = 0; e < P; ++e) eq += is(e);
-      uint64_t total;
-      uint64_t pre = block_scan<kWaves>(eq, sh.wave_u, total);
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        if (is(e) && ++pre == want) sh.eq_last = j * P + e - view.lead;
-      }
-      __syncthreads();
-      eq_last = sh.eq_last;
-    }
+    n_kept = cut_masses<E, kDrawThreads>(source, sh, frame, cut, rec, eq_last);
   }
-
-  // S, and the chunk the uniform lands in
-  auto mass_of = [&](int32_t c) { return c < C ? (kCut && f.cut ? rec[c].s : stats_mass(rec[c])) : 0.0; };
-  double S = 0.0;
-  for (int32_t c0 = 0; c0 < C; c0 += kWave) S += mass_of(c0 + lane);
-  S = wave_sum(S);
-  const double target = u * S;
-  double carry = 0.0, before = 0.0;
-  int32_t chunk = -1, last_chunk = 0;
-  for (int32_t c0 = 0; c0 < C && chunk < 0; c0 += kWave) {
-    const double x = mass_of(c0 + lane);
-    const double inc = carry + wave_detail::inclusive_scan(x);
-    const uint64_t hit = __ballot(x > 0.0 && inc > target), some = __ballot(x > 0.0);
-    if (some) last_chunk = c0 + 63 - __builtin_clzll(some);
-    if (hit) {
-      const int who = __ffsll((unsigned long long)hit) - 1;
-      chunk = c0 + who;
-      before = lane_value(inc - x, who);
-    }
-    carry = lane_value(inc, kWave - 1);
-  }
-  // u S within rounding of S: the last chunk with a kept weight, and its last kept token
-  const bool past = chunk < 0;
-  if (past) chunk = last_chunk;
-  const int32_t j = chunk * kVecs + t;
-  double w[P], sum = 0.0;
-  {
-    float z[P];
-    E::unpack(view.one(t < kVecs ? j : 0), z);
-#pragma unroll
-    for (int e = 0; e < P; ++e) {
-      const int32_t at = j * P + e;
-      bool keep = t < kVecs && at >= view.lead && at < view.end;
-      if (kCut && f.cut) {
-        const uint32_t key = row_key<E>(z[e]);
-        keep = keep && (key > cut.key || (key == cut.key && at - view.lead <= eq_last));
-      }
-      w[e] = keep ? frame.weight(z[e]) : 0.0;
-      sum += w[e];
-    }
-  }
-  double total;
-  double run = before + block_scan<kWaves>(sum, sh.wave_d, total);
-  int32_t first = kNone, last = kNone;
-  float first_p = 0.0f, last_p = 0.0f;
-#pragma unroll
-  for (int e = 0; e < P; ++e) {
-    if (!(w[e] > 0.0)) continue;
-    run += w[e];
-    const int32_t id = j * P + e - view.lead;
-    last = id;
-    last_p = (float)(w[e] / S);
-    if (!past && run > target && first == kNone) {
-      first = id;
-      first_p = last_p;
-    }
-  }
-  const int32_t y = block_first<kWaves>(first, sh.wave_i[0]);
-  const int32_t y_last = block_last<kWaves>(last, sh.wave_i[1]);
-  if (y != kNone ? first == y : last == y_last && last != kNone)
-    write_token(a, slot, y != kNone ? y : y_last, y != kNone ? first_p : last_p, (int32_t)n_kept);
+  const double S = draw<E, kDrawThreads, kCut>(a, source, sh, frame, f.cut, cut, eq_last, u, slot, n_kept, [&](int32_t c) {
+    return c < C ? (kCut && f.cut ? rec[c].s : stats_mass(rec[c])) : 0.0;
+  });
   if (a.probs && t == 0) a.state[row] = state_of(slot, base, k2, S, cut, eq_last);
 }
 
-// A row of at most kThreads x kVecs vectors, in one launch: it stays in shared memory.  Sums per
-// vector go to shared memory too, and each thread takes kVecs neighbouring ones, so prefix sums over the
-// threads are prefix sums over the ids.
+// A row of at most kThreads x kVecs vectors, in one launch: it stays in shared memory.
 template <class E, int kThreads, int kVecs, bool kCut>
 __global__ __launch_bounds__(kThreads) void row_whole(Args a) {
   constexpr int kWaves = kThreads / kWave, P = E::kPerVec;
   __shared__ Shared<kThreads> sh;
   __shared__ u32x4 row_s[kThreads * kVecs];
-  static_assert(kThreads * kVecs <= kWindow, "the sums take the histogram's place");
+  __shared__ Record rec[kWaves];
   const int t = threadIdx.x, lane = t & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int64_t row = blockIdx.x;
   const int64_t slot = slot_of(a, row);
   if (slot < 0) return;
   const RowView<E> view(a, row);
-  const SharedSource<E, kThreads> x{row_s, (view.end + P - 1) / P, view.lead, a.V};
+  const int32_t n = (view.end + P - 1) / P;
+  const SharedSource<E, kThreads> source{row_s, n, (n + kWaves - 1) / kWaves, view.lead, a.V};
   float m = -__builtin_inff();
   {
     u32x4 v[kVecs];
-    view.template edge<kVecs>(t, kThreads, v);
+    if (view.inside(0, kThreads * kVecs)) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) v[i] = view.vec(t + i * kThreads);
+    } else {
+      view.template edge<kVecs>(t, kThreads, v);
+    }
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       float z[P];
       E::unpack(v[i], z);
 #pragma unroll
       for (int e = 0; e < P; ++e) m = fmaxf(m, z[e]);
-      row_s[i * kThreads + t] = v[i];  // read back by this thread alone, but for the draw's last step
+      row_s[i * kThreads + t] = v[i];
     }
   }
   const Profile f = profile_of(a, row);
   const double u = f.greedy ? 0.0 : a.uniform[row];
   m = wave_max(m);
   if (lane == 0) sh.wave_f[wave] = m;
+  if (t == 0) sh.chunk = kNone;
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sh.wave_f[w]);
@@ -1019,12 +1091,11 @@ __global__ __launch_bounds__(kThreads) void row_whole(Args a) {
   RowState st = empty_state(slot, kNothing);
   if (f.ok && m > -__builtin_inff() && m < __builtin_inff() && u >= 0.0 && u < 1.0) {
     if (f.greedy) {
-      if (t == 0) sh.chunk = kNone;
-      __syncthreads();
       int32_t id = kNone;
-      x.vectors([&](int32_t, int32_t id0, u32x4 v) {
+      source.all([&](int32_t j, u32x4 v) {
         float z[P];
         E::unpack(v, z);
+        const int32_t id0 = j * P - view.lead;
 #pragma unroll
         for (int e = P - 1; e >= 0; --e) id = z[e] == m && id0 + e < id ? id0 + e : id;
       });
@@ -1035,121 +1106,35 @@ __global__ __launch_bounds__(kThreads) void row_whole(Args a) {
       if (t == 0) write_token(a, slot, st.token, 1.0f, 1);
     } else {
       const Frame frame(m, kLog2e / f.T);
-      double* const sums = reinterpret_cast<double*>(sh.hist);
       Cut cut;
       cut.key = 0;
       cut.copies = ~0ull;
       int32_t eq_last = kNone;
       int64_t n_kept = a.V;
-      if (kCut && f.cut) {
+      const bool is_cut = kCut && f.cut;
+      if (!is_cut || (f.top_p && !f.top_k)) {  // the whole row's masses, chunk by chunk
+        double s = 0.0;
+        source.chunk(wave, [&](int32_t, u32x4 v) {
+          float z[P];
+          E::unpack(v, z);
+#pragma unroll
+          for (int e = 0; e < P; ++e) s += frame.weight(z[e]);
+        });
+        s = wave_sum(s);
+        if (lane == 0) rec[wave].s = s;
+        __syncthreads();
+      }
+      if (is_cut) {
         double S = 0.0;
         if (f.top_p && !f.top_k) {
-          double s = 0.0;
-          x.each([&](float z) { s += frame.weight(z); });
-          (void)block_scan<kWaves>(s, sh.wave_d, S);
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) S += rec[w].s;
         }
-        cut = cut_of<E, kThreads>(x, sh, a, f, frame, m, S);
-        uint64_t n = 0;  // kept above the cut in the high half, copies of its key in the low one
-        x.each([&](float z) {
-          const uint32_t key = row_key<E>(z);
-          n += (key > cut.key ? 1ull << 32 : 0) + (key == cut.key ? 1ull : 0);
-        });
-        uint64_t all;
-        (void)block_scan<kWaves>(n, sh.wave_u, all);
-        const uint64_t n_eq = all & 0xffffffffu;
-        n_kept = (int64_t)((all >> 32) + (cut.copies < n_eq ? cut.copies : n_eq));
-        if (cut.copies < n_eq) {  // the id of the last kept copy
-          auto copies = [&](int32_t j, auto found) {
-            float z[P];
-            E::unpack(row_s[j], z);
-#pragma unroll
-            for (int e = 0; e < P; ++e) {
-              const int32_t id = j * P - view.lead + e;
-              if ((uint32_t)id < (uint32_t)a.V && row_key<E>(z[e]) == cut.key) found(id);
-            }
-          };
-          __syncthreads();
-          uint64_t eq = 0;
-          for (int i = 0; i < kVecs; ++i) {
-            const int32_t j = t * kVecs + i;
-            if (j < x.n) copies(j, [&](int32_t) { ++eq; });
-          }
-          uint64_t total;
-          uint64_t pre = block_scan<kWaves>(eq, sh.wave_u, total);
-          if (pre < cut.copies && pre + eq >= cut.copies) {
-            for (int i = 0; i < kVecs; ++i) {
-              const int32_t j = t * kVecs + i;
-              if (j < x.n)
-                copies(j, [&](int32_t id) {
-                  if (++pre == cut.copies) sh.eq_last = id;
-                });
-            }
-          }
-          __syncthreads();
-          eq_last = sh.eq_last;
-        }
+        cut = cut_of<E, kThreads>(source, sh, a, f, frame, m, S);
+        n_kept = cut_masses<E, kThreads>(source, sh, frame, cut, rec, eq_last);
       }
-      auto weight_at = [&](int32_t id, float z) {  // -inf beside the row weighs 0
-        const uint32_t key = row_key<E>(z);
-        const bool keep = !kCut || !f.cut || key > cut.key || (key == cut.key && id <= eq_last);
-        return keep ? frame.weight(z) : 0.0;
-      };
-      __syncthreads();
-      x.vectors([&](int32_t j, int32_t id0, u32x4 v) {
-        float z[P];
-        E::unpack(v, z);
-        double s = 0.0;
-#pragma unroll
-        for (int e = 0; e < P; ++e) s += weight_at(id0 + e, z[e]);
-        sums[j] = s;
-      });
-      __syncthreads();
-      double own[kVecs], s = 0.0;
-      int32_t last = kNone;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const int32_t j = t * kVecs + i;
-        own[i] = j < x.n ? sums[j] : 0.0;
-        s += own[i];
-        last = own[i] > 0.0 ? j : last;
-      }
-      double S;
-      const double pre = block_scan<kWaves>(s, sh.wave_d, S);
-      const double target = u * S;
-      int32_t first = kNone;
-      double run = pre, before = 0.0;
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        if (first == kNone && own[i] > 0.0 && run + own[i] > target) {
-          first = t * kVecs + i;
-          before = run;
-        }
-        run += own[i];
-      }
-      // the first vector whose sums pass the target; else (u S within rounding of S) the last one with a kept value
-      const int32_t j_last = block_last<kWaves>(last, sh.wave_i[1]);
-      const int32_t j_first = block_first<kWaves>(first, sh.wave_i[0]);
-      const bool past = j_first == kNone;
-      if (past ? last == j_last && last != kNone : first == j_first) {
-        const int32_t j = past ? last : first;
-        float z[P];
-        E::unpack(row_s[j], z);
-        int32_t y = kNone;
-        double w_y = 0.0;
-        run = before;
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-          const int32_t id = j * P - view.lead + e;
-          const double w = weight_at(id, z[e]);
-          // the first value past the target, or the last kept one
-          if (w > 0.0 && (past || y == kNone || !(run > target))) {
-            y = id;
-            w_y = w;
-          }
-          run += w;
-        }
-        write_token(a, slot, y, (float)(w_y / S), (int32_t)n_kept);
-      }
+      const double S = draw<E, kThreads, kCut>(a, source, sh, frame, f.cut, cut, eq_last, u, slot, n_kept,
+                                               [&](int32_t c) { return c < kWaves ? rec[c < kWaves ? c : 0].s : 0.0; });
       st = state_of(slot, frame.base, frame.k2, S, cut, eq_last);
     }
   } else if (t == 0) {
@@ -1159,9 +1144,10 @@ __global__ __launch_bounds__(kThreads) void row_whole(Args a) {
   float* out = a.probs + slot * a.V;
   const double d_min = st.kind == kDistribution ? -1100.0 / st.k2 : 0.0;
   const bool grid = ((reinterpret_cast<uintptr_t>(out) - view.lead * 4) & 15) == 0;
-  x.vectors([&](int32_t, int32_t id0, u32x4 v) {
+  source.all([&](int32_t j, u32x4 v) {
     float z[P], p[P];
     E::unpack(v, z);
+    const int32_t id0 = j * P - view.lead;
 #pragma unroll
     for (int e = 0; e < P; ++e)
       p[e] = st.kind == kDistribution ? prob_of<E>(st, d_min, z[e], id0 + e) : (id0 + e == st.token ? 1.0f : 0.0f);
