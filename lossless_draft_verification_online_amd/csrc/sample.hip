@@ -275,53 +275,64 @@ __global__ __launch_bounds__(kStatsWaves* kWave) void row_stats(Args a) {
   const int32_t c = (int32_t)(unit - row * a.C);
   if (slot_of(a, row) < 0) return;
   const RowView<E> view(a, row);
-  u32x4 v[kVpl];
-  view.template load<kVpl>(c * (kVpl * kWave), lane, v);
   const Profile f = profile_of(a, row);
   Record r;
   r.s = 0.0;
   r.m = -__builtin_inff();
   r.far = 0;
-  if (f.ok && !f.greedy && !f.cut) {
-    const NearFrame frame(kLog2e / f.T);
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < kVpl; ++i) {
-      float z[E::kPerVec];
-      E::unpack(v[i], z);
-#pragma unroll
-      for (int e = 0; e < E::kPerVec; ++e) s += frame.weight(z[e]);
-      __builtin_amdgcn_sched_barrier(0);  // vectors one after another: interleaved they spill
-    }
-    r.s = wave_sum(s);
-  }
-  const bool mass = f.ok && !f.greedy && f.top_p && !f.top_k;  // the nucleus is a share of the whole row
-  if (f.ok && (f.greedy || f.cut || !near_sum(r.s))) {
-    float m = -__builtin_inff();
-    forget(v);
-#pragma unroll
-    for (int i = 0; i < kVpl; ++i) {
-      float z[E::kPerVec];
-      E::unpack(v[i], z);
-#pragma unroll
-      for (int e = 0; e < E::kPerVec; ++e) m = fmaxf(m, z[e]);
-    }
-    r.m = wave_max(m);
-    r.far = 1;
-    if (!f.greedy && (!f.cut || mass)) {
-      forget(v);
+  const int32_t j0 = c * (kVpl * kWave);
+  u32x4 v[kVpl];
+  // A body for each way of loading: behind a common one the first vector would wait for the last.
+  auto chunk = [&] {
+    if (f.ok && !f.greedy && !f.cut) {
+      const NearFrame frame(kLog2e / f.T);
       double s = 0.0;
-      const Frame frame(r.m, kLog2e / f.T);
 #pragma unroll
       for (int i = 0; i < kVpl; ++i) {
         float z[E::kPerVec];
         E::unpack(v[i], z);
 #pragma unroll
         for (int e = 0; e < E::kPerVec; ++e) s += frame.weight(z[e]);
-        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);  // vectors one after another: interleaved they spill
       }
       r.s = wave_sum(s);
     }
+    const bool mass = f.ok && !f.greedy && f.top_p && !f.top_k;  // the nucleus is a share of the whole row
+    if (f.ok && (f.greedy || f.cut || !near_sum(r.s))) {
+      float m = -__builtin_inff();
+      forget(v);
+#pragma unroll
+      for (int i = 0; i < kVpl; ++i) {
+        float z[E::kPerVec];
+        E::unpack(v[i], z);
+#pragma unroll
+        for (int e = 0; e < E::kPerVec; ++e) m = fmaxf(m, z[e]);
+      }
+      r.m = wave_max(m);
+      r.far = 1;
+      if (!f.greedy && (!f.cut || mass)) {
+        forget(v);
+        double s = 0.0;
+        const Frame frame(r.m, kLog2e / f.T);
+#pragma unroll
+        for (int i = 0; i < kVpl; ++i) {
+          float z[E::kPerVec];
+          E::unpack(v[i], z);
+#pragma unroll
+          for (int e = 0; e < E::kPerVec; ++e) s += frame.weight(z[e]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        r.s = wave_sum(s);
+      }
+    }
+  };
+  if (view.inside(j0, kVpl * kWave)) {
+#pragma unroll
+    for (int i = 0; i < kVpl; ++i) v[i] = view.vec((int64_t)j0 + i * kWave + lane);
+    chunk();
+  } else {
+    view.template edge<kVpl>(j0 + lane, kWave, v);
+    chunk();
   }
   if (lane == 0) a.rec[unit] = r;
 }
@@ -329,14 +340,16 @@ __global__ __launch_bounds__(kStatsWaves* kWave) void row_stats(Args a) {
 template <int kThreads>
 struct Shared {
   static constexpr int kWaves = kThreads / kWave;
+  static constexpr int kRoom = 4096;  // logits of a bracket
   uint64_t hist[kWindow];
+  u32x4 room[kRoom / 4];
   double wave_d[kWaves];
   uint64_t wave_u[kWaves];
   float wave_f[kWaves];
   int32_t wave_i[2][kWaves];
   uint64_t found_before, found_at;
   double mass_before;
-  uint32_t found_bin, key;
+  uint32_t found_bin, key, n_room;
   int32_t eq_last, chunk;
 };
 
@@ -456,8 +469,9 @@ struct SharedSource {
   }
   template <class F>
   __device__ __forceinline__ void all(F f) const {
+    // whole waves in every round: f may use the wave's other lanes
 #pragma unroll 1
-    for (int32_t j = threadIdx.x; j < n; j += kThreads) f(j, v[j]);
+    for (int32_t j = threadIdx.x; j - (int32_t)(threadIdx.x & (kWave - 1)) < n; j += kThreads) f(j, one(j));
   }
   template <class F>
   __device__ __forceinline__ void chunk(int32_t c, F f) const {
@@ -525,7 +539,10 @@ __device__ Selected radix_select(const Source& source, Shared<kThreads>& sh, Val
     }
     uint64_t total;
     uint64_t pre = block_scan<kThreads / kWave>(own, sh.wave_u, total);
-    if (level == 0) r.need = need_of(total);
+    if (level == 0) {
+      r.need = need_of(total);
+      if (r.need > total) r.need = total;
+    }
     const uint64_t want = r.need - r.before;
     for (int b = 0; b < kPer; ++b) {
       const int bin = bins - 1 - (kPer * t + b);
@@ -660,48 +677,192 @@ __device__ __forceinline__ bool window_cut(const Source& source, Shared<kThreads
   return true;
 }
 
+// Top-k and top-p by radix selection over a source's logits.  Of a top-p without top-k, `above` is the mass of
+// the logits that rank before all of the source's, and S the whole row's (S < 0: the source is the row).
+template <class E, int kThreads, class Source>
+__device__ __forceinline__ void select_cut(const Source& source, Shared<kThreads>& sh, int32_t V, const Profile& f,
+                                           const Frame& frame, double above, double S, Cut& cut) {
+  uint64_t k_copies_all = 0;
+  cut.key = 0;
+  cut.copies = ~0ull;
+  if (f.top_k) {
+    const uint64_t k = (uint64_t)f.k;
+    const Selected r = radix_select<E, kThreads>(
+        source, sh, [](float) { return (uint64_t)1; }, [k](uint64_t) { return k; });
+    cut.key = r.key;
+    cut.copies = k - r.before;
+    k_copies_all = r.at;
+  }
+  if (f.top_p) {
+    // Masses as integers, with room for V of them in 62 bits.  The copies of the top-k key behind
+    // rank k count in the passes and are taken off the total; they rank last, so no prefix that
+    // the smaller sum asks for reaches them.
+    const int bits = 62 - (32 - __builtin_clz((unsigned)V));
+    auto mass = [&](float z) { return (uint64_t)__builtin_rint(__builtin_amdgcn_ldexp(frame.weight(z), bits)); };
+    const uint32_t k_key = cut.key;
+    const uint64_t p = (uint64_t)f.p;
+    const uint64_t over = f.top_k ? (k_copies_all - cut.copies) * mass(row_key_logit<E>(k_key)) : 0;
+    const Selected r = radix_select<E, kThreads>(
+        source, sh, [&](float z) { return row_key<E>(z) >= k_key ? mass(z) : (uint64_t)0; },
+        [&](uint64_t total) {
+          const double rest = (double)f.p * S / 1000.0 - above;
+          const uint64_t need = S >= 0.0 ? (rest > 0.0 ? (uint64_t)__builtin_ceil(__builtin_amdgcn_ldexp(rest, bits)) : 0)
+                                         : (uint64_t)(((unsigned __int128)(total - over) * p + 999) / 1000);
+          return need ? need : (uint64_t)1;
+        });
+    const uint64_t one = mass(row_key_logit<E>(r.key));
+    cut.key = r.key;
+    cut.copies = (r.need - r.before + one - 1) / one;
+  }
+}
+
+// Top-k and top-p of a binary32 row.  The counts of the 4096 leading 16-bit parts of keys below the maximum's
+// bracket the cut: for top-k the bins down to rank k; for top-p, a bin's mass lying between its count times its
+// smallest and its largest weight, the bins from where the nucleus may end to where it must.  A second pass
+// gathers the bracket's logits in shared memory, where the selection is exact, and sums the mass above it.
+// False if the cut lies below the window or more logits lie in the bracket than there is room for.
+template <class E, int kThreads, class Source>
+__device__ __forceinline__ bool bracket_cut(const Source& source, Shared<kThreads>& sh, int32_t V, const Profile& f,
+                                            const Frame& frame, uint32_t top, double S, Cut& cut) {
+  constexpr int kPer = kWindow / kThreads, kWaves = kThreads / kWave, P = E::kPerVec;
+  constexpr int kRoom = Shared<kThreads>::kRoom, kList = (1 + P) * kWave;
+  static_assert(kWaves * kList * sizeof(float) <= sizeof(sh.hist), "the lists take the histogram's place");
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const uint32_t top16 = top >> 16;
+  if (top16 - (order_key(-__builtin_inff()) >> 16) < kWindow) return false;  // -inf must lie below the window
+  uint32_t* const count = reinterpret_cast<uint32_t*>(sh.hist);
+  __syncthreads();
+  for (int b = t; b < kWindow; b += kThreads) count[b] = 0;
+  if (t == 0) {
+    sh.found_bin = kWindow;
+    sh.n_room = 0;
+  }
+  __syncthreads();
+  if (top16 >= 0x8000u + kWindow) {  // positive logits alone, as in window_cut
+    const uint32_t max16 = top16 & 0x7fffu;
+    source.all([&](int32_t, u32x4 v) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t d = max16 - (v[w] >> 16);
+        if (d < kWindow) atomicAdd(&count[d], 1u);
+      }
+    });
+  } else {
+    source.all([&](int32_t, u32x4 v) {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t d = top16 - (order_key(__uint_as_float(v[w])) >> 16);
+        if (d < kWindow) atomicAdd(&count[d], 1u);
+      }
+    });
+  }
+  __syncthreads();
+  uint64_t c[kPer], own = 0;
+#pragma unroll
+  for (int b = 0; b < kPer; ++b) {
+    c[b] = count[kPer * t + b];
+    own += c[b];
+  }
+  uint64_t total;
+  const uint64_t pre = block_scan<kWaves>(own, sh.wave_u, total);
+  int32_t lo_bin = kNone, hi_bin = kNone;  // this thread's candidates for the bracket's ends
+  if (f.top_k) {
+    if (total < (uint64_t)f.k) return false;
+    uint64_t run = pre;
+#pragma unroll
+    for (int b = 0; b < kPer; ++b) {
+      run += c[b];
+      if (hi_bin == kNone && run >= (uint64_t)f.k) hi_bin = kPer * t + b;
+    }
+  } else {
+    double lo[kPer], hi[kPer], own_lo = 0.0, own_hi = 0.0;
+#pragma unroll
+    for (int b = 0; b < kPer; ++b) {
+      const uint32_t bin = kPer * t + b;
+      lo[b] = hi[b] = 0.0;
+      if (c[b] > 0) {
+        const uint32_t key = (top16 - bin) << 16;
+        lo[b] = (double)c[b] * frame.weight(key_logit(key));
+        hi[b] = (double)c[b] * fmin(frame.weight(key_logit(key | 0xffffu)), 1.0);
+      }
+      own_lo += lo[b];
+      own_hi += hi[b];
+    }
+    // both ends a little wide: the sums carry roundings
+    const double want = (double)f.p * S / 1000.0;
+    double all, run_lo = block_scan<kWaves>(own_lo, sh.wave_d, all);
+    double run_hi = block_scan<kWaves>(own_hi, sh.wave_d, all);
+#pragma unroll
+    for (int b = 0; b < kPer; ++b) {
+      run_lo += lo[b];
+      run_hi += hi[b];
+      if (lo_bin == kNone && c[b] > 0 && run_hi * (1.0 + 1e-9) >= want) lo_bin = kPer * t + b;
+      if (hi_bin == kNone && c[b] > 0 && run_lo * (1.0 - 1e-9) >= want) hi_bin = kPer * t + b;
+    }
+  }
+  const int32_t first = f.top_k ? 0 : block_first<kWaves>(lo_bin, sh.wave_i[0]);
+  const int32_t last = block_first<kWaves>(hi_bin, sh.wave_i[1]);
+  if (first == kNone || last == kNone) return false;
+  uint64_t mine = 0, held_total;
+#pragma unroll
+  for (int b = 0; b < kPer; ++b) mine += kPer * t + b >= first && kPer * t + b <= last ? c[b] : 0;
+  (void)block_scan<kWaves>(mine, sh.wave_u, held_total);
+  if (held_total > (uint64_t)kRoom) return false;
+  __syncthreads();
+
+  float* const list = reinterpret_cast<float*>(sh.hist) + wave * kList;
+  float* const room = reinterpret_cast<float*>(sh.room);
+  double s = 0.0;
+  uint32_t held = 0;
+  source.all([&](int32_t, u32x4 v) {
+    float z[P];
+    E::unpack(v, z);
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      const uint32_t d = top16 - (order_key(z[e]) >> 16);
+      const bool before = d < (uint32_t)first, in = !before && d <= (uint32_t)last;
+      const uint64_t over = __ballot(before), put = __ballot(in);
+      if (before)
+        list[held + __builtin_amdgcn_mbcnt_hi((uint32_t)(over >> 32),
+                                              __builtin_amdgcn_mbcnt_lo((uint32_t)over, 0))] = z[e];
+      held += __builtin_popcountll(over);
+      if (put) {  // the order in the room does not matter: the selection goes by value
+        const int leader = __ffsll((unsigned long long)put) - 1;
+        uint32_t at = 0;
+        if (lane == leader) at = atomicAdd(&sh.n_room, (uint32_t)__builtin_popcountll(put));
+        at = lane_value(at, leader);
+        at += __builtin_amdgcn_mbcnt_hi((uint32_t)(put >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)put, 0));
+        if (in && at < (uint32_t)kRoom) room[at] = z[e];
+      }
+    }
+    while (held >= kWave) {
+      held -= kWave;
+      s += frame.weight(list[held + lane]);
+    }
+  });
+  if (lane < held) s += frame.weight(list[lane]);
+  double above;
+  (void)block_scan<kWaves>(s, sh.wave_d, above);
+  const SharedSource<E, kThreads> chosen{sh.room, (int32_t)((held_total + P - 1) / P), 0, 0, (int32_t)held_total};
+  select_cut<E, kThreads>(chosen, sh, V, f, frame, above, f.top_k ? -1.0 : S, cut);
+  return true;
+}
+
 // The cut of a row's profile.  S: the whole row's mass in the frame (of a row with top-p, without top-k).
 template <class E, int kThreads, class Source>
-__device__ __forceinline__ Cut cut_of(const Source& source, Shared<kThreads>& sh, const Args& a, const Profile& f, const Frame& frame,
-                      float m, double S) {
+__device__ __forceinline__ Cut cut_of(const Source& source, Shared<kThreads>& sh, const Args& a, const Profile& f,
+                                      const Frame& frame, float m, double S) {
   Cut cut;
   cut.key = 0;
   cut.copies = ~0ull;
-  bool done = !f.top_k && !f.top_p;
-  if constexpr (E::kBytes == 2) {
-    if (!done) done = window_cut<E, kThreads>(source, sh, f, frame, row_key<E>(m), S, cut);
-  }
-  if (!done) {
-    uint64_t k_copies_all = 0;
-    cut.key = 0;
-    cut.copies = ~0ull;
-    if (f.top_k) {
-      const uint64_t k = (uint64_t)f.k;
-      const Selected r = radix_select<E, kThreads>(
-          source, sh, [](float) { return (uint64_t)1; }, [k](uint64_t) { return k; });
-      cut.key = r.key;
-      cut.copies = k - r.before;
-      k_copies_all = r.at;
-    }
-    if (f.top_p) {
-      // Masses as integers, with room for V of them in 62 bits.  The copies of the top-k key behind
-      // rank k count in the passes and are taken off the total; they rank last, so no prefix that
-      // the smaller sum asks for reaches them.
-      const int bits = 62 - (32 - __builtin_clz((unsigned)a.V));
-      auto mass = [&](float z) { return (uint64_t)__builtin_rint(__builtin_amdgcn_ldexp(frame.weight(z), bits)); };
-      const uint32_t k_key = cut.key;
-      const uint64_t p = (uint64_t)f.p;
-      const uint64_t over = f.top_k ? (k_copies_all - cut.copies) * mass(row_key_logit<E>(k_key)) : 0;
-      const Selected r = radix_select<E, kThreads>(
-          source, sh, [&](float z) { return row_key<E>(z) >= k_key ? mass(z) : (uint64_t)0; },
-          [&](uint64_t total) {
-            const uint64_t need = (uint64_t)(((unsigned __int128)(total - over) * p + 999) / 1000);
-            return need ? need : (uint64_t)1;
-          });
-      const uint64_t one = mass(row_key_logit<E>(r.key));
-      cut.key = r.key;
-      cut.copies = (r.need - r.before + one - 1) / one;
-    }
+  if (f.top_k || f.top_p) {
+    bool done;
+    if constexpr (E::kBytes == 2)
+      done = window_cut<E, kThreads>(source, sh, f, frame, row_key<E>(m), S, cut);
+    else
+      done = bracket_cut<E, kThreads>(source, sh, a.V, f, frame, row_key<E>(m), S, cut);
+    if (!done) select_cut<E, kThreads>(source, sh, a.V, f, frame, 0.0, -1.0, cut);
   }
   if (f.min_p > 0.0f) {
     // the smallest key of weight min_p or more lies within rounding of z_max + T ln(min_p)
@@ -1151,7 +1312,7 @@ __global__ __launch_bounds__(kThreads) void row_whole(Args a) {
 #pragma unroll
     for (int e = 0; e < P; ++e)
       p[e] = st.kind == kDistribution ? prob_of<E>(st, d_min, z[e], id0 + e) : (id0 + e == st.token ? 1.0f : 0.0f);
-    if (grid && id0 >= 0 && id0 + P <= a.V) {
+    if (grid && id0 >= 0 && id0 <= a.V - P) {
       write_probs<P>(out + id0, p);
     } else {
 #pragma unroll

@@ -120,6 +120,22 @@ def test_equal_logits_rank_by_id(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [3000, 90000])
+def test_log_probabilities_and_narrow_rows(V, dtype):
+    """Rows without a positive logit, rows whose logits lie close together, and cuts far below the maximum."""
+    z = torch.log_softmax(logits_of(6, V, "fp32", 30), 1)
+    z[1] = 5.0 + 0.01 * torch.randn(V, generator=torch.Generator().manual_seed(31))
+    z[2] = -3.0 + 1e-4 * torch.randn(V, generator=torch.Generator().manual_seed(32))
+    z[3] = 0.001 * z[3]
+    z[4, 100:] -= 200.0
+    z = z.to(DT[dtype])
+    check(z, uniforms(6, 33), 1.0)
+    check(z, uniforms(6, 34), 0.9, top_p=[900, 900, 500, 999, 990, 10])
+    check(z, uniforms(6, 35), 0.9, top_k=[50, 2500, 2000, 2999, 700, 1], top_p=[950, 1000, 700, 1000, 400, 1000])
+    check(z, uniforms(6, 36), 1.1, min_p=[0.001, 0.99, 0.9999, 0.9, 1e-30, 0.5])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_masked_and_special_logits(dtype):
     V = 3001
     inf, nan = float("inf"), float("nan")
