@@ -19,6 +19,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "../../include/sdv.h"
 #include "sdv_device.hpp"
 
@@ -32,7 +34,7 @@ constexpr int kWindow = 4096;  // bins of the counts below the maximum
 
 struct Record {  // one chunk of a row
   double s;      // sum of weights: absolute ones, 2^(z k2), or with far those in the frame of m
-  float m;       // maximum (far chunks, and rows that are cut or take their argmax)
+  float m;       // maximum (of far chunks, and in rows that are cut or take their argmax)
   uint32_t far;  // truncated rows: copies of the cut's key
 };
 
@@ -162,14 +164,6 @@ struct RowView {
   }
 };
 
-// Hides from the compiler that a pass works on the values of the pass before: it would keep every
-// unpacked logit and weight in registers for the second use, and spill.
-template <int N>
-__device__ __forceinline__ void forget(u32x4 (&v)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(v[i]));
-}
-
 // 2^t: t = n + r with |r| <= 1/2 by adding 1.5 x 2^52, and 2^r = 1 + r q(r) with q the
 // interpolation of (2^r - 1) / r at the eight Chebyshev nodes (relative error 2.1e-12).  t = d k2
 // enters both steps unrounded; |t| is below 2^31.
@@ -282,53 +276,51 @@ __global__ __launch_bounds__(kStatsWaves* kWave) void row_stats(Args a) {
   r.far = 0;
   const int32_t j0 = c * (kVpl * kWave);
   u32x4 v[kVpl];
+  const bool mass = f.ok && !f.greedy && (!f.cut || (f.top_p && !f.top_k));  // the nucleus is a share of the whole row
+  const bool peak = f.ok && (f.greedy || f.cut);
   // A body for each way of loading: behind a common one the first vector would wait for the last.
   auto chunk = [&] {
-    if (f.ok && !f.greedy && !f.cut) {
-      const NearFrame frame(kLog2e / f.T);
+    float m = -__builtin_inff();
+    auto pass = [&](auto with_mass, auto with_peak, const auto& frame) {
       double s = 0.0;
 #pragma unroll
       for (int i = 0; i < kVpl; ++i) {
+        // hides from the compiler that passes work on the same values: it would keep them all unpacked, and spill
+        asm volatile("" : "+v"(v[i]));
         float z[E::kPerVec];
         E::unpack(v[i], z);
 #pragma unroll
-        for (int e = 0; e < E::kPerVec; ++e) s += frame.weight(z[e]);
+        for (int e = 0; e < E::kPerVec; ++e) {
+          if constexpr (with_mass.value) s += frame.weight(z[e]);
+          if constexpr (with_peak.value) m = fmaxf(m, z[e]);
+        }
         __builtin_amdgcn_sched_barrier(0);  // vectors one after another: interleaved they spill
       }
-      r.s = wave_sum(s);
-    }
-    const bool mass = f.ok && !f.greedy && f.top_p && !f.top_k;  // the nucleus is a share of the whole row
-    if (f.ok && (f.greedy || f.cut || !near_sum(r.s))) {
-      float m = -__builtin_inff();
-      forget(v);
-#pragma unroll
-      for (int i = 0; i < kVpl; ++i) {
-        float z[E::kPerVec];
-        E::unpack(v[i], z);
-#pragma unroll
-        for (int e = 0; e < E::kPerVec; ++e) m = fmaxf(m, z[e]);
-      }
-      r.m = wave_max(m);
+      if constexpr (with_mass.value) r.s = wave_sum(s);
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    const NearFrame near(kLog2e / f.T);
+    if (mass && peak)
+      pass(yes, yes, near);
+    else if (mass)
+      pass(yes, no, near);
+    else if (peak)
+      pass(no, yes, near);
+    if (mass && !near_sum(r.s)) {
+      if (!peak) pass(no, yes, near);
+      m = wave_max(m);
+      pass(yes, no, Frame(m, kLog2e / f.T));
       r.far = 1;
-      if (!f.greedy && (!f.cut || mass)) {
-        forget(v);
-        double s = 0.0;
-        const Frame frame(r.m, kLog2e / f.T);
-#pragma unroll
-        for (int i = 0; i < kVpl; ++i) {
-          float z[E::kPerVec];
-          E::unpack(v[i], z);
-#pragma unroll
-          for (int e = 0; e < E::kPerVec; ++e) s += frame.weight(z[e]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        r.s = wave_sum(s);
-      }
     }
+    r.m = wave_max(m);
   };
   if (view.inside(j0, kVpl * kWave)) {
 #pragma unroll
-    for (int i = 0; i < kVpl; ++i) v[i] = view.vec((int64_t)j0 + i * kWave + lane);
+    for (int i = 0; i < kVpl; ++i) {
+      v[i] = view.vec((int64_t)j0 + i * kWave + lane);
+      __builtin_amdgcn_sched_barrier(0);  // asked for in the order of their use
+    }
     chunk();
   } else {
     view.template edge<kVpl>(j0 + lane, kWave, v);
@@ -563,6 +555,10 @@ __device__ Selected radix_select(const Source& source, Shared<kThreads>& sh, Val
   return r;
 }
 
+// A mass within 2^-44 of its share reaches it: the sums carry roundings of about 2^-50, and copies of one logit
+// that make the share exactly (500 of 1000) have to.
+constexpr double kReach = 1.0 - 0x1p-44;
+
 struct Cut {
   uint32_t key;  // kept: keys above it, and its first `copies` copies
   uint64_t copies;
@@ -638,7 +634,7 @@ __device__ __forceinline__ bool window_cut(const Source& source, Shared<kThreads
     double total;
     double pre = block_scan<kWaves>(x, sh.wave_d, total);
     if (f.top_k) S = total;
-    const double want = (double)f.p * S;  // thousandths of S
+    const double want = (double)f.p * S * kReach;  // thousandths of S
     int32_t bin = kNone;
 #pragma unroll
     for (int b = kPer - 1; b >= 0; --b) {
@@ -705,7 +701,7 @@ __device__ __forceinline__ void select_cut(const Source& source, Shared<kThreads
     const Selected r = radix_select<E, kThreads>(
         source, sh, [&](float z) { return row_key<E>(z) >= k_key ? mass(z) : (uint64_t)0; },
         [&](uint64_t total) {
-          const double rest = (double)f.p * S / 1000.0 - above;
+          const double rest = (double)f.p * S * kReach / 1000.0 - above;
           const uint64_t need = S >= 0.0 ? (rest > 0.0 ? (uint64_t)__builtin_ceil(__builtin_amdgcn_ldexp(rest, bits)) : 0)
                                          : (uint64_t)(((unsigned __int128)(total - over) * p + 999) / 1000);
           return need ? need : (uint64_t)1;
@@ -1132,12 +1128,9 @@ __global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
   const double k2 = f.ok && !f.greedy ? kLog2e / f.T : 1.0;
   for (int32_t c = lane; c < C; c += kWave) {
     const Record r = rec[c];
-    if (r.far) {
-      m = fmaxf(m, r.m);
-      any_high = any_high || (double)r.m * k2 > 900.0;
-    } else {
-      any_near = true;
-    }
+    m = fmaxf(m, r.m);
+    any_near = any_near || !r.far;
+    any_high = any_high || (r.far && (double)r.m * k2 > 900.0);
   }
   m = wave_max(m);
   const bool plain = f.ok && !f.greedy && !(kCut && f.cut);
