@@ -14,6 +14,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "cache_view.hpp"
 
 namespace attend_impl {
@@ -759,11 +761,21 @@ __device__ __forceinline__ int piece_of(int token, int p) {
   return D == 128 ? p ^ (2 * (token & 7)) : p ^ (2 * ((token >> 1) & 3));
 }
 
+// 16 bytes per lane from base + off to to + 16 lane, past the registers.  As a buffer load: a load by flat address that
+// writes shared memory counts as a flat one, and while one is in flight every wait for a read of shared memory is a
+// wait for all of them.
+__device__ __forceinline__ void direct_load(const char* base, int32_t bytes, uint32_t off, char* to) {
+  constexpr int kRaw = 0x27000;  // last word of the buffer's description: bytes, no stride
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(__builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, kRaw),
+                                           (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
+}
+
 template <int D>
 __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a) {
   constexpr int kLine = D * 2, kPieces = D / 8, kSteps = D / 16, kDB = D / 32;
   constexpr int kLoadRows = kWave / kPieces;       // rows of one direct load
   constexpr int kLoads = 16 / kLoadRows;           // of a wave's 16 rows
+  constexpr int kKeys = 6;                         // keys' operands in flight
   // arrays of their own: reads of one tile do not wait for the loads into the other
   __shared__ __align__(16) char k_0[kRowsTile * kLine], k_1[kRowsTile * kLine];
   __shared__ __align__(16) char v_0[kRowsTile * kLine], v_1[kRowsTile * kLine];
@@ -774,11 +786,16 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   const int32_t head = (int32_t)(unit / a.tiles);
   const TileOf at = tile_of<kRowsColumns>(a, a.tiles - 1 - (unit - head * a.tiles));
   if (at.r.index < 0) return;
-  const int32_t i = at.r.index, len = a.cache.len[i];
+  // one value in all lanes: kept in scalar registers
+  auto all = [](int32_t x) { return __builtin_amdgcn_readfirstlane(x); };
+  const int32_t i = all(at.r.index), len = all(a.cache.len[i]);
   const bool ok = len_fits(len, at.r.k);
   const int32_t columns = (at.r.k + 1) * a.G;
   const int32_t c_end = at.c0 + kRowsColumns < columns ? at.c0 + kRowsColumns : columns;
-  const Span span = span_of(len, (uint32_t)at.c0 / (uint32_t)a.G, (uint32_t)(c_end - 1) / (uint32_t)a.G, a.window, a.sinks);
+  Span span = span_of(len, (uint32_t)at.c0 / (uint32_t)a.G, (uint32_t)(c_end - 1) / (uint32_t)a.G, a.window, a.sinks);
+  span.lo = all(span.lo);
+  span.hi = all(span.hi);
+  span.near_end = all(span.near_end);
   // tiles of 64 tokens over [0, near_end) and [lo, hi)
   int32_t t_lo = span.lo / kRowsTile, n_near = (span.near_end + kRowsTile - 1) / kRowsTile;
   if (t_lo <= n_near) t_lo = n_near = 0;
@@ -791,7 +808,6 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   const int32_t j = (uint32_t)(live ? c : columns - 1) / (uint32_t)a.G;
   const int32_t h = head * a.G + (live ? c - j * a.G : 0);
   const int32_t pos = len + j;
-  const bool wave_live = at.c0 + 32 * wave < columns;
   const int32_t pos_lo = lane_value(pos, 0), pos_hi = lane_value(pos, 31);  // ascending over the columns
   bf16x8 q[kSteps];
   {
@@ -802,8 +818,6 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   }
 
   // Rows 16 wave .. of a tile are the wave's to load: one page.
-  typedef __attribute__((address_space(3))) void* Lds;
-  typedef const __attribute__((address_space(1))) void* Global;
   uint32_t off[kLoads];
 #pragma unroll
   for (int x = 0; x < kLoads; ++x) {
@@ -820,16 +834,12 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     const int32_t p = __builtin_amdgcn_readfirstlane(entry);
     return p >= 0 && p < a.cache.n_pages ? p : -1;
   };
-  auto load = [&](int32_t n, int32_t page, char* k_to, char* v_to) {
+  auto load = [&](const char* from, int32_t n, int32_t page, char* to) {
     const int64_t at_row = a.cache.row(page < 0 ? 0 : page, head, start(n) + 16 * wave) * kLine;
-    k_to += 16 * wave * kLine;
-    v_to += 16 * wave * kLine;
+    from += ((int64_t)all((int32_t)(at_row >> 32)) << 32) | (uint32_t)all((int32_t)at_row);
+    to += 16 * wave * kLine;
 #pragma unroll
-    for (int x = 0; x < kLoads; ++x)
-      __builtin_amdgcn_global_load_lds((Global)(a.cache.keys + at_row + off[x]), (Lds)(k_to + x * 1024), 16, 0, 0);
-#pragma unroll
-    for (int x = 0; x < kLoads; ++x)
-      __builtin_amdgcn_global_load_lds((Global)(a.cache.values + at_row + off[x]), (Lds)(v_to + x * 1024), 16, 0, 0);
+    for (int x = 0; x < kLoads; ++x) direct_load(from, 16 * kLine, off[x], to + x * 1024);
   };
 
   f32x16 acc[kDB];
@@ -840,8 +850,31 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   float m = -__builtin_inff(), l = 0.0f;
   __shared__ __align__(16) int32_t page_s[2][kRowsWaves];
 
-  int32_t page = page_of(entry_at(0)), entry_1 = entry_at(1);
-  auto tile = [&](int32_t n, int buffer, char* k_s, char* v_s, char* k_next, char* v_next) {
+  typedef f32x16 Scores[2];  // element e of a block: token 8 (e / 4) + 4 half + e mod 4
+  const f32x16 none16 = {};
+  auto key = [&](const char* k_s, int blk, int s) {
+    const int token = 32 * blk + col;
+    return *reinterpret_cast<const bf16x8*>(k_s + token * kLine + piece_of<D>(token, 2 * s + half) * 16);
+  };
+  // values of step s: tokens 16 s + 4 half + 0 .. 3 and 8 further; a 16-lane group reads 4 tokens x 16 values
+  auto value = [&](char* v_s, int s, bf16x4 (&v)[kDB][2]) {
+    typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
+    const int g = (lane >> 4) & 1, in = lane & 15, token = 16 * s + 4 * half + (in >> 2);
+#pragma unroll
+    for (int d = 0; d < kDB; ++d) {
+      const int pc = 4 * d + 2 * g + ((in >> 1) & 1);
+      char* const r0 = v_s + token * kLine + piece_of<D>(token, pc) * 16 + (in & 1) * 8;
+      char* const r1 = v_s + (token + 8) * kLine + piece_of<D>(token + 8, pc) * 16 + (in & 1) * 8;
+      v[d][0] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)r0);
+      v[d][1] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)r1);
+    }
+  };
+  const int32_t near = a.window ? pos - a.window : -1;  // slots above it are seen, and the first `sinks`
+
+  // Tile n's softmax and product with its values, the next tile's scores under the softmax (behind the last tile those
+  // of what its buffer holds, which nothing uses).
+  int32_t page = page_of(entry_at(0)), page_1 = page_of(entry_at(1)), entry_2 = entry_at(2);
+  auto tile = [&](int32_t n, Scores& sc, Scores& ahead, char* k_s, char* v_s, char* k_next, char* v_next) {
     const int32_t s0 = start(n);
     // a value no row sees is 0: what lies there may be NaN
     const int32_t first = s0 + 16 * wave;
@@ -858,61 +891,23 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
         for (int x = 0; x < kPieces / 4; ++x) *reinterpret_cast<u32x4*>(to + ((lane & 3) + 4 * x) * 16) = z;
       }
     }
-    if (lane == 0) page_s[buffer][wave] = page;
+    if (lane == 0) page_s[n & 1][wave] = page;
     __builtin_amdgcn_s_waitcnt(0x0f70);  // this wave's direct loads
-    __syncthreads();  // the tile is there, and every wave is done with the other one
-    const int4 pages = *reinterpret_cast<const int4*>(page_s[buffer]);
-    page = page_of(entry_1);
-    if (n + 1 < n_tiles) load(n + 1, page, k_next, v_next);
-    entry_1 = entry_at(n + 2);
-    // tiles that no column of the wave sees
-    if (!wave_live || s0 > pos_hi || (a.window && s0 + kRowsTile <= pos_lo - a.window + 1 && s0 >= a.sinks)) return;
+    __syncthreads();  // its values and the next keys are there, and every wave is done with the other buffers
+    const int4 pages = *reinterpret_cast<const int4*>(page_s[n & 1]);
+    bf16x8 kf[kKeys];
+#pragma unroll
+    for (int f = 0; f < kKeys; ++f) kf[f] = key(k_s, f / kSteps, f % kSteps);
+    page = page_1;
+    page_1 = page_of(entry_2);
+    if (n + 1 < n_tiles) load(a.cache.values, n + 1, page, v_next);
+    if (n + 2 < n_tiles) load(a.cache.keys, n + 2, page_1, k_next);
+    entry_2 = entry_at(n + 3);
     bool whole = s0 + kRowsTile <= pos_lo + 1 && (a.window == 0 || s0 > pos_hi - a.window || s0 + kRowsTile <= a.sinks);
     const int missing = pages.x | pages.y | pages.z | pages.w;  // negative: one of the four pages is none
     whole = whole && missing >= 0;
-
-    // Products in the order written: the next operands are read under the products of the last ones.
-    f32x16 sc[2];
-    bf16x8 kf[2][kSteps];
-    auto key = [&](int blk, int s) {
-      const int token = 32 * blk + col;
-      return *reinterpret_cast<const bf16x8*>(k_s + token * kLine + piece_of<D>(token, 2 * s + half) * 16);
-    };
-#pragma unroll
-    for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) sc[blk][e] = 0.0f;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) kf[0][s] = key(0, s);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      kf[1][s] = key(1, s);
-      sc[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[0][s], q[s], sc[0], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    // values of step s: tokens 16 s + 4 half + 0 .. 3 and 8 further; a 16-lane group reads 4 tokens x 16 values
-    bf16x4 vf[2][kDB][2];
-    auto value = [&](int s, bf16x4 (&v)[kDB][2]) {
-      typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
-      const int g = (lane >> 4) & 1, in = lane & 15, token = 16 * s + 4 * half + (in >> 2);
-#pragma unroll
-      for (int d = 0; d < kDB; ++d) {
-        const int pc = 4 * d + 2 * g + ((in >> 1) & 1);
-        char* const r0 = v_s + token * kLine + piece_of<D>(token, pc) * 16 + (in & 1) * 8;
-        char* const r1 = v_s + (token + 8) * kLine + piece_of<D>(token + 8, pc) * 16 + (in & 1) * 8;
-        v[d][0] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)r0);
-        v[d][1] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)r1);
-      }
-    };
-    value(0, vf[0]);
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) sc[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[1][s], q[s], sc[1], 0, 0, 0);
-    // element e of a block: token 8 (e / 4) + 4 half + e mod 4
     if (!whole) {
       const int32_t none = (pages.x < 0 ? 1 : 0) | (pages.y < 0 ? 2 : 0) | (pages.z < 0 ? 4 : 0) | (pages.w < 0 ? 8 : 0);
-      const int32_t near = a.window ? pos - a.window : -1;  // slots above it, and the first `sinks`
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
 #pragma unroll
@@ -947,30 +942,56 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     const float frame = m == -__builtin_inff() ? 0.0f : m;
     float sum = 0.0f;
     bf16x8 p[4];
+    auto weigh = [&](int blk, int e) {
+      const float x = fast_exp2(fmaf(sc[blk][e], a.scale2, -frame));
+      sum += x;
+      p[2 * blk + (e >> 3)][e & 7] = (__bf16)x;
+    };
+    // In the order written: a product of the next scores, then the weights that fill its cycles; operands are read
+    // a block or a step ahead.
+    bf16x4 vf[2][kDB][2];
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int blk = 0; blk < 2; ++blk)
+    for (int f = 0; f < 2 * kSteps; ++f) {
+      const int blk = f / kSteps, s = f % kSteps;
+      ahead[blk] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[f % kKeys], q[s], s == 0 ? none16 : ahead[blk], 0, 0, 0);
+      if (f + kKeys < 2 * kSteps) kf[f % kKeys] = key(k_s, (f + kKeys) / kSteps, (f + kKeys) % kSteps);
+      if (f == 2 * kSteps - 4) value(v_s, 0, vf[0]);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float x = fast_exp2(fmaf(sc[blk][e], a.scale2, -frame));
-        sum += x;
-        p[2 * blk + (e >> 3)][e & 7] = (__bf16)x;
-      }
+      for (int e = 0; e < 16 / kSteps; ++e) weigh(blk, 16 / kSteps * s + e);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     l += sum;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      __builtin_amdgcn_sched_barrier(0);
-      if (s < 3) value(s + 1, vf[(s + 1) & 1]);
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int d = 0; d < kDB; ++d)
+      for (int d = 0; d < kDB; ++d) {
         acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
             __builtin_shufflevector(vf[s & 1][d][0], vf[s & 1][d][1], 0, 1, 2, 3, 4, 5, 6, 7), p[s], acc[d], 0, 0, 0);
+        if (d == 0 && s < 3) {  // behind the first product, which waits for this step's: counts of such reads in flight are not told apart
+          __builtin_amdgcn_sched_barrier(0);
+          value(v_s, s + 1, vf[(s + 1) & 1]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
     }
   };
-  if (n_tiles > 0) load(0, page, k_0, v_0);
-  for (int32_t n = 0; n < n_tiles; n += 2) {
-    tile(n, 0, k_0, v_0, k_1, v_1);
-    if (n + 1 < n_tiles) tile(n + 1, 1, k_1, v_1, k_0, v_0);
+  if (n_tiles > 0) {
+    Scores sc_0, sc_1;
+    load(a.cache.keys, 0, page, k_0);
+    load(a.cache.values, 0, page, v_0);
+    if (n_tiles > 1) load(a.cache.keys, 1, page_1, k_1);
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      sc_0[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key(k_0, 0, s), q[s], s == 0 ? none16 : sc_0[0], 0, 0, 0);
+      sc_0[1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key(k_0, 1, s), q[s], s == 0 ? none16 : sc_0[1], 0, 0, 0);
+    }
+    for (int32_t n = 0; n < n_tiles; n += 2) {
+      tile(n, sc_0, sc_1, k_1, v_0, k_0, v_1);
+      if (n + 1 < n_tiles) tile(n + 1, sc_1, sc_0, k_0, v_1, k_1, v_0);
+    }
   }
   {
     float x, y;
