@@ -782,13 +782,37 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   const int t = threadIdx.x, lane = t & (kWave - 1), col = lane & 31, half = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
   // head by head, the last tiles (of the longest rows) first
-  const int64_t unit = unit_of_block(blockIdx.x, gridDim.x);
-  const int32_t head = (int32_t)(unit / a.tiles);
-  const TileOf at = tile_of<kRowsColumns>(a, a.tiles - 1 - (unit - head * a.tiles));
-  if (at.r.index < 0) return;
+  const uint32_t unit = (uint32_t)unit_of_block(blockIdx.x, gridDim.x), tiles = (uint32_t)a.tiles;
+  const int32_t head = (int32_t)(unit / tiles);
+  const int64_t tile_no = tiles - 1 - (unit - head * tiles);
   // one value in all lanes: kept in scalar registers
   auto all = [](int32_t x) { return __builtin_amdgcn_readfirstlane(x); };
-  const int32_t i = all(at.r.index), len = all(a.cache.len[i]);
+  // tile_of, with the lengths loaded beside the offsets, 64 requests at a time: a workgroup has nothing to do until
+  // its pages are known, so each load behind another counts
+  TileOf at;
+  int32_t len;
+  {
+    const int32_t i0 =
+        a.B <= kWave ? 0 : find_last(a.B, tile_no, [&](int32_t q) { return first_tile(a.cu, q, a.G, kRowsColumns); });
+    if (i0 < 0) return;
+    const bool in = i0 + lane < a.B;
+    const int32_t mine = in ? i0 + lane : a.B - 1;
+    const int32_t lo = a.cu[mine], hi = a.cu[mine + 1], n = a.cache.len[mine];
+    const int64_t first = (uint32_t)(lo + mine) * (uint32_t)a.G / (uint32_t)kRowsColumns + mine;  // first_tile
+    const uint64_t who = __ballot(in && first <= tile_no);
+    if (!who) return;
+    const int src = a.B <= kWave ? 63 - __builtin_clzll(who) : 0;
+    at.r.index = i0 + src;
+    at.r.first = lane_value(lo, src);
+    at.r.k = lane_value(hi, src) - at.r.first;
+    at.r.row0 = (int64_t)at.r.first + at.r.index;
+    if (at.r.first < 0 || at.r.k < 0 || (int64_t)at.r.first + at.r.k > a.n_d) return;
+    const int64_t c0 = (tile_no - (int64_t)lane_value((uint64_t)first, src)) * kRowsColumns;
+    if (c0 >= (int64_t)(at.r.k + 1) * a.G) return;
+    at.c0 = (int32_t)c0;
+    len = lane_value(n, src);
+  }
+  const int32_t i = at.r.index;
   const bool ok = len_fits(len, at.r.k);
   const int32_t columns = (at.r.k + 1) * a.G;
   const int32_t c_end = at.c0 + kRowsColumns < columns ? at.c0 + kRowsColumns : columns;
@@ -809,13 +833,6 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   const int32_t h = head * a.G + (live ? c - j * a.G : 0);
   const int32_t pos = len + j;
   const int32_t pos_lo = lane_value(pos, 0), pos_hi = lane_value(pos, 31);  // ascending over the columns
-  bf16x8 q[kSteps];
-  {
-    const char* src = a.queries + ((at.r.row0 + j) * a.query_stride + (int64_t)h * D) * 2 + 16 * half;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      q[s] = __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(src + 32 * s) ^ a.flip);
-  }
 
   // Rows 16 wave .. of a tile are the wave's to load: one page.
   uint32_t off[kLoads];
@@ -841,6 +858,22 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) direct_load(from, 16 * kLine, off[x], to + x * 1024);
   };
+
+  const int32_t entry_0 = entry_at(0), entry_1 = entry_at(1);
+  int32_t entry_2 = entry_at(2);
+  u32x4 q_raw[kSteps];
+  {
+    const char* src = a.queries + ((at.r.row0 + j) * a.query_stride + (int64_t)h * D) * 2 + 16 * half;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) q_raw[s] = *reinterpret_cast<const u32x4*>(src + 32 * s);
+  }
+  int32_t page = page_of(entry_0), page_1 = page_of(entry_1);
+  if (n_tiles > 0) {
+    load(a.cache.keys, 0, page, k_0);
+    load(a.cache.values, 0, page, v_0);
+    if (n_tiles > 1) load(a.cache.keys, 1, page_1, k_1);
+  }
+  bf16x8 q[kSteps];
 
   f32x16 acc[kDB];
 #pragma unroll
@@ -873,7 +906,6 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
 
   // Tile n's softmax and product with its values, the next tile's scores under the softmax (behind the last tile those
   // of what its buffer holds, which nothing uses).
-  int32_t page = page_of(entry_at(0)), page_1 = page_of(entry_at(1)), entry_2 = entry_at(2);
   auto tile = [&](int32_t n, Scores& sc, Scores& ahead, char* k_s, char* v_s, char* k_next, char* v_next) {
     const int32_t s0 = start(n);
     // a value no row sees is 0: what lies there may be NaN
@@ -907,14 +939,18 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     const int missing = pages.x | pages.y | pages.z | pages.w;  // negative: one of the four pages is none
     whole = whole && missing >= 0;
     if (!whole) {
-      const int32_t none = (pages.x < 0 ? 1 : 0) | (pages.y < 0 ? 2 : 0) | (pages.z < 0 ? 4 : 0) | (pages.w < 0 ? 8 : 0);
+      // the tile's tokens that the column sees, a bit each
+      auto below = [&](int32_t x) { return x - s0 >= 64 ? ~0ull : (x > s0 ? (1ull << (x - s0)) - 1 : 0ull); };
+      uint64_t see = below(pos + 1) & (~below(near + 1) | below(a.sinks));
+      see &= (pages.x < 0 ? 0 : 0xffffull) | (pages.y < 0 ? 0 : 0xffffull << 16) | (pages.z < 0 ? 0 : 0xffffull << 32) |
+             (pages.w < 0 ? 0 : 0xffffull << 48);
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
+        const uint32_t hide = (uint32_t)~see >> (4 * half);
+        see >>= 32;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const int32_t s = s0 + 32 * blk + 8 * (e >> 2) + 4 * half + (e & 3);
-          const bool see = (s <= pos) & ((s > near) | (s < a.sinks)) & !((none >> (2 * blk + (e >> 3))) & 1);
-          sc[blk][e] = see ? sc[blk][e] : -__builtin_inff();
+          sc[blk][e] = hide & (1u << (8 * (e >> 2) + (e & 3))) ? -__builtin_inff() : sc[blk][e];
         }
       }
     }
@@ -978,11 +1014,10 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   };
   if (n_tiles > 0) {
     Scores sc_0, sc_1;
-    load(a.cache.keys, 0, page, k_0);
-    load(a.cache.values, 0, page, v_0);
-    if (n_tiles > 1) load(a.cache.keys, 1, page_1, k_1);
     __builtin_amdgcn_s_waitcnt(0x0f70);
     __syncthreads();
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) q[s] = __builtin_bit_cast(bf16x8, q_raw[s] ^ a.flip);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       sc_0[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key(k_0, 0, s), q[s], s == 0 ? none16 : sc_0[0], 0, 0, 0);
