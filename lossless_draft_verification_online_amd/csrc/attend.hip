@@ -861,17 +861,32 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
 
   const int32_t entry_0 = entry_at(0), entry_1 = entry_at(1);
   int32_t entry_2 = entry_at(2);
-  u32x4 q_raw[kSteps];
+  // The wave's queries and results pass through shared memory, where they change between a column per lane and whole
+  // lines (16-byte pieces of 32 columns took 2 to 3 us of a workgroup's time each way): one array holds the
+  // first halves of its 32 columns, another the second halves, each in the place of the wave's 16 rows of a tile.
+  constexpr int kHalf = kPieces / 2;                // pieces of half a column
+  constexpr int kQLoads = 32 * kHalf / kWave;
+  auto half_piece = [](int column, int p) { return 16 * (column * kHalf + (p ^ (column & (kHalf - 1)))); };
+  auto column_of = [&](int x) { return x * (kWave / kHalf) + lane / kHalf; };
+  auto from_lane = [](int64_t v, int src) {
+    return ((int64_t)__shfl((int32_t)(v >> 32), src) << 32) | (uint32_t)__shfl((int32_t)v, src);
+  };
   {
-    const char* src = a.queries + ((at.r.row0 + j) * a.query_stride + (int64_t)h * D) * 2 + 16 * half;
+    typedef __attribute__((address_space(3))) void* Lds;
+    typedef const __attribute__((address_space(1))) void* Global;
+    const int64_t q_at = ((at.r.row0 + j) * a.query_stride + (int64_t)h * D) * 2;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) q_raw[s] = *reinterpret_cast<const u32x4*>(src + 32 * s);
+    for (int x = 0; x < kQLoads; ++x) {
+      const int column = column_of(x);
+      const char* const src = a.queries + from_lane(q_at, column) + 16 * ((lane % kHalf) ^ (column & (kHalf - 1)));
+      __builtin_amdgcn_global_load_lds((Global)src, (Lds)(k_1 + 16 * wave * kLine + x * 1024), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((Global)(src + 16 * kHalf), (Lds)(v_1 + 16 * wave * kLine + x * 1024), 16, 0, 0);
+    }
   }
   int32_t page = page_of(entry_0), page_1 = page_of(entry_1);
   if (n_tiles > 0) {
     load(a.cache.keys, 0, page, k_0);
     load(a.cache.values, 0, page, v_0);
-    if (n_tiles > 1) load(a.cache.keys, 1, page_1, k_1);
   }
   bf16x8 q[kSteps];
 
@@ -1015,9 +1030,14 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   if (n_tiles > 0) {
     Scores sc_0, sc_1;
     __builtin_amdgcn_s_waitcnt(0x0f70);
-    __syncthreads();
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) q[s] = __builtin_bit_cast(bf16x8, q_raw[s] ^ a.flip);
+    for (int s = 0; s < kSteps; ++s) {
+      const char* const from = (s < kSteps / 2 ? k_1 : v_1) + 16 * wave * kLine;
+      q[s] = __builtin_bit_cast(
+          bf16x8, *reinterpret_cast<const u32x4*>(from + half_piece(col, (2 * s) % kHalf + half)) ^ a.flip);
+    }
+    __syncthreads();
+    if (n_tiles > 1) load(a.cache.keys, 1, page_1, k_1);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       sc_0[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(key(k_0, 0, s), q[s], s == 0 ? none16 : sc_0[0], 0, 0, 0);
@@ -1033,18 +1053,37 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     wave_detail::both<32>(l, x, y);
     l = x + y;
   }
-  if (!live) return;
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  char* const dst = a.out + ((at.r.row0 + j) * a.n_q + h) * kLine + 8 * half;
+  const int64_t out_at = ((at.r.row0 + j) * a.n_q + h) * (int64_t)kLine;
+  // the buffers that the last tile's successors would have taken are free
+  auto store = [&](char* first, char* second) {
+    first += 16 * wave * kLine;
+    second += 16 * wave * kLine;
 #pragma unroll
-  for (int d = 0; d < kDB; ++d)
+    for (int d = 0; d < kDB; ++d)
 #pragma unroll
-    for (int e = 0; e < 16; e += 4) {
-      bf16x4 w;
+      for (int e = 0; e < 16; e += 4) {
+        bf16x4 w;
 #pragma unroll
-      for (int x = 0; x < 4; ++x) w[x] = (__bf16)(acc[d][e + x] * inv);
-      *reinterpret_cast<bf16x4*>(dst + d * 64 + e * 4) = w;
+        for (int x = 0; x < 4; ++x) w[x] = (__bf16)(acc[d][e + x] * inv);
+        const int piece = 4 * d + e / 4;
+        *reinterpret_cast<bf16x4*>((d < kDB / 2 ? first : second) + half_piece(col, piece % kHalf) + 8 * half) = w;
+      }
+#pragma unroll
+    for (int x = 0; x < kQLoads; ++x) {
+      const int column = column_of(x);
+      char* const dst = a.out + from_lane(out_at, column) + 16 * (lane % kHalf);
+      const u32x4 lo = *reinterpret_cast<const u32x4*>(first + half_piece(column, lane % kHalf));
+      const u32x4 hi = *reinterpret_cast<const u32x4*>(second + half_piece(column, lane % kHalf));
+      if (at.c0 + 32 * wave + column >= columns) continue;
+      *reinterpret_cast<u32x4*>(dst) = lo;
+      *reinterpret_cast<u32x4*>(dst + 16 * kHalf) = hi;
     }
+  };
+  if (n_tiles & 1)
+    store(k_0, v_1);
+  else
+    store(k_1, v_0);
 }
 
 enum Mode { kUnits, kRanges, kSmallPages, kRows };
