@@ -587,7 +587,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
 
 // Two waves per SIMD hide each other's loads; sums of 64 columns, or of 256 values, take the registers of both.
 template <class E, int D, int QB>
-constexpr int kMinWaves = D * QB <= 256 ? 2 : 1;
+constexpr int kMinWaves = E::kBytes == 4 ? (D <= 128 ? 2 : 1) : (D * QB <= 256 ? 2 : 1);
 
 // A workgroup per unit.
 template <class E, int D, int QB, int kWaves, bool kWholePages>
@@ -1175,12 +1175,15 @@ int launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
 
 template <class E, int D>
 int launch_columns(const AttendArgs& a, const Plan& p, hipStream_t s) {
-  if constexpr (E::kBytes == 4 && D > 64) return launch<E, D, 1>(a, p, s);
-  if (p.qb == 1) return launch<E, D, 1>(a, p, s);
-  if constexpr (E::kBytes == 2 && D <= 128) {
-    if (p.qb == 4) return launch<E, D, 4>(a, p, s);
+  if constexpr (E::kBytes == 4 && D > 64) {
+    return launch<E, D, 1>(a, p, s);
+  } else {
+    if (p.qb == 1) return launch<E, D, 1>(a, p, s);
+    if constexpr (E::kBytes == 2 && D <= 128) {
+      if (p.qb == 4) return launch<E, D, 4>(a, p, s);
+    }
+    return launch<E, D, 2>(a, p, s);
   }
-  return launch<E, D, 2>(a, p, s);
 }
 
 template <class E>
