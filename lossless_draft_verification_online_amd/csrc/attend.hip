@@ -804,9 +804,10 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     const int src = a.B <= kWave ? 63 - __builtin_clzll(who) : 0;
     at.r.index = i0 + src;
     at.r.first = lane_value(lo, src);
-    at.r.k = lane_value(hi, src) - at.r.first;
+    const int32_t behind = lane_value(hi, src);
+    if (at.r.first < 0 || behind < at.r.first || behind > a.n_d) return;
+    at.r.k = behind - at.r.first;
     at.r.row0 = (int64_t)at.r.first + at.r.index;
-    if (at.r.first < 0 || at.r.k < 0 || (int64_t)at.r.first + at.r.k > a.n_d) return;
     const int64_t c0 = (tile_no - (int64_t)lane_value((uint64_t)first, src)) * kRowsColumns;
     if (c0 >= (int64_t)(at.r.k + 1) * a.G) return;
     at.c0 = (int32_t)c0;
@@ -1027,9 +1028,9 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
       }
     }
   };
+  __builtin_amdgcn_s_waitcnt(0x0f70);  // the direct loads, of a request without tiles too: its zeros take their place
   if (n_tiles > 0) {
     Scores sc_0, sc_1;
-    __builtin_amdgcn_s_waitcnt(0x0f70);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const char* const from = (s < kSteps / 2 ? k_1 : v_1) + 16 * wave * kLine;

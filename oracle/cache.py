@@ -23,11 +23,16 @@ def depths(parents) -> list[int] | None:
     return d
 
 
+def fits(length, K) -> bool:
+    """Whether positions behind `length` cached slots are 32-bit numbers, with room for a tile."""
+    return 0 <= length < 2 ** 31 - 1 - 1024 - K
+
+
 def requests(cu, cache_len, n_draft_rows, parents=None):
     """(i, first row, K, L, depths, visible rows per row) of the requests that are not passed over."""
     for i in range(len(cu) - 1):
         lo, hi = int(cu[i]), int(cu[i + 1])
-        if lo < 0 or hi < lo or hi > n_draft_rows or cache_len[i] < 0:
+        if lo < 0 or hi < lo or hi > n_draft_rows or not fits(int(cache_len[i]), hi - lo):
             continue
         K = hi - lo
         if parents is None:
@@ -115,7 +120,7 @@ def settle(key_cache, value_cache, table, cache_len, cu, accepted_len, accepted_
     new_len = np.array(cache_len, dtype=np.int32)
     for i in range(len(cu) - 1):
         lo, K, a, L = int(cu[i]), int(cu[i + 1] - cu[i]), int(accepted_len[i]), int(cache_len[i])
-        if lo < 0 or not 0 <= K <= 64 or int(cu[i + 1]) > len(accepted_nodes) or not 0 <= a <= K or L < 0:
+        if lo < 0 or not 0 <= K <= 64 or int(cu[i + 1]) > len(accepted_nodes) or not 0 <= a <= K or not fits(L, K):
             continue
         path = [int(n) for n in accepted_nodes[lo:lo + a]]
         if any(not b < n < K for b, n in zip([-1] + path, path)):

@@ -77,6 +77,24 @@ def test_prompts_under_windows(window, sinks):
     check(b, "bf16", window, sinks)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("length", [0, 1, 29, 64, 128, 129])
+def test_prompts_of_few_tiles(length, D):
+    check(Batch([27, 31, 33], [length, length + 37, length + 64], 2, D, 16, "bf16", length, Hq=8), "bf16")
+
+
+def test_prompts_of_many_requests():
+    ks = [(5 * i) % 40 for i in range(150)]
+    b = Batch(ks, [(7 * i) % 90 for i in range(150)], 1, 64, 16, "bf16", 22, Hq=16)
+    b.len[70] = -1
+    out = check(b, "bf16", 48, 2)
+    lo = int(b.cu[70]) + 70
+    assert not out[lo:lo + ks[70] + 1].any()
+    b.len[70] = 2 ** 31 - 1024 - ks[70]
+    table, length, cu = b.index_args()
+    assert torch.equal(sdv.attend(b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), table, length, cu, window=48, sinks=2), out)
+
+
 def test_what_no_row_of_a_prompt_sees_may_hold_anything():
     b = Batch([200, 100], [300, 9], 2, 128, 16, "bf16", 20, Hq=4)
     window, sinks = 64, 3
