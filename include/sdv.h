@@ -570,7 +570,7 @@ int sdv_kv_append(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, const
  *   queries [n_draft_rows + B][n_q_heads][head_dim], rows query_stride elements apart, 16-byte aligned;
  *   out     [n_draft_rows + B][n_q_heads][head_dim] contiguous, 16-byte aligned
  * Scores, statistics and sums are binary32; with bf16 the probabilities are rounded to bf16 for their
- * product with the values (relative 2^-9 each).  The same call gives the same bits.
+ * product with the values (relative 2^-8 each).  The same call gives the same bits.
  * workspace: sdv_attend_workspace_bytes(...), 16-byte aligned, not initialised.
  * Errors as sdv_kv_append, plus n_q_heads not a multiple of n_kv_heads, window < 0, sinks < 0 or a
  * scale that is not finite -> SDV_ERR_INVALID_ARG; more than INT32_MAX - 1024 rows times n_q_heads /

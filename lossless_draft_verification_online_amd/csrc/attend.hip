@@ -31,8 +31,7 @@ typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 struct AttendArgs {
   CacheView cache;
   int32_t B, n_q, G, window, sinks;
-  int32_t ranges;      // the ranges that the batch's work is cut into
-  int32_t part_tiles;  // > 0: a range is a part of one unit, of at most so many token tiles; 0: ranges of equal work
+  int32_t ranges;  // the ranges that the batch's work is cut into
   int64_t n_d, query_stride, tiles;
   float scale2;  // |scale| log2(e), at least 2^-126: a masked -inf stays one; the sign goes to the queries
   uint32_t flip;  // sign bits of a word of queries, set for a negative scale
@@ -95,19 +94,17 @@ __device__ __forceinline__ Span span_of(int32_t len, int32_t pos_lo, int32_t pos
   return s;
 }
 
-// The batch's work is the list of its units (tile of columns, head), request by request, each of `parts` items.
-// Long work: an item is a token tile, and the list is cut into equal ranges, one per workgroup.  Lengths
-// differ between requests, and one workgroup per unit leaves the card half empty at the end (1136 units of 64
-// requests in 512 places: 3 rounds for 2.2).  Short work: an item is a part of part_tiles tiles, and a range is one
-// item, so that no workgroup sets up two units (8 to 25 us each) for a few tiles.
+// The batch's work is the list of its units (tile of columns, head), request by request, each of its token tiles.
+// The list is cut into equal ranges, one per workgroup: lengths differ between requests, and few units leave
+// places empty (one request of 8 heads on 4000 tokens: 17 us by ranges, 42 by units).
 struct Work {
   int32_t first, k, len;      // the request
-  int32_t tiles, n, parts;    // column tiles; token tiles of a unit (those of all its rows), its items
+  int32_t tiles, n;           // column tiles; token tiles of a unit (those of all its rows)
   __device__ int64_t units(const AttendArgs& a) const { return (int64_t)tiles * a.cache.n_heads; }
 };
 __device__ __forceinline__ Work work_of(const AttendArgs& a, int32_t i, int32_t columns) {
   Work w;
-  w.tiles = w.n = w.parts = 0;
+  w.tiles = w.n = 0;
   w.len = a.cache.len[i];
   const Request r = request_at(a.cu, i, a.n_d);
   w.first = r.first;
@@ -115,7 +112,6 @@ __device__ __forceinline__ Work work_of(const AttendArgs& a, int32_t i, int32_t 
   if (r.index < 0) return w;
   w.tiles = (int32_t)(((uint32_t)(r.k + 1) * a.G + columns - 1) / (uint32_t)columns);
   w.n = !len_fits(w.len, r.k) ? 1 : span_of(w.len, 0, r.k, a.window, a.sinks).n;
-  w.parts = a.part_tiles ? (w.n + a.part_tiles - 1) / a.part_tiles : w.n;
   return w;
 }
 struct Stream {
@@ -129,21 +125,21 @@ __device__ __forceinline__ Stream stream_of(const AttendArgs& a, int32_t columns
   const int lane = threadIdx.x & (kWave - 1);
   Stream s;
   s.per = (a.B + kWave - 1) / kWave;
-  s.own.first = s.own.k = s.own.len = s.own.tiles = s.own.n = s.own.parts = 0;
+  s.own.first = s.own.k = s.own.len = s.own.tiles = s.own.n = 0;
   uint64_t items = 0, units = 0;
   for (int32_t k = 0; k < s.per; ++k) {
     const int32_t i = lane * s.per + k;
     if (i >= a.B) break;
     const Work w = work_of(a, i, columns);
     if (k == 0) s.own = w;
-    items += (uint64_t)(w.units(a) * w.parts);
+    items += (uint64_t)(w.units(a) * w.n);
     units += (uint64_t)w.units(a);
   }
   const uint64_t inc = wave_inclusive_scan(items);
   s.before = (int64_t)(inc - items);
   s.units_before = (int64_t)(wave_inclusive_scan(units) - units);
   s.total = (int64_t)lane_value(inc, kWave - 1);
-  s.length = a.part_tiles ? 1 : (s.total + a.ranges - 1) / a.ranges;
+  s.length = (s.total + a.ranges - 1) / a.ranges;
   return s;
 }
 // The work of request i: from the lanes where they hold one request each.
@@ -155,7 +151,6 @@ __device__ __forceinline__ Work work_at(const AttendArgs& a, const Stream& s, in
   w.len = lane_value(s.own.len, i);
   w.tiles = lane_value(s.own.tiles, i);
   w.n = lane_value(s.own.n, i);
-  w.parts = lane_value(s.own.parts, i);
   return w;
 }
 __device__ __forceinline__ Request request_with(const Work& w, int32_t i) {
@@ -215,6 +210,11 @@ struct Scratch {
 //
 // kWholePages: pages hold 16 slots or more, so 16 tokens lie in one page and its address is a scalar; smaller
 // pages take an address per token.
+//
+// The waves of a workgroup take every fourth tile of 32 tokens, keys and values loaded a tile ahead, and join their sums
+// at the end.  Bound by the reads of the cache: 64 requests of K in 0..8 on 4096 to 8192 tokens (window 4096, 8 heads of
+// 128, bf16) 218 us, 5.0 TB/s of 1.08 GB, with the second tile of requests of more than 32 columns read again.  Small
+// batches are bound by the latency of a tile (loads, two products, the exponentials between): 0.3 us each wave's.
 template <class E, int D, int QB, int kWaves, bool kWholePages>
 __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, QB, kWaves>& sh, const TileOf& at,
                                             int32_t len, int32_t head, bool pos_all, int32_t w_lo, int32_t w_hi, int64_t slot) {
@@ -617,22 +617,21 @@ __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void at
   int64_t base = (int64_t)lane_value((uint64_t)s.before, who);
   while (p < end && i < a.B) {
     const Work w = work_at(a, s, i, kColumns);
-    const int64_t items = w.units(a) * w.parts;
+    const int64_t items = w.units(a) * w.n;
     if (p >= base + items) {
       base += items;
       ++i;
       continue;
     }
-    const uint32_t unit = (uint32_t)((p - base) / w.parts);
-    const int32_t q_lo = (int32_t)(p - base - unit * w.parts);
-    const int32_t q_hi = q_lo + (end - p) < w.parts ? (int32_t)(q_lo + (end - p)) : w.parts;
+    const uint32_t unit = (uint32_t)((p - base) / w.n);
+    const int32_t q_lo = (int32_t)(p - base - (int64_t)unit * w.n);
+    const int32_t q_hi = q_lo + (end - p) < w.n ? (int32_t)(q_lo + (end - p)) : w.n;
     TileOf at;
     at.r = request_with(w, i);
     at.c0 = (int32_t)(unit / (uint32_t)a.cache.n_heads) * kColumns;
-    const bool first = q_lo == 0, whole = first && q_hi == w.parts;
+    const bool first = q_lo == 0, whole = first && q_hi == w.n;
     attend_unit<E, D, QB, kStreamWaves, true>(a, sh, at, w.len, (int32_t)(unit % (uint32_t)a.cache.n_heads), true,
-                                              (int32_t)((int64_t)w.n * q_lo / w.parts),
-                                              (int32_t)((int64_t)w.n * q_hi / w.parts),
+                                              q_lo, q_hi,
                                               whole ? -1 : 2 * range + (first ? 1 : 0));
     p += q_hi - q_lo;
     __syncthreads();
@@ -663,11 +662,11 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
     w = work_at(a, s, i, kColumns);
     if (unit < w.units(a)) break;
     unit -= w.units(a);
-    begin += w.units(a) * w.parts;
+    begin += w.units(a) * w.n;
   }
-  begin += unit * w.parts;
+  begin += unit * w.n;
   const int64_t r_lo = begin / s.length;
-  const int32_t pieces = (int32_t)((begin + w.parts - 1) / s.length - r_lo) + 1;
+  const int32_t pieces = (int32_t)((begin + w.n - 1) / s.length - r_lo) + 1;
   if (pieces == 1) return;
   const Request r = request_with(w, i);
   const int32_t head = (uint32_t)unit % (uint32_t)a.cache.n_heads;
@@ -741,11 +740,14 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
   }
 }
 
-// Many rows per request (prompts), bf16, linear: products bound the call.  A workgroup takes 128 columns, a
+// Many rows per request (prompts), bf16, linear: products bound the call (16 x 2501 rows on 4000 tokens 1024 TF/s, as a
+// large library product; under a window of 1024 676 TF/s, where the 8 to 10 us in which a workgroup finds its pages, loads its
+// queries and stores its results weigh, and tiles at the window's ends are cut).  A workgroup takes 128 columns, a
 // wave 32 of them, and the waves share the keys and values of 64 tokens through shared memory, where direct loads
 // put the next 64 meanwhile.  Matrix instructions of 32 x 32 x 16; per tile and wave 32 of them (1024
-// cycles at D = 128) against 32 KiB of shared-memory reads, so two waves per SIMD keep both busy, one's
-// softmax under the other's products.
+// cycles at D = 128) against 32 KiB of shared-memory reads.  The scores of the next tile are computed between the
+// exponentials of this one, whose cycles they fill: without, two waves per SIMD wait for each other (954 TF/s at
+// the same shape).
 //
 // A row of a tile keeps its 16-byte pieces in the order p ^ 2 (token mod 8) (for D = 64, of 8 pieces, p ^ 2 (token
 // / 2 mod 4)): the 32 rows that a key read takes, and the 8 that a transposing value read takes, then lie in
@@ -1089,15 +1091,35 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
 
 enum Mode { kUnits, kRanges, kSmallPages, kRows };
 
-constexpr int64_t kManyColumns = 96;
+// The rules, by the batch's means; times of 8 heads, D = 128, bf16, for one side and the other.
+//
+// attend_rows from this many columns of a request (its rows times the heads of a group) and this many workgroups on: 64
+// requests of 96 columns on 4000 tokens 258 us for 552, 16 of 128 on 1000 29 for 36, of 64 on 4000 260 for
+// 227; one request of 512 on 4000 (32 workgroups) 87 for 55.
+constexpr int64_t kManyColumns = 96, kManyWorkgroups = 128;
 
-// Two workgroups per compute unit.
+// Ranges for units of more token tiles than this: one request on 1000 tokens 14 us either way, on 4000 17 for 42 by
+// units; 16 requests (128 units) 52 for 50.  With this many units, of more than twice that: 16 trees of binary32 on 1045
+// tokens 54 us by ranges, 25 by units.
+constexpr int64_t kShort = 32, kSomeUnits = 64;
+
+// Units, however long, from this many on: their rounds are even enough (256 requests on 1000 tokens 200 us for 224
+// by ranges).
+constexpr int64_t kManyUnits = 2048;
+
+// Units of 16 columns up to which they are not paired (4 requests of 64 columns on 1000 tokens 16.3 us for 19.4 in
+// pairs; 16 of 32 columns, 256 units, 25.4 for 20.2).  Binary32 units never are (16 of 52 columns 25 us for 35.5): the
+// binary32 matrix instructions set their time, which a pair doubles.  Ranges are in pairs: they read the cache
+// again for each column tile (16 of 48 columns on 4000 tokens 126 us for 58).
+constexpr int64_t kFewUnits = 128;
+
+// Workgroups at once: two per compute unit.
 constexpr int64_t kPlaces = 512;
 
 struct Plan {
   int qb;
   Mode mode;
-  int32_t ranges, part_tiles;
+  int32_t ranges;
   int32_t pieces;  // of a unit, about
   int64_t tiles;
   size_t part_bytes, bytes;
@@ -1108,41 +1130,29 @@ inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int32_t window, int32_t sinks,
                     bool tree) {
   const int64_t G = n_q / c->n_kv_heads, rows = n_d + B, mean = (rows * G + B - 1) / B;
-  Plan p;
-  p.qb = mean <= 16 || (c->dtype == SDV_FP32 && c->head_dim > 64) ? 1 : 2;
-  if (mean > 48 && c->dtype == SDV_BF16 && c->head_dim <= 128) p.qb = 4;
-  const int64_t columns = 16 * p.qb;
-  p.tiles = rows * G / columns + B;
-  const int64_t units = (rows * G / columns > B ? rows * G / columns : B) * c->n_kv_heads;
   int64_t seen = (int64_t)c->max_pages * c->page_size;
   if (window && (int64_t)window + sinks + rows / B < seen) seen = (int64_t)window + sinks + rows / B;
-  const bool many_rows =
-      !tree && c->dtype == SDV_BF16 && c->head_dim <= 128 && c->page_size >= 16 && mean >= kManyColumns;
-  p.mode = kUnits;
-  if (many_rows) {
+  const int64_t tokens = (seen + kTile - 1) / kTile;
+  auto units_of = [&](int64_t columns) { return (mean + columns - 1) / columns * B * c->n_kv_heads; };
+  Plan p = {};
+  p.qb = 1;
+  if (!tree && c->dtype == SDV_BF16 && c->head_dim <= 128 && c->page_size >= 16 && mean >= kManyColumns &&
+      units_of(kRowsColumns) >= kManyWorkgroups) {
     p.mode = kRows;
     p.tiles = rows * G / kRowsColumns + B;
+    return p;
   }
-  p.ranges = p.part_tiles = p.pieces = 0;
-  p.part_bytes = p.bytes = 0;
-  if (many_rows) return p;
-  if (c->page_size < 16) {
-    p.mode = kSmallPages;
-    if (p.qb > 2) p.qb = 2;
-    p.tiles = rows * G / (16 * p.qb) + B;
-  } else if (B <= 512 && rows <= 64 * (int64_t)B && units <= 4096 && seen > kStreamWaves * kTile) {
-    p.mode = kRanges;
-    const int64_t tokens = (seen + kTile - 1) / kTile;
-    if (units * tokens >= kPlaces * kStreamWaves * 8) {
-      p.ranges = kPlaces;
-      p.pieces = (int32_t)((kPlaces + units - 1) / units) + 1;
-    } else {  // a part per place, of a tile per wave at least
-      const int64_t part = (units * tokens + kPlaces - 1) / kPlaces;
-      p.part_tiles = part < kStreamWaves ? kStreamWaves : (int32_t)part;
-      p.pieces = (int32_t)((tokens + p.part_tiles) / p.part_tiles);
-      p.ranges = (int32_t)(p.tiles * c->n_kv_heads * p.pieces);
-    }
-    const size_t n = (size_t)2 * p.ranges * columns;
+  const bool pairs = mean > 16 && !(c->dtype == SDV_FP32 && c->head_dim > 64);
+  const bool split = tokens > (units_of(16) < kSomeUnits ? kShort : 2 * kShort) && B <= 512 &&
+                     rows <= 64 * (int64_t)B && units_of(32) < kManyUnits;
+  p.mode = c->page_size < 16 ? kSmallPages : (split ? kRanges : kUnits);
+  if (pairs && (p.mode == kRanges || (c->dtype == SDV_BF16 && units_of(16) > kFewUnits))) p.qb = 2;
+  p.tiles = rows * G / (16 * p.qb) + B;
+  if (p.mode == kRanges) {
+    const int64_t units = units_of(16 * p.qb), groups = (units * tokens + kStreamWaves - 1) / kStreamWaves;
+    p.ranges = (int32_t)(groups < kPlaces ? groups : kPlaces);
+    p.pieces = (int32_t)((p.ranges + units - 1) / units) + 1;
+    const size_t n = (size_t)2 * p.ranges * 16 * p.qb;
     p.part_bytes = up256(n * c->head_dim * 4);
     p.bytes = p.part_bytes + up256(n * 8);
   }
@@ -1151,40 +1161,33 @@ inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int
 
 template <class E, int D, int QB>
 int launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
-  const Mode mode = p.mode;
-  const dim3 units((unsigned)(a.tiles * a.cache.n_heads));
-  if (mode == kRows) {
-    if constexpr (E::kBytes == 2 && D <= 128 && QB == 4)
-      hipLaunchKernelGGL((attend_rows<D>), units, dim3(kRowsWaves * kWave), 0, s, a);
-    return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
-  }
-  if (mode == kSmallPages) {
-    if constexpr (QB <= 2) hipLaunchKernelGGL((attend_units<E, D, QB, 4, false>), units, dim3(4 * kWave), 0, s, a);
-    return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
-  }
-  if (mode == kRanges) {
-    hipLaunchKernelGGL((attend_ranges<E, D, QB>), dim3((unsigned)a.ranges), dim3(kStreamWaves * kWave), 0, s, a);
+  const dim3 units((unsigned)(a.tiles * a.cache.n_heads)), threads(kStreamWaves * kWave);
+  if (p.mode == kSmallPages) {
+    hipLaunchKernelGGL((attend_units<E, D, QB, kStreamWaves, false>), units, threads, 0, s, a);
+  } else if (p.mode == kUnits) {
+    hipLaunchKernelGGL((attend_units<E, D, QB, kStreamWaves, true>), units, threads, 0, s, a);
+  } else {
+    hipLaunchKernelGGL((attend_ranges<E, D, QB>), dim3((unsigned)a.ranges), threads, 0, s, a);
     if (p.pieces > 16)
       hipLaunchKernelGGL((join<E, D, QB, true>), dim3(units.x, 16 * QB), dim3(kJoinWaves * kWave), 0, s, a);
     else
       hipLaunchKernelGGL((join<E, D, QB, false>), dim3(units.x, 16 * QB / kJoin), dim3(kJoinWaves * kWave), 0, s, a);
-  } else {
-    hipLaunchKernelGGL((attend_units<E, D, QB, 4, true>), units, dim3(4 * kWave), 0, s, a);
   }
   return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
 }
 
 template <class E, int D>
 int launch_columns(const AttendArgs& a, const Plan& p, hipStream_t s) {
-  if constexpr (E::kBytes == 4 && D > 64) {
-    return launch<E, D, 1>(a, p, s);
-  } else {
-    if (p.qb == 1) return launch<E, D, 1>(a, p, s);
-    if constexpr (E::kBytes == 2 && D <= 128) {
-      if (p.qb == 4) return launch<E, D, 4>(a, p, s);
+  if constexpr (E::kBytes == 2 && D <= 128) {
+    if (p.mode == kRows) {
+      hipLaunchKernelGGL((attend_rows<D>), dim3((unsigned)(a.tiles * a.cache.n_heads)), dim3(kRowsWaves * kWave), 0, s, a);
+      return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
     }
-    return launch<E, D, 2>(a, p, s);
   }
+  if constexpr (E::kBytes == 2 || D <= 64) {
+    if (p.qb == 2) return launch<E, D, 2>(a, p, s);
+  }
+  return launch<E, D, 1>(a, p, s);
 }
 
 template <class E>
@@ -1232,7 +1235,6 @@ extern "C" int sdv_attend(const sdv_cache* cache, int32_t B, int64_t n_draft_row
   a.n_q = n_q_heads;
   a.G = n_q_heads / cache->n_kv_heads;
   a.ranges = p.ranges;
-  a.part_tiles = p.part_tiles;
   a.window = window;
   a.sinks = sinks;
   a.n_d = n_draft_rows;

@@ -257,8 +257,9 @@ __device__ __forceinline__ int64_t slot_of(const Args& a, int64_t row) {
 
 constexpr double kLog2e = 0x1.71547652b82fep0;
 
-// The row pass: 17 instructions of binary64 arithmetic per logit of a row whose weights are all
-// needed, about the time the loads take; a row that only needs its maximum is bound by the loads.
+// The row pass: 17 instructions of binary64 arithmetic per logit of a row whose weights are all needed take about 16 us
+// for 256 x 128256, the loads 11: together 25 us (2.6 TB/s).  A row that only needs its maximum is bound by the
+// loads.
 template <class E, int kVpl>
 __global__ __launch_bounds__(kStatsWaves* kWave) void row_stats(Args a) {
   const int lane = threadIdx.x & (kWave - 1);
@@ -1104,6 +1105,9 @@ __device__ __forceinline__ double draw(const Args& a, const Source& source, Shar
   return S;
 }
 
+// The rest of a row: two passes over it where it is cut (counts, then the kept masses; from the last-level cache, 512 x
+// 151936 105 us, of which shared-memory atomics and the gathering of kept logits take most), none where it is not (256 x
+// 128256 8.5 us, the latency of the fold, the search of one chunk and its barriers).
 template <class E, int kVpl, bool kCut>
 __global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
   constexpr int kWaves = kDrawThreads / kWave, P = E::kPerVec;
@@ -1200,7 +1204,9 @@ __global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
   if (a.probs && t == 0) a.state[row] = state_of(slot, base, k2, S, cut, eq_last);
 }
 
-// A row of at most kThreads x kVecs vectors, in one launch: it stays in shared memory.
+// A row of at most kThreads x kVecs vectors, in one launch: it stays in shared memory, read from memory once.  Bound by
+// the latency of its passes one after another (64 rows of 32000 under every truncation 31 us, where reading the
+// rows and writing the probabilities takes 2.5; one plain row of 1000 4 us).
 template <class E, int kThreads, int kVecs, bool kCut>
 __global__ __launch_bounds__(kThreads) void row_whole(Args a) {
   constexpr int kWaves = kThreads / kWave, P = E::kPerVec;
@@ -1318,7 +1324,8 @@ __global__ __launch_bounds__(kThreads) void row_whole(Args a) {
 constexpr int kProbThreads = 256;
 
 // The probability rows: a thread reads one vector of logits and writes its P values; on the 16-byte grid of
-// both as whole vectors.
+// both as whole vectors.  Bound by memory: 512 x 151936 67 to 85 us, 467 MB at 5.5 to 7 TB/s (the logits partly from the
+// last-level cache).
 template <class E>
 __global__ __launch_bounds__(kProbThreads) void row_probs(Args a, int32_t tiles) {
   constexpr int P = E::kPerVec, kTile = kProbThreads * P;
@@ -1352,9 +1359,11 @@ __global__ __launch_bounds__(kProbThreads) void row_probs(Args a, int32_t tiles)
   }
 }
 
-// Units below which the chunks are a quarter as long, so that a small batch spreads over the card.
+// Units below which the chunks are a quarter as long, so that a small batch spreads over the card (rows of 128256: 96 of
+// them 17.3 us for 20.7 in long chunks; one 15.7 for 16.5).  From there on long chunks fill it, and a row has fewer
+// of them to fold.
 constexpr int64_t kFullUnits = 1024;
-constexpr int32_t kMostChunks = 256;  // a wave folds a row's chunks 64 at a time
+constexpr int32_t kMostChunks = 256;  // of short ones: a wave folds a row's chunks 64 at a time
 
 struct Plan {
   int vpl;           // 16 or 4: chunks; 0: the row in one workgroup
@@ -1366,6 +1375,9 @@ struct Plan {
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Chunks of a row of V elements that may begin anywhere in its first 16-byte block.
+// Rows that fit a workgroup's shared memory stay in one: 64 rows of 4000 under every truncation 19.3 us for 29.4 by
+// chunks, of 32000 31.4 for 33.0; one plain row 12.8 for 15.6.  A row of at most 256 vectors takes 256
+// threads (256 rows of 2000: 13.0 us for 13.6 with 1024).
 inline Plan plan_of(int64_t n, int32_t V, int32_t dtype) {
   const int64_t per = dtype == SDV_BF16 ? 8 : 4, vecs = ((int64_t)V + 2 * per - 2) / per;
   Plan p = {};
