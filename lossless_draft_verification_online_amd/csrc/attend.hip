@@ -741,8 +741,8 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
 }
 
 // Many rows per request (prompts), bf16, linear: products bound the call (16 x 2501 rows on 4000 tokens 1024 TF/s, as a
-// large library product; under a window of 1024 676 TF/s, where the 8 to 10 us in which a workgroup finds its pages, loads its
-// queries and stores its results weigh, and tiles at the window's ends are cut).  A workgroup takes 128 columns, a
+// large library product; under a window of 1024 676 TF/s, where the 8 to 10 us in which a workgroup finds its pages,
+// loads its queries and stores its results weigh, and tiles at the window's ends are cut).  A workgroup takes 128 columns, a
 // wave 32 of them, and the waves share the keys and values of 64 tokens through shared memory, where direct loads
 // put the next 64 meanwhile.  Matrix instructions of 32 x 32 x 16; per tile and wave 32 of them (1024
 // cycles at D = 128) against 32 KiB of shared-memory reads.  The scores of the next tile are computed between the
@@ -1022,7 +1022,7 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
       for (int d = 0; d < kDB; ++d) {
         acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
             __builtin_shufflevector(vf[s & 1][d][0], vf[s & 1][d][1], 0, 1, 2, 3, 4, 5, 6, 7), p[s], acc[d], 0, 0, 0);
-        if (d == 0 && s < 3) {  // behind the first product, which waits for this step's: counts of such reads in flight are not told apart
+        if (d == 0 && s < 3) {  // the next step's, under the rest of this one
           __builtin_amdgcn_sched_barrier(0);
           value(v_s, s + 1, vf[(s + 1) & 1]);
           __builtin_amdgcn_sched_barrier(0);
