@@ -566,14 +566,15 @@ int sdv_kv_append(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, const
  *   s < L_i, or s is the slot of j itself or of one of its ancestors (every row before it in a
  *   linear draft, the path to row 0 in a tree); and
  *   window == 0, or position(j) - position(s) < window, or s < sinks (the first tokens stay visible).
- * out[r][h] = sum_s softmax_s(scale * <q, k_s>) v_s, zeros for a row that sees nothing.
+ * out[r][h] = sum_s softmax_s(scale * <q, k_s>) v_s, zeros for a row that sees nothing.  Keys and values of slots
+ * that a row does not see do not reach it, whatever they hold.
  *   queries [n_draft_rows + B][n_q_heads][head_dim], rows query_stride elements apart, 16-byte aligned;
- *   out     [n_draft_rows + B][n_q_heads][head_dim] contiguous, 16-byte aligned
+ *   out     [n_draft_rows + B][n_q_heads][head_dim] contiguous, 16-byte aligned, apart from every input
  * Scores, statistics and sums are binary32; with bf16 the probabilities are rounded to bf16 for their
  * product with the values (relative 2^-8 each).  The same call gives the same bits.
  * workspace: sdv_attend_workspace_bytes(...), 16-byte aligned, not initialised.
- * Errors as sdv_kv_append, plus n_q_heads not a multiple of n_kv_heads, window < 0, sinks < 0 or a
- * scale that is not finite -> SDV_ERR_INVALID_ARG; more than INT32_MAX - 1024 rows times n_q_heads /
+ * Errors as sdv_kv_append, plus n_q_heads not a multiple of n_kv_heads, window < 0, sinks < 0, out at the
+ * queries' address or a scale that is not finite -> SDV_ERR_INVALID_ARG; more than INT32_MAX - 1024 rows times n_q_heads /
  * n_kv_heads, or more than INT32_MAX units of work -> SDV_ERR_LIMIT; a small workspace ->
  * SDV_ERR_WORKSPACE.
  */

@@ -199,10 +199,63 @@ struct Scratch {
   using S = Shape<E, D, QB, kWaves>;
   __align__(16) char smem[S::kBytes];
   float m_s[kWaves][S::kColumns], l_s[kWaves][S::kColumns];
+  int32_t odd_s[kWaves];
   int32_t parent_s[kWave], depth_s[kMaxNodes + 1];
   uint64_t sight_s[kMaxNodes + 1];
   int32_t last_s[kMaxNodes + 1];
 };
+
+// Values that are not finite, in a tile that not every column sees whole: a column that does not see such a token has
+// the weight 0 for it, and 0 times NaN is NaN.  The tiles' products take 0 in their place, and where there were
+// some, a pass behind the unit adds them to the results of the columns that do see them (an infinity or NaN times a
+// positive weight is itself).
+__device__ __forceinline__ bool not_finite(u32x4 v) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 top = {0, 0};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[w] & 0x7fff7fffu));
+  return top.x >= 0x7f80 || top.y >= 0x7f80;
+}
+__device__ __forceinline__ u32x4 finite_of(u32x4 v) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    if ((v[w] & 0x7f80u) == 0x7f80u) v[w] &= 0xffff0000u;
+    if ((v[w] & 0x7f800000u) == 0x7f800000u) v[w] &= 0xffffu;
+  }
+  return v;
+}
+// One wave, for its columns and the tiles of [lo, hi) that are not all_see(start): add(column, d, value).
+template <class E, int D, int kTokens, class Start, class AllSee, class Sees, class Add>
+__device__ __forceinline__ void add_not_finite(const AttendArgs& a, int32_t i, int32_t head, int32_t lo, int32_t hi,
+                                               int32_t columns, Start start, AllSee all_see, Sees sees, Add add) {
+  const int lane = threadIdx.x & (kWave - 1);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the results are there
+  for (int32_t n = lo; n < hi; ++n) {
+    if (all_see(start(n))) continue;
+    for (int32_t s = start(n); s < start(n) + kTokens; ++s) {
+      const int32_t page = a.cache.page(i, s);
+      if (page < 0) continue;
+      const char* const row = a.cache.values + a.cache.row(page, head, s) * (D * E::kBytes);
+#pragma unroll 1
+      for (int d = lane; d < D; d += kWave) {
+        const float v = E::at(row, d);
+        const bool bad = !(v - v == 0.0f);
+        if (!__any(bad)) continue;
+        for (int32_t c = 0; c < columns; ++c)
+          if (sees(c, s) && bad) add(c, d, v);
+      }
+    }
+  }
+}
+template <class E>
+__device__ __forceinline__ void add_to(char* out, int d, float v) {
+  if constexpr (E::kBytes == 2) {
+    __bf16* const p = reinterpret_cast<__bf16*>(out) + d;
+    *p = (__bf16)((float)*p + v);
+  } else {
+    reinterpret_cast<float*>(out)[d] += v;
+  }
+}
 
 // One unit (a tile of a request's columns, one key/value head), or of its token tiles [w_lo, w_hi) when
 // pos_all (then the tiles are those of all of the request's rows).  slot: where the sums go that another
@@ -305,6 +358,13 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
 #pragma unroll
     for (int d = 0; d < kDB; ++d) acc[b][d] = f32x4{0, 0, 0, 0};
   }
+
+  // every row of the tile's columns sees every token from s0 on that is in a page
+  auto all_see = [&](int32_t s0) {
+    return s0 + kTile <= (a.parents ? len : len + j_lo + 1) &&
+           (a.window == 0 || s0 > far - a.window || s0 + kTile <= a.sinks);
+  };
+  bool odd = false;
 
   char* const v_lds = smem + wave * kTile * S::kValueStride;
   u32x4 kreg[2][kSteps];
@@ -416,15 +476,23 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
         for (int x = 0; x < D / 16; ++x)
           if (!((there >> (x * kRows + lane / kLanes)) & 1)) vreg[x].x = vreg[x].y = vreg[x].z = vreg[x].w = 0;
       }
+      if (!all_see(s0)) {
+        bool bad = false;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) bad |= not_finite(vreg[x]);
+        if (__any(bad)) {
+          odd = true;
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) vreg[x] = finite_of(vreg[x]);
+        }
+      }
 #pragma unroll
       for (int x = 0; x < D / 16; ++x)
         *reinterpret_cast<u32x4*>(v_lds + (x * kRows + lane / kLanes) * S::kValueStride + (lane % kLanes) * 16) = vreg[x];
       if (more) load_values(n + kWaves, page_1);
     }
 
-    // every row sees every token of the tile: no masks
-    const bool whole = paged && s0 + kTile <= (a.parents ? len : len + j_lo + 1) &&
-                       (a.window == 0 || s0 > far - a.window || s0 + kTile <= a.sinks);
+    const bool whole = paged && all_see(s0);  // no masks
     bf16x8 pb[QB];
     float pf[QB][8];
 #pragma unroll
@@ -490,17 +558,35 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
       }
       __builtin_amdgcn_wave_barrier();
     } else {
+      if (!paged) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const bool held_e = (there >> (16 * (e >> 2) + 4 * g + (e & 3))) & 1;
+        for (int e = 0; e < 8; ++e) {
+          const bool held_e = (there >> (16 * (e >> 2) + 4 * g + (e & 3))) & 1;
 #pragma unroll
-        for (int d = 0; d < kDB; ++d) {
-          const float v = held_e ? vf[e][d] : 0.0f;
-#pragma unroll
-          for (int b = 0; b < QB; ++b)
-            acc[b][d] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, pf[b][e], acc[b][d], 0, 0, 0);
+          for (int d = 0; d < kDB; ++d) vf[e][d] = held_e ? vf[e][d] : 0.0f;
         }
       }
+      if (!all_see(s0)) {
+        float none = 0.0f;  // stays 0 over finite values
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+#pragma unroll
+          for (int d = 0; d < kDB; ++d) none = fmaf(vf[e][d], 0.0f, none);
+        if (__any(!(none == 0.0f))) {
+          odd = true;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+#pragma unroll
+            for (int d = 0; d < kDB; ++d) vf[e][d] = vf[e][d] - vf[e][d] == 0.0f ? vf[e][d] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int d = 0; d < kDB; ++d)
+#pragma unroll
+          for (int b = 0; b < QB; ++b)
+            acc[b][d] = __builtin_amdgcn_mfma_f32_16x16x4f32(vf[e][d], pf[b][e], acc[b][d], 0, 0, 0);
       if (more) load_values(n + kWaves, page_1);
     }
     page = page_1;
@@ -508,6 +594,8 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
 
   // the four waves' sums in one frame
   __syncthreads();
+  odd = __any(odd);
+  if (lane == 0) sh.odd_s[wave] = odd;
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
     l[b] = both_sum16_32(l[b]);
@@ -582,6 +670,27 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
         }
       }
     }
+  }
+  for (int w = 1; w < kWaves; ++w) odd |= sh.odd_s[w] != 0;
+  if (odd) {
+    auto row_of = [&](int32_t c) { return (int32_t)((uint32_t)(at.c0 + c) / (uint32_t)a.G); };
+    add_not_finite<E, D, kTile>(
+        a, i, head, w_lo, w_hi, c_last - at.c0 + 1, start, all_see,
+        [&](int32_t c, int32_t s) {
+          const int32_t j = row_of(c), pos_c = len + (a.parents ? depth_s[j] : j);
+          if (a.parents && s >= len) {
+            const int32_t r = s - len;
+            return r < 64 ? ((sight_s[j] >> r) & 1) != 0 : r == 64 && last_s[j] != 0;
+          }
+          return s <= pos_c && (a.window == 0 || s > pos_c - a.window || s < a.sinks);
+        },
+        [&](int32_t c, int d, float v) {
+          const int32_t j = row_of(c), h = head * a.G + (at.c0 + c - j * a.G);
+          if (slot >= 0)
+            a.part[(slot * S::kColumns + c) * D + d] += v;
+          else
+            add_to<E>(a.out + ((at.r.row0 + j) * a.n_q + h) * (D * E::kBytes), d, v);
+        });
   }
 }
 
@@ -900,6 +1009,13 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     for (int e = 0; e < 16; ++e) acc[d][e] = 0.0f;
   float m = -__builtin_inff(), l = 0.0f;
   __shared__ __align__(16) int32_t page_s[2][kRowsWaves];
+  __shared__ int32_t odd_s;
+  if (t == 0) odd_s = 0;
+  const int32_t first_pos = len + (int32_t)((uint32_t)at.c0 / (uint32_t)a.G);
+  const int32_t last_pos = len + (int32_t)((uint32_t)(c_end - 1) / (uint32_t)a.G);
+  auto all_see = [&](int32_t s0) {
+    return s0 + kRowsTile <= first_pos + 1 && (a.window == 0 || s0 > last_pos - a.window || s0 + kRowsTile <= a.sinks);
+  };
 
   typedef f32x16 Scores[2];  // element e of a block: token 8 (e / 4) + 4 half + e mod 4
   const f32x16 none16 = {};
@@ -943,6 +1059,16 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     }
     if (lane == 0) page_s[n & 1][wave] = page;
     __builtin_amdgcn_s_waitcnt(0x0f70);  // this wave's direct loads
+    if (!all_see(s0)) {
+      u32x4* const mine = reinterpret_cast<u32x4*>(v_s + 16 * wave * kLine) + lane;
+      bool bad = false;
+#pragma unroll
+      for (int x = 0; x < kLoads; ++x) bad |= not_finite(mine[64 * x]);
+      if (__any(bad)) {
+        for (int x = 0; x < kLoads; ++x) mine[64 * x] = finite_of(mine[64 * x]);
+        odd_s = 1;
+      }
+    }
     __syncthreads();  // its values and the next keys are there, and every wave is done with the other buffers
     const int4 pages = *reinterpret_cast<const int4*>(page_s[n & 1]);
     bf16x8 kf[kKeys];
@@ -1087,6 +1213,20 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     store(k_0, v_1);
   else
     store(k_1, v_0);
+  if (n_tiles > 0 && odd_s) {
+    const int32_t c_lo = at.c0 + 32 * wave;
+    auto row_of = [&](int32_t x) { return (int32_t)((uint32_t)(c_lo + x) / (uint32_t)a.G); };
+    add_not_finite<Bf16, D, kRowsTile>(
+        a, i, head, 0, n_tiles, c_end - c_lo < 32 ? c_end - c_lo : 32, start, all_see,
+        [&](int32_t x, int32_t s) {
+          const int32_t at_pos = len + row_of(x);
+          return s <= at_pos && (a.window == 0 || s > at_pos - a.window || s < a.sinks);
+        },
+        [&](int32_t x, int d, float v) {
+          const int32_t row = row_of(x), q_head = head * a.G + (c_lo + x - row * a.G);
+          add_to<Bf16>(a.out + ((at.r.row0 + row) * a.n_q + q_head) * kLine, d, v);
+        });
+  }
 }
 
 enum Mode { kUnits, kRanges, kSmallPages, kRows };
@@ -1223,7 +1363,7 @@ extern "C" int sdv_attend(const sdv_cache* cache, int32_t B, int64_t n_draft_row
   rc = check(cache, B, n_draft_rows, n_q_heads, window, sinks);
   if (rc != SDV_OK) return rc;
   const int64_t per = cache->dtype == SDV_BF16 ? 8 : 4;
-  if (!queries || !out || !aligned16(queries) || !aligned16(out) || query_stride % per ||
+  if (!queries || !out || out == queries || !aligned16(queries) || !aligned16(out) || query_stride % per ||
       query_stride < (int64_t)n_q_heads * cache->head_dim || !(scale - scale == 0.0f))
     return SDV_ERR_INVALID_ARG;
   if (query_stride > ((int64_t)1 << 31)) return SDV_ERR_LIMIT;

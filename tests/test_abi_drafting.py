@@ -76,7 +76,7 @@ def _append(lib, cache=None, **kw):
 
 
 def _attend(lib, cache=None, **kw):
-    a = dict(B=3, n_d=5, cu=P, parents=None, q=P, qs=256, n_q=4, scale=1.0, window=0, sinks=0, out=P, ws=None, bytes=0)
+    a = dict(B=3, n_d=5, cu=P, parents=None, q=P, qs=256, n_q=4, scale=1.0, window=0, sinks=0, out=2 * P, ws=None, bytes=0)
     a.update(kw)
     c = _cache(**(cache or {}))
     return lib.sdv_attend(ctypes.byref(c), a["B"], a["n_d"], a["cu"], a["parents"], a["q"], a["qs"], a["n_q"], a["scale"],
@@ -112,7 +112,7 @@ def test_append_invalid(lib, kw):
 
 @pytest.mark.parametrize("kw", [dict(q=None), dict(out=None), dict(q=P + 2), dict(out=P + 2), dict(qs=255), dict(qs=260),
                                 dict(n_q=0), dict(n_q=5), dict(window=-1), dict(sinks=-1), dict(scale=float("nan")),
-                                dict(scale=float("inf"))])
+                                dict(scale=float("inf")), dict(out=P)])
 def test_attend_invalid(lib, kw):
     assert _attend(lib, **kw) == INVALID
 

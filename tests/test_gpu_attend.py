@@ -248,3 +248,53 @@ def test_refusals():
     with pytest.raises(sdv.SdvError):
         sdv.attend(long.q.to(DEV), long.kc.to(DEV), long.vc.to(DEV), table, length, cu,
                    workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("poison", [float("nan"), float("inf")])
+@pytest.mark.parametrize("ks,tree,D,dtype,page,Hq", [
+    ([12, 5, 3], False, 64, "bf16", 16, 2), ([12, 5, 3], False, 128, "bf16", 16, 8), ([12, 5, 3], False, 128, "bf16", 4, 8),
+    ([12, 5, 3], False, 256, "bf16", 32, 4), ([12, 5, 3], False, 64, "fp32", 16, 8), ([12, 5, 3], False, 256, "fp32", 16, 2),
+    ([30, 12, 9], True, 64, "bf16", 16, 8), ([30, 12, 9], True, 64, "fp32", 16, 8),
+    ([200, 150, 260], False, 128, "bf16", 16, 16), ([200, 150, 260], False, 64, "bf16", 64, 16)])
+def test_rows_that_do_not_see_a_value(ks, tree, D, dtype, page, Hq, poison):
+    # a value of one slot that is not finite reaches the rows that see the slot, and no other
+    Hkv = 2 if Hq < 16 else 4
+    b = Batch(ks, [70, 33, 130], Hkv, D, page, dtype, 31, tree=tree, Hq=Hq if Hq < 16 else 64)
+    table, length, cu = b.index_args()
+    window, sinks = 40, 2
+
+    def run():
+        return sdv.attend(b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), table, length, cu, parents=b.tree_arg(), window=window,
+                          sinks=sinks).float().cpu()
+
+    want = run()
+    hit = torch.zeros(b.rows, dtype=torch.bool)
+    for i, row0, K, L, d, see in oracle.requests(b.cu, b.len, b.n_d, b.parents):
+        for slot in (L + K // 2, max(L - 36, sinks)):  # a draft's own, and one that leaves the window on the way
+            place = oracle.place(b.table[i], b.n_pages, page, slot)
+            b.vc[place[0], :, place[1], 3] = poison
+            for j in range(K + 1):
+                position = slot if slot < L else L + d[slot - L]
+                seen = slot < L or slot - L in see[j]
+                hit[row0 + j] |= seen and L + d[j] - position < window
+    out = run()
+    assert hit.any() and not hit.all()
+    assert torch.equal(out[~hit], want[~hit])
+    assert not torch.isfinite(out[hit][..., 3]).any()
+    rest = [k for k in range(D) if k != 3]
+    assert torch.equal(out[hit][..., rest], want[hit][..., rest])
+
+
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "bf16"), (256, "bf16"), (64, "fp32"), (128, "fp32")])
+def test_rows_of_long_caches_that_do_not_see_a_value(D, dtype):
+    b = Batch([12, 5, 30], [1500, 33, 2900], 2, D, 16, dtype, 32, Hq=8)
+    table, length, cu = b.index_args()
+    want = sdv.attend(b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), table, length, cu).float().cpu()
+    hit = torch.zeros(b.rows, dtype=torch.bool)
+    for i, row0, K, L, _, _ in oracle.requests(b.cu, b.len, b.n_d):
+        place = oracle.place(b.table[i], b.n_pages, 16, L + K // 2)
+        b.vc[place[0], :, place[1], 5] = math.nan
+        b.kc[place[0], :, place[1], 7] = math.nan
+        hit[row0 + K // 2:row0 + K + 1] = True
+    out = sdv.attend(b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), table, length, cu).float().cpu()
+    assert torch.equal(out[~hit], want[~hit]) and torch.isnan(out[hit]).all()
