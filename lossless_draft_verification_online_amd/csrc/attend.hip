@@ -266,7 +266,7 @@ __device__ __forceinline__ void add_to(char* out, int d, float v) {
 //
 // The waves of a workgroup take every fourth tile of 32 tokens, keys and values loaded a tile ahead, and join their sums
 // at the end.  Bound by the reads of the cache: 64 requests of K in 0..8 on 4096 to 8192 tokens (window 4096, 8 heads of
-// 128, bf16) 218 us, 5.0 TB/s of 1.08 GB, with the second tile of requests of more than 32 columns read again.  Few units
+// 128, bf16) 220 us, 4.9 TB/s of 1.08 GB, with the second tile of requests of more than 32 columns read again.  Few units
 // are bound by what a compute unit loads (1000 tokens of a head, 512 KB, in about 8 us; 8 waves instead of 4 take as long).
 template <class E, int D, int QB, int kWaves, bool kWholePages>
 __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, QB, kWaves>& sh, const TileOf& at,
@@ -849,8 +849,8 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
   }
 }
 
-// Many rows per request (prompts), bf16, linear: products bound the call (16 x 2501 rows on 4000 tokens 1024 TF/s, as a
-// large library product; under a window of 1024 676 TF/s, where the 8 to 10 us in which a workgroup finds its pages,
+// Many rows per request (prompts), bf16, linear: products bound the call (16 x 2501 rows on 4000 tokens 970 to 1024 TF/s, near
+// a large library product; under a window of 1024 650 TF/s, where the 8 to 10 us in which a workgroup finds its pages,
 // loads its queries and stores its results weigh, and tiles at the window's ends are cut).  A workgroup takes 128 columns, a
 // wave 32 of them, and the waves share the keys and values of 64 tokens through shared memory, where direct loads
 // put the next 64 meanwhile.  Matrix instructions of 32 x 32 x 16; per tile and wave 32 of them (1024
