@@ -83,6 +83,56 @@ def test_prompts_of_few_tiles(length, D):
     check(Batch([27, 31, 33], [length, length + 37, length + 64], 2, D, 16, "bf16", length, Hq=8), "bf16")
 
 
+# Batches of 128 workgroups of 128 columns and more, which the prompts' kernel takes.
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("length", [0, 1, 29, 64, 128, 129])
+def test_many_heads_of_few_tiles(length, D):
+    check(Batch([27, 31, 33], [length, length + 37, length + 64], 48, D, 16, "bf16", length, Hq=192), "bf16")
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 3), (64, 0), (100, 40), (90, 200), (5000, 3)])
+def test_many_heads_under_windows(window, sinks):
+    check(Batch([127, 300, 64], [33, 500, 0], 4, 128, 16, "bf16", window, Hq=32), "bf16", window, sinks)
+    b = Batch([127, 300, 64], [33, 500, 0], 8, 64, 64, "bf16", window, Hq=32)
+    b.table[1, 2:4] = [-1, b.n_pages]  # pages that are missing
+    check(b, "bf16", window, sinks, scale=-0.2)
+
+
+def test_what_no_row_of_many_heads_sees_may_hold_anything():
+    b = Batch([200, 100], [300, 9], 16, 128, 16, "bf16", 20, Hq=128)
+    window, sinks = 64, 3
+    args = b.index_args()
+
+    def run(length):
+        return sdv.attend(b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), args[0], length, args[2], window=window, sinks=sinks)
+
+    want = check(b, "bf16", window, sinks)
+    seen = np.zeros((b.n_pages, 16), dtype=bool)
+    for i, _, K, L, _, _ in oracle.requests(b.cu, b.len, b.n_d):
+        for s in range(L + K + 1):
+            if s < sinks or s > L - window:
+                seen[oracle.place(b.table[i], b.n_pages, 16, s)] = True
+    for c in (b.kc, b.vc):
+        c[torch.from_numpy(~seen)[:, None, :, None].expand(c.shape)] = float("nan")
+    assert torch.equal(run(args[1]), want)
+    b.len[0] = -1
+    out = run(torch.from_numpy(b.len).to(DEV))
+    assert not out[:201].any() and torch.equal(out[201:], want[201:])
+
+
+def test_many_heads_with_offsets_that_are_not_valid():
+    b = Batch([100, 130, 100], [30, 0, 70], 16, 64, 16, "bf16", 23, Hq=128)
+    table, length, cu = b.index_args()
+    q, kc, vc = b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV)
+    want = sdv.attend(q, kc, vc, table, length, cu)
+    for bad in ([0, 100, 230, 331], [0, 100, 90, 330], [0, -5, 230, 330], [400, 300, 200, 100], [-1, -1, -1, -1],
+                [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 5]):
+        out = torch.full(q.shape, 5.0, dtype=torch.bfloat16, device=DEV)
+        sdv.attend(q, kc, vc, table, length, torch.tensor(bad, dtype=torch.int32, device=DEV), out=out)
+        if bad[:3] == [0, 100, 230]:  # the requests before are as they were
+            assert torch.equal(out[:232], want[:232]) and (out[232:] == 5.0).all()
+
+
 def test_prompts_of_many_requests():
     ks = [(5 * i) % 40 for i in range(150)]
     b = Batch(ks, [(7 * i) % 90 for i in range(150)], 1, 64, 16, "bf16", 22, Hq=16)
@@ -298,3 +348,39 @@ def test_rows_of_long_caches_that_do_not_see_a_value(D, dtype):
         hit[row0 + K // 2:row0 + K + 1] = True
     out = sdv.attend(b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), table, length, cu).float().cpu()
     assert torch.equal(out[~hit], want[~hit]) and torch.isnan(out[hit]).all()
+
+
+@pytest.mark.parametrize("ks,lens,dtype", [([3, 0, 7], [20, 90, 5], "bf16"), ([3, 0, 7], [20, 90, 5], "fp32"),
+                                           ([3, 0, 7], [20, 1900, 5], "bf16"), ([200, 130, 70], [20, 90, 5], "bf16")])
+def test_rows_behind_the_last_request_stay(ks, lens, dtype):
+    b = Batch(ks, lens, 8, 64, 16, dtype, 40, Hq=64)
+    table, length, cu = b.index_args()
+    want = sdv.attend(b.q.to(DEV), b.kc.to(DEV), b.vc.to(DEV), table, length, cu)
+    q = torch.cat([b.q, b.q[:9]]).to(DEV)
+    out = torch.full(q.shape, 5.0, dtype=DT[dtype], device=DEV)
+    sdv.attend(q, b.kc.to(DEV), b.vc.to(DEV), table, length, cu, out=out)
+    assert (out[b.rows:] == 5.0).all()
+    assert (out[:b.rows].float() - want.float()).abs().max() <= 2.0 ** -7 * want.float().abs().max()
+
+
+@pytest.mark.parametrize("ks,lens,dtype", [([3, 0, 7], [20, 90, 5], "bf16"), ([3, 0, 7], [20, 90, 5], "fp32"),
+                                           ([3, 0, 7], [20, 1900, 5], "bf16"), ([400, 230, 170], [20, 90, 5], "bf16")])
+def test_caches_of_more_than_32_bit_offsets(ks, lens, dtype):
+    b = Batch(ks, lens, 8, 128, 16, dtype, 41, Hq=32)
+    table, length, cu = b.index_args()
+    q = b.q.to(DEV)
+    want = sdv.attend(q, b.kc.to(DEV), b.vc.to(DEV), table, length, cu)
+    page = 8 * 16 * 128 * (2 if dtype == "bf16" else 4)
+    first = (2 ** 32 + 2 ** 31) // page  # pages from 6 GiB on
+    caches = []
+    for c in (b.kc, b.vc):
+        big = torch.empty((first + b.n_pages,) + c.shape[1:], dtype=c.dtype, device=DEV)
+        big[first:] = c.to(DEV)
+        caches.append(big)
+    far = torch.where(table >= 0, table + first, table)
+    assert torch.equal(sdv.attend(q, *caches, far, length, cu), want)
+    k, v = b.k.to(DEV), b.v.to(DEV)
+    near = [b.kc.to(DEV), b.vc.to(DEV)]
+    sdv.kv_append(k, v, *near, table, length, cu)
+    sdv.kv_append(k, v, *caches, far, length, cu)
+    assert torch.equal(caches[0][first:], near[0]) and torch.equal(caches[1][first:], near[1])
