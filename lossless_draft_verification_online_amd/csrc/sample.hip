@@ -1377,7 +1377,8 @@ inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 // Chunks of a row of V elements that may begin anywhere in its first 16-byte block.
 // Rows that fit a workgroup's shared memory stay in one: 64 rows of 4000 under every truncation 19.3 us for 29.4 by
 // chunks, of 32000 31.4 for 33.0; one plain row 12.8 for 15.6.  A row of at most 256 vectors takes 256
-// threads (256 rows of 2000: 13.0 us for 13.6 with 1024).
+// threads (256 rows of 2000: 13.0 us for 13.6 with 1024), and one of at most 1024 no room for more, so that two rows share a
+// compute unit (1024 plain rows of 8000: 21.0 us for 28.7).
 inline Plan plan_of(int64_t n, int32_t V, int32_t dtype) {
   const int64_t per = dtype == SDV_BF16 ? 8 : 4, vecs = ((int64_t)V + 2 * per - 2) / per;
   Plan p = {};
