@@ -846,6 +846,19 @@ __device__ __forceinline__ bool bracket_cut(const Source& source, Shared<kThread
   return true;
 }
 
+// The key of the smallest logit of weight min_p or more: the first of the row's type from m + T ln(min_p) on, which is no
+// further than m.  The border itself, and not a search for it among weights: next to a border near zero lie more
+// logits than the weights' rounding tells apart.
+template <class E>
+__device__ __forceinline__ uint32_t min_p_key(float m, const Profile& f) {
+  const double border = fmax((double)m + f.T * log((double)f.min_p), -(double)__FLT_MAX__);  // every finite logit
+  const float z = (float)border;
+  uint32_t u = __float_as_uint(z);
+  if ((double)z < border) u = z == 0.0f ? 1u : ((u >> 31) ? u - 1 : u + 1);  // the next one up
+  if (E::kBytes == 2) u = (u >> 31) ? u & 0xffff0000u : (u + 0xffffu) & 0xffff0000u;
+  return row_key<E>(__uint_as_float(u));
+}
+
 // The cut of a row's profile.  S: the whole row's mass in the frame (of a row with top-p, without top-k).
 template <class E, int kThreads, class Source>
 __device__ __forceinline__ Cut cut_of(const Source& source, Shared<kThreads>& sh, const Args& a, const Profile& f,
@@ -862,18 +875,8 @@ __device__ __forceinline__ Cut cut_of(const Source& source, Shared<kThreads>& sh
     if (!done) select_cut<E, kThreads>(source, sh, a.V, f, frame, 0.0, -1.0, cut);
   }
   if (f.min_p > 0.0f) {
-    // the smallest key of weight min_p or more lies within rounding of z_max + T ln(min_p)
     __syncthreads();
-    const int lane = threadIdx.x & (kWave - 1);
-    if (threadIdx.x < kWave) {
-      const float z0 = (float)((double)m + f.T * log((double)f.min_p));
-      const int64_t step = E::kBytes == 2 ? 0x10000 : 1;
-      const int64_t k = (int64_t)row_key<E>(z0) + (lane - 32) * step;
-      const bool in = k >= 0 && k <= 0xffffffffll;
-      const bool reach = in && frame.weight(row_key_logit<E>((uint32_t)k)) >= (double)f.min_p;
-      const uint64_t who = __ballot(reach);
-      if (who ? lane == __ffsll((unsigned long long)who) - 1 : lane == 0) sh.key = who ? (uint32_t)k : row_key<E>(m);
-    }
+    if (threadIdx.x == 0) sh.key = min_p_key<E>(m, f);
     __syncthreads();
     if (sh.key > cut.key) {
       cut.key = sh.key;
