@@ -196,6 +196,8 @@ struct NearFrame {
   double k2;
   float lo, hi;
   __device__ NearFrame(double k2_) : k2(k2_), lo((float)(-1100.0 / k2_)), hi((float)(1100.0 / k2_)) {}
+  // Whether binary32 holds the bounds: below its normal numbers their rounding would move them.
+  __device__ bool holds() const { return hi >= 0x1p-126f; }
   __device__ double weight(float z) const { return exp2_of((double)__builtin_amdgcn_fmed3f(z, lo, hi), k2); }
 };
 __device__ __forceinline__ bool near_sum(double s) { return s >= 0x1p-900 && s <= 0x1p1000; }
@@ -257,6 +259,11 @@ __device__ __forceinline__ int64_t slot_of(const Args& a, int64_t row) {
 
 constexpr double kLog2e = 0x1.71547652b82fep0;
 
+// A temperature given as a number is binary64; beyond these bounds the weights no longer change, and 1 / T or 1100 T could leave
+// binary64.  Logits that differ do so by 2^-149 or more, which at T = 2^-160 is a weight of e^-2048, 0 in binary64; and by
+// less than 2^129, which at T = 2^200 is a weight that rounds to 1.
+constexpr double kLeastT = 0x1p-160, kMostT = 0x1p200;
+
 // The row pass: 17 instructions of binary64 arithmetic per logit of a row whose weights are all needed take about 16 us
 // for 256 x 128256, the loads 11: together 25 us (2.6 TB/s).  A row that only needs its maximum is bound by the
 // loads.
@@ -302,9 +309,10 @@ __global__ __launch_bounds__(kStatsWaves* kWave) void row_stats(Args a) {
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
     const NearFrame near(kLog2e / f.T);
-    if (mass && peak)
+    const bool absolute = mass && near.holds();  // else r.s stays 0, and the maximum's frame is taken
+    if (absolute && peak)
       pass(yes, yes, near);
-    else if (mass)
+    else if (absolute)
       pass(yes, no, near);
     else if (peak)
       pass(no, yes, near);
@@ -1464,7 +1472,7 @@ extern "C" int sdv_sample(const void* logits, int64_t n_rows, int64_t row_stride
   a.stride = row_stride;
   a.V = V;
   a.C = p.C;
-  a.T = temperature;
+  a.T = temperature > 0.0 ? fmin(fmax(temperature, kLeastT), kMostT) : 0.0;
   a.temperature = o.temperature;
   a.top_k = o.top_k;
   a.top_p = o.top_p_milli;
