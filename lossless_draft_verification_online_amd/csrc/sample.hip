@@ -1192,9 +1192,14 @@ __global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
 
   const double base = near ? 0.0 : (double)m;
   const Frame frame(base, k2);
-  // a chunk's mass in the row's frame
+  // A chunk's mass in the row's frame; 0 only where none of its tokens has a weight there, since the chunk is searched for the
+  // token: of absolute weights a sum above 2^-1060 of at most 2^13 holds one above 2^-1074.
   const double near_scale = near ? 1.0 : frame.weight(0.0f);
-  auto stats_mass = [&](const Record& r) { return r.far ? (r.s > 0.0 ? r.s * frame.weight(r.m) : 0.0) : r.s * near_scale; };
+  auto stats_mass = [&](const Record& r) {
+    if (r.far) return r.s > 0.0 ? r.s * frame.weight(r.m) : 0.0;
+    const double x = r.s * near_scale;
+    return x > 0x1p-1060 ? x : 0.0;
+  };
   Cut cut;
   cut.key = 0;
   cut.copies = ~0ull;

@@ -149,3 +149,18 @@ def test_long_rows_that_describe_no_draw(dtype):
     tok, prob, cells = check(z, [1.0, .5, .5, .5, -0.1, nan, .5, .5, .5], T, top_k=[0] * 6 + [-1, 0, 5],
                              top_p=[1000] * 7 + [1001, 900], min_p=[0.0] * 8 + [0.1])
     assert (tok[:8] == -1).all() and tok[8] >= 0 and not cells[:8].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_the_lowest_uniform_among_weights_that_vanish(dtype):
+    """u = 0 takes the first token with a weight: logits 749 below the maximum have none in binary64, though the sum of a
+    thousand of them would be above its smallest number."""
+    z = torch.full((2, 40001), -7.0).to(DT[dtype])
+    z[0, 30000:30003] = 742.0
+    z[1, 39000:] = -float("inf")
+    z[1, 20000] = 742.0
+    tok, prob, extra = sdv.sample(place(z), torch.zeros(2, dtype=torch.float64, device=DEV), 1.0, probs=True, out=(
+        torch.full((2,), -7, dtype=torch.int32, device=DEV), torch.full((2,), -7.0, device=DEV)))
+    assert tok.tolist() == [30000, 20000]
+    assert np.allclose(prob.cpu().numpy(), [1 / 3, 1.0], rtol=2.0 ** -23, atol=0)
+    assert extra["kept_tokens"].tolist() == [40001] * 2
