@@ -594,8 +594,9 @@ int sdv_attend(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, const in
  * behind cache->keys / values.  A rejected request (accepted_len -1), one whose offsets are not
  * valid, or whose accepted nodes do not ascend within its tree, moves nothing and keeps new_len = L_i.
  * A move from or to a slot without a page is dropped.  Slots that no accepted node moved to are left
- * as they were.  Errors as sdv_kv_append; n_layers < 1 -> SDV_ERR_INVALID_ARG, more than 65535 layers x
- * heads x 2 -> SDV_ERR_LIMIT.
+ * as they were.  new_len is apart from every input (cache_len is read while it is written).  Errors as
+ * sdv_kv_append; n_layers < 1, or new_len that overlaps cache_len, accepted_len, the offsets, accepted_nodes or the
+ * page table -> SDV_ERR_INVALID_ARG, more than 65535 layers x heads x 2 -> SDV_ERR_LIMIT.
  */
 int sdv_kv_settle(const sdv_cache* cache, int32_t n_layers, int32_t B, int64_t n_draft_rows,
                   const int32_t* ragged_offsets, const int32_t* accepted_len, const int32_t* accepted_nodes,

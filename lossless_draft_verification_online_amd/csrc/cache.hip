@@ -267,6 +267,12 @@ extern "C" int sdv_kv_settle(const sdv_cache* cache, int32_t n_layers, int32_t B
   if (rc != SDV_OK) return rc;
   if (n_layers < 1 || !accepted_len || (n_draft_rows > 0 && !accepted_nodes) || !new_len) return SDV_ERR_INVALID_ARG;
   if ((int64_t)n_layers * cache->n_kv_heads * 2 > 65535) return SDV_ERR_LIMIT;
+  // every workgroup of a request reads these while one of them writes new_len
+  const int64_t word = sizeof(int32_t), own = B * word;
+  if (overlap(new_len, own, cache->cache_len, own) || overlap(new_len, own, accepted_len, own) ||
+      overlap(new_len, own, ragged_offsets, own + word) || overlap(new_len, own, accepted_nodes, n_draft_rows * word) ||
+      overlap(new_len, own, cache->page_table, own * cache->max_pages))
+    return SDV_ERR_INVALID_ARG;
   SettleArgs a;
   a.cache = view_of(cache);
   a.n_d = n_draft_rows;

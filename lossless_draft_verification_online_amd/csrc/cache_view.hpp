@@ -114,6 +114,11 @@ inline int log2_of(int32_t n) {
   return k;
 }
 
+inline bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < (uintptr_t)a_bytes : x - y < (uintptr_t)b_bytes;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Checks what every call over a cache has in common.
