@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import threading
 
 import torch
 
@@ -427,16 +428,18 @@ def _stream(index: int) -> int:
 
 
 def _scratch(nbytes: int, device: torch.device, index: int, stream: int) -> torch.Tensor | None:
-    """Device scratch of a call on the current device: one buffer per stream, which the stream's order protects; or, while
-    a graph is captured, memory of that graph's own (two graphs captured on one stream may be
-    replayed on two)."""
+    """Device scratch of a call on the current device: one buffer per stream and host thread.  A call's kernels hand each
+    other results in it, which the stream's order protects from a later call, and from another thread's only a buffer of its
+    own: the threads' launches on one stream may alternate.  While a graph is captured, memory of that graph's own (two
+    graphs captured on one stream may be replayed on two)."""
     if nbytes == 0:
         return None
     if _CAPTURING():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    ws = _SCRATCH.get((index, stream))
+    key = (index, stream, threading.get_ident())
+    ws = _SCRATCH.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = _SCRATCH[index, stream] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = _SCRATCH[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
     return ws
 
 
