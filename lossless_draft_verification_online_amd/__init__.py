@@ -54,7 +54,8 @@ def _launch_on(dev: torch.device):
 
 
 def _workspace(nbytes: int, device: torch.device) -> torch.Tensor:
-    key = (device.index, torch.cuda.current_stream(device).cuda_stream)
+    """A verification's device scratch: one buffer per stream and host thread (see _scratch)."""
+    key = (device.index, torch.cuda.current_stream(device).cuda_stream, threading.get_ident())
     ws = _WORKSPACE.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)

@@ -61,3 +61,18 @@ def test_attention_and_sampling():
     z, u = place(logits_of(5, 40001, "fp32", 9)), torch.tensor(uniforms(5, 9), device=DEV)
     calls.append(lambda: sdv.sample(z, u, 1.0)[:2])
     run_in_threads(calls)
+
+
+def test_verification():
+    calls = []
+    for k in range(4):
+        K, B, V = 3, 4 + k, 32000
+        target, draft = place(logits_of(B * K + B, V, "bf16", 20 + k)), place(logits_of(B * K, V, "bf16", 30 + k))
+        tok = torch.tensor([(7919 * (k + 1) * n) % V for n in range(B * K)], dtype=torch.int32, device=DEV)
+        cu = torch.arange(0, B * K + 1, K, dtype=torch.int32, device=DEV)
+
+        def call(target=target.contiguous(), draft=draft.contiguous(), tok=tok, cu=cu, k=k):
+            return sdv.verify(target, draft, tok, cu, 1.0, k)[:2]
+
+        calls.append(call)
+    run_in_threads(calls)

@@ -1,5 +1,6 @@
 """Whose device scratch a call takes.  The buffers are made on the CPU here: who gets which is the host's business."""
 import threading
+import types
 
 import pytest
 import torch
@@ -15,7 +16,17 @@ def drafting(monkeypatch):
     return lambda nbytes, stream=7: sdv._scratch(nbytes, CPU, 0, stream)
 
 
-@pytest.fixture(params=[drafting])
+def verification(monkeypatch):
+    monkeypatch.setattr(sdv, "_WORKSPACE", {})
+
+    def take(nbytes, stream=7):
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device: types.SimpleNamespace(cuda_stream=stream))
+        return sdv._workspace(nbytes, CPU)
+
+    return take
+
+
+@pytest.fixture(params=[drafting, verification])
 def take(request, monkeypatch):
     return request.param(monkeypatch)
 
