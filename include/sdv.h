@@ -488,9 +488,10 @@ int sdv_verify_noalloc(const void* target_logits, const void* draft_logits, cons
  * aligned, not initialised; it holds nothing between calls.  Errors: NULL required pointers,
  * n_rows < 1, V < 1, row_stride < V, misaligned logits, a scalar temperature that is negative, NaN
  * or infinite, n_slots < 0 or n_slots != 0 without slots -> SDV_ERR_INVALID_ARG; unknown dtype ->
- * SDV_ERR_UNSUPPORTED; V above INT32_MAX - 64, row_stride above 2^40 or more than INT32_MAX rows, chunks of rows or
- * tiles of probability rows -> SDV_ERR_LIMIT; a workspace that is NULL, small or misaligned ->
- * SDV_ERR_WORKSPACE.
+ * SDV_ERR_UNSUPPORTED; V above INT32_MAX - 64, row_stride above 2^40, or what takes a launch of 2^32 threads or more
+ * (2^22 rows, or 2^24 of at most 256 16-byte vectors; of rows of more than 4096 vectors also 2^26 chunks of 256 or 1024
+ * vectors, or 2^24 tiles of 256 vectors of probability rows) -> SDV_ERR_LIMIT; a workspace that is NULL, small or
+ * misaligned -> SDV_ERR_WORKSPACE.
  */
 typedef struct sdv_sample_options { /* every member may be NULL / 0 */
   const float* temperature;   /* [n_rows], in place of the scalar */
@@ -552,8 +553,8 @@ typedef struct sdv_cache {
  * Two requests must not share a page that either writes.  Errors: NULL required pointers, sizes
  * < 1, an unsupported page_size or head_dim, strides smaller than a row or off the 16-byte grid,
  * misaligned pointers, rotary outside [0, head_dim] or not a multiple of 16, queries without queries_out
- * or n_q_heads -> SDV_ERR_INVALID_ARG; unknown dtype -> SDV_ERR_UNSUPPORTED; more than INT32_MAX
- * rows, or more than 1024 heads of a kind -> SDV_ERR_LIMIT.
+ * or n_q_heads -> SDV_ERR_INVALID_ARG; unknown dtype -> SDV_ERR_UNSUPPORTED; 2^24 rows or more (a launch
+ * holds fewer than 2^32 threads), strides above 2^31 or more than 1024 heads of a kind -> SDV_ERR_LIMIT.
  */
 int sdv_kv_append(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, const int32_t* ragged_offsets,
                   const int32_t* parents, const void* keys, int64_t key_stride, const void* values,
@@ -574,9 +575,9 @@ int sdv_kv_append(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, const
  * product with the values (relative 2^-8 each).  The same call gives the same bits.
  * workspace: sdv_attend_workspace_bytes(...), 16-byte aligned, not initialised.
  * Errors as sdv_kv_append, plus n_q_heads not a multiple of n_kv_heads, window < 0, sinks < 0, out at the
- * queries' address or a scale that is not finite -> SDV_ERR_INVALID_ARG; more than INT32_MAX - 1024 rows times n_q_heads /
- * n_kv_heads, or more than INT32_MAX units of work -> SDV_ERR_LIMIT; a small workspace ->
- * SDV_ERR_WORKSPACE.
+ * queries' address or a scale that is not finite -> SDV_ERR_INVALID_ARG; more than INT32_MAX - 1024 rows, or rows times
+ * n_q_heads / n_kv_heads, or 2^24 workgroups or more, each a tile of 16 to 128 of those on one key/value head
+ * -> SDV_ERR_LIMIT; a small workspace -> SDV_ERR_WORKSPACE.
  */
 size_t sdv_attend_workspace_bytes(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, int32_t n_q_heads,
                                   int32_t window, int32_t sinks);
@@ -596,7 +597,7 @@ int sdv_attend(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, const in
  * A move from or to a slot without a page is dropped.  Slots that no accepted node moved to are left
  * as they were.  new_len is apart from every input (cache_len is read while it is written).  Errors as
  * sdv_kv_append; n_layers < 1, or new_len that overlaps cache_len, accepted_len, the offsets, accepted_nodes or the
- * page table -> SDV_ERR_INVALID_ARG, more than 65535 layers x heads x 2 -> SDV_ERR_LIMIT.
+ * page table -> SDV_ERR_INVALID_ARG; more than 65535 layers x heads x 2, or 2^24 requests or more -> SDV_ERR_LIMIT.
  */
 int sdv_kv_settle(const sdv_cache* cache, int32_t n_layers, int32_t B, int64_t n_draft_rows,
                   const int32_t* ragged_offsets, const int32_t* accepted_len, const int32_t* accepted_nodes,

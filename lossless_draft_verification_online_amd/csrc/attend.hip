@@ -1368,6 +1368,8 @@ extern "C" int sdv_attend(const sdv_cache* cache, int32_t B, int64_t n_draft_row
     return SDV_ERR_INVALID_ARG;
   if (query_stride > ((int64_t)1 << 31)) return SDV_ERR_LIMIT;
   const Plan p = plan_of(cache, B, n_draft_rows, n_q_heads, window, sinks, parents != nullptr);
+  static_assert(kStreamWaves == kRowsWaves && kStreamWaves == kJoinWaves, "one bound for every launch");
+  if (too_many(p.tiles * cache->n_kv_heads, kStreamWaves * kWave)) return SDV_ERR_LIMIT;
   if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return SDV_ERR_WORKSPACE;
   AttendArgs a;
   a.cache = view_of(cache);

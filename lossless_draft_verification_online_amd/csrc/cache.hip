@@ -223,7 +223,7 @@ extern "C" int sdv_kv_append(const sdv_cache* cache, int32_t B, int64_t n_draft_
       (!aligned16(queries) || !aligned16(queries_out) || query_stride < q_row || query_stride % per ||
        (queries == queries_out && query_stride != q_row)))
     return SDV_ERR_INVALID_ARG;
-  if (n_q_heads > 1024 || key_stride > ((int64_t)1 << 31) || value_stride > ((int64_t)1 << 31) ||
+  if (too_many(n_draft_rows + B, kThreads) || n_q_heads > 1024 || key_stride > ((int64_t)1 << 31) || value_stride > ((int64_t)1 << 31) ||
       query_stride > ((int64_t)1 << 31))
     return SDV_ERR_LIMIT;
   AppendArgs a;
@@ -266,7 +266,7 @@ extern "C" int sdv_kv_settle(const sdv_cache* cache, int32_t n_layers, int32_t B
   const int rc = check_cache(cache, B, n_draft_rows, ragged_offsets);
   if (rc != SDV_OK) return rc;
   if (n_layers < 1 || !accepted_len || (n_draft_rows > 0 && !accepted_nodes) || !new_len) return SDV_ERR_INVALID_ARG;
-  if ((int64_t)n_layers * cache->n_kv_heads * 2 > 65535) return SDV_ERR_LIMIT;
+  if ((int64_t)n_layers * cache->n_kv_heads * 2 > 65535 || too_many(B, kThreads)) return SDV_ERR_LIMIT;
   // every workgroup of a request reads these while one of them writes new_len
   const int64_t word = sizeof(int32_t), own = B * word;
   if (overlap(new_len, own, cache->cache_len, own) || overlap(new_len, own, accepted_len, own) ||

@@ -1470,6 +1470,11 @@ extern "C" int sdv_sample(const void* logits, int64_t n_rows, int64_t row_stride
   if (n_rows > INT32_MAX || V > INT32_MAX - 64 || row_stride > ((int64_t)1 << 40) ||
       n_rows * p.C > (int64_t)INT32_MAX || (o.probs && n_rows * prob_tiles<F32>(V) > INT32_MAX))
     return SDV_ERR_LIMIT;
+  if (p.vpl > 0 ? too_many(n_rows, kDrawThreads) ||
+                      too_many((n_rows * p.C + kStatsWaves - 1) / kStatsWaves, kStatsWaves * kWave) ||
+                      (o.probs && too_many(n_rows * (dtype == SDV_BF16 ? prob_tiles<Bf16>(V) : prob_tiles<F32>(V)), kProbThreads))
+                : too_many(n_rows, p.threads))
+    return SDV_ERR_LIMIT;
   if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 || workspace_bytes < p.bytes) return SDV_ERR_WORKSPACE;
   Args a = {};
   a.logits = logits;
