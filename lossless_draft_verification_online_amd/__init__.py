@@ -422,6 +422,7 @@ def repad(offsets: torch.Tensor, accepted_len: torch.Tensor, out_tokens: torch.T
 _GET_DEVICE = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _CAPTURING = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
 _SCRATCH: dict = {}
+_INT32_MAX = 2 ** 31 - 1
 
 
 def _stream(index: int) -> int:
@@ -450,6 +451,11 @@ def _vector(t, dtype, n: int, index: int, name: str) -> int:
             and t.is_contiguous():
         return t.data_ptr()
     raise ValueError(f"{name} must be a contiguous {dtype} vector of {n} values on the call's device")
+
+
+def _int32(n: int) -> int:
+    """n for a 32-bit argument: ctypes would take its lower bits."""
+    return n if -_INT32_MAX <= n <= _INT32_MAX else (_INT32_MAX if n > 0 else -_INT32_MAX)
 
 
 def _on(index: int, call):
@@ -526,8 +532,8 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, *, top_
     def call(stream):
         ws = workspace
         if ws is None:
-            ws = _scratch(lib.sdv_sample_workspace_bytes(n, V, dt), dev, index, stream)
-        return lib.sdv_sample(logits.data_ptr(), n, stride if n > 1 else V, V, dt, float(temperature), p_u,
+            ws = _scratch(lib.sdv_sample_workspace_bytes(n, _int32(V), dt), dev, index, stream)
+        return lib.sdv_sample(logits.data_ptr(), n, stride if n > 1 else V, _int32(V), dt, float(temperature), p_u,
                               ctypes.byref(opt), p_tokens, p_prob, _ptr(ws),
                               0 if ws is None else ws.numel() * ws.element_size(), stream)
 
@@ -560,6 +566,8 @@ def _cache(key_cache, value_cache, page_table, cache_len, offsets, layers=False)
             or not page_table.is_contiguous():
         raise ValueError("page_table must be a contiguous int32 [B, max_pages] tensor on the cache's device")
     n_pages, heads, page_size, head_dim = shape[-4:]
+    if max(B, table[1], heads, page_size, head_dim) > _INT32_MAX:
+        raise ValueError("sizes of the cache beyond 32 bits")
     return (_native.SdvCache(key_cache.data_ptr(), value_cache.data_ptr(), page_table.data_ptr(), p_len, n_pages,
                              table[1], page_size, heads, head_dim, dt), index, B, p_offsets, heads, head_dim)
 
@@ -595,8 +603,8 @@ def kv_append(keys: torch.Tensor, values: torch.Tensor, key_cache: torch.Tensor,
     p_parents = None if parents is None else _vector(parents, torch.int32, rows - B, index, "parents")
     rotary, p_freq = 0, None
     if inv_freq is not None:
-        rotary = 2 * inv_freq.numel()
-        p_freq = _vector(inv_freq, torch.float32, rotary // 2, index, "inv_freq")
+        rotary = _int32(2 * inv_freq.numel())
+        p_freq = _vector(inv_freq, torch.float32, inv_freq.numel(), index, "inv_freq")
     n_q, qs, p_q, p_qo = 0, 0, None, None
     if queries is not None:
         qs = _rows(queries, "queries", rows, None, head_dim, dtype, index)
@@ -642,6 +650,7 @@ def attend(queries: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Te
     lib = _native.lib()
     p_c = ctypes.byref(c)
     scale = head_dim ** -0.5 if scale is None else float(scale)
+    window, sinks = _int32(window), _int32(sinks)  # slots are numbered below 2^31: what is larger sees no more
 
     def call(stream):
         ws = workspace
