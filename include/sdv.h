@@ -522,7 +522,9 @@ int sdv_sample(const void* logits, int64_t n_rows, int64_t row_stride, int32_t V
  * n + 1 (node n) the depth of its parent's row plus 1.
  * A page number outside [0, n_pages) is no page: slots there, and slots beyond max_pages *
  * page_size, are neither written nor seen (a serving engine frees the pages that left a window and
- * leaves -1).  Rows that no request names by valid offsets are left as they were.  A request with
+ * leaves -1).  A request's offsets are valid if 0 <= cu[i] <= cu[i + 1] <= n_draft_rows; one with offsets that are
+ * not is passed over, those beside it are served (of two that name one row or do not lie in their order, any).
+ * Rows that no request names by valid offsets are left as they were.  A request with
  * cache_len outside [0, INT32_MAX - 1024 - K), or of a tree with more than 64 nodes or a parent
  * outside [-1, n - 1], is passed over: sdv_kv_append writes nothing of it, sdv_attend writes zeros
  * for its rows.

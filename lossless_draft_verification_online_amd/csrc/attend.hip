@@ -53,18 +53,34 @@ struct TileOf {
   int32_t c0;  // its first column within the request
 };
 
+// The tile of request r, whose index is -1 if it does not have that one.
 template <int kColumns>
-__device__ __forceinline__ TileOf tile_of(const AttendArgs& a, int64_t tile) {
+__device__ __forceinline__ TileOf tile_in(const AttendArgs& a, const Request& r, int64_t tile) {
   TileOf t;
-  const int32_t i =
-      find_last(a.B, tile, [&](int32_t q) { return first_tile(a.cu, q, a.G, kColumns); });
-  t.r = request_at(a.cu, i, a.n_d);
+  t.r = r;
   t.c0 = 0;
-  if (t.r.index < 0) return t;
-  const int64_t c0 = (tile - first_tile(a.cu, i, a.G, kColumns)) * kColumns;
-  if (c0 >= (int64_t)(t.r.k + 1) * a.G) t.r.index = -1;
+  if (r.index < 0) return t;
+  const int64_t c0 = (tile - first_tile(a.cu, r.index, a.G, kColumns)) * kColumns;
+  if (c0 < 0 || c0 >= (int64_t)(r.k + 1) * a.G) t.r.index = -1;
   t.c0 = (int32_t)c0;
   return t;
+}
+
+// The request of a tile by a look at every one: for batches with offsets that are not valid (as in request_of_row).
+template <int kColumns>
+__device__ __forceinline__ int32_t tile_among(const AttendArgs& a, int64_t tile) {
+  return find_among(a.B, [&](int32_t q) {
+    return tile_in<kColumns>(a, request_at(a.cu, q, a.n_d), tile).r.index >= 0;
+  });
+}
+
+template <int kColumns>
+__device__ __forceinline__ TileOf tile_of(const AttendArgs& a, int64_t tile) {
+  const int32_t i =
+      find_last(a.B, tile, [&](int32_t q) { return first_tile(a.cu, q, a.G, kColumns); });
+  Request r = request_at(a.cu, i, a.n_d);
+  if (__builtin_expect(r.index < 0, 0)) r = request_at(a.cu, tile_among<kColumns>(a, tile), a.n_d);
+  return tile_in<kColumns>(a, r, tile);
 }
 
 // Workgroups go to the 8 XCDs in turn.  Each XCD takes a run of neighbouring units instead: the heads of one page
@@ -905,24 +921,30 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   {
     const int32_t i0 =
         a.B <= kWave ? 0 : find_last(a.B, tile_no, [&](int32_t q) { return first_tile(a.cu, q, a.G, kRowsColumns); });
-    if (i0 < 0) return;
-    const bool in = i0 + lane < a.B;
+    const bool in = i0 >= 0 && i0 + lane < a.B;
     const int32_t mine = in ? i0 + lane : a.B - 1;
     const int32_t lo = a.cu[mine], hi = a.cu[mine + 1], n = a.cache.len[mine];
     const int64_t first = (uint32_t)(lo + mine) * (uint32_t)a.G / (uint32_t)kRowsColumns + mine;  // first_tile
     const uint64_t who = __ballot(in && first <= tile_no);
-    if (!who) return;
-    const int src = a.B <= kWave ? 63 - __builtin_clzll(who) : 0;
+    const int src = who && a.B <= kWave ? 63 - __builtin_clzll(who) : 0;
+    int32_t begin = lane_value(lo, src), behind = lane_value(hi, src);
+    int64_t tile_0 = (int64_t)lane_value((uint64_t)first, src);
     at.r.index = i0 + src;
-    at.r.first = lane_value(lo, src);
-    const int32_t behind = lane_value(hi, src);
-    if (at.r.first < 0 || behind < at.r.first || behind > a.n_d) return;
-    at.r.k = behind - at.r.first;
-    at.r.row0 = (int64_t)at.r.first + at.r.index;
-    const int64_t c0 = (tile_no - (int64_t)lane_value((uint64_t)first, src)) * kRowsColumns;
+    len = lane_value(n, src);
+    if (__builtin_expect(!who || (who & (who + 1)) || begin < 0 || behind < begin || behind > a.n_d, 0)) {
+      at.r.index = tile_among<kRowsColumns>(a, tile_no);  // some offsets are not valid
+      if (at.r.index < 0) return;
+      begin = all(a.cu[at.r.index]);
+      behind = all(a.cu[at.r.index + 1]);
+      tile_0 = all((int32_t)first_tile(a.cu, at.r.index, a.G, kRowsColumns));
+      len = all(a.cache.len[at.r.index]);
+    }
+    at.r.first = begin;
+    at.r.k = behind - begin;
+    at.r.row0 = (int64_t)begin + at.r.index;
+    const int64_t c0 = (tile_no - tile_0) * kRowsColumns;
     if (c0 >= (int64_t)(at.r.k + 1) * a.G) return;
     at.c0 = (int32_t)c0;
-    len = lane_value(n, src);
   }
   const int32_t i = at.r.index;
   const bool ok = len_fits(len, at.r.k);
