@@ -6,7 +6,8 @@
  * sdv_philox4x32_10 is a DEVICE pointer owned by the caller; the library never allocates, frees,
  * copies to the host or synchronizes.  All work is enqueued on the caller's HIP stream and the call
  * returns as soon as it is enqueued.  Calls are stateless and may run concurrently on different
- * streams as long as they use different workspaces and outputs.
+ * streams, or be made by several host threads on one, as long as they use different workspaces and outputs
+ * (a call is several launches, and those of two threads may alternate).
  *
  * Definitions the entry points follow:
  *  - Rule 1 (temperature 0) and Rule 2 (temperature > 0) of "Speculative Decoding Coordination
@@ -478,7 +479,9 @@ int sdv_verify_noalloc(const void* target_logits, const void* draft_logits, cons
  *   tokens [.] int32, prob [.] float   the token and its probability w / S
  *   kept_tokens [.] int32              tokens the row keeps (V when nothing truncates, 1 at T = 0)
  *   probs [.][V] float                 the distribution: w_v / S for the kept tokens, 0 elsewhere
- *                                      (a one-hot row at T = 0)
+ *                                      (a one-hot row at T = 0).  prob is a binary64 quotient rounded
+ *                                      once; a probs cell takes its weight's fraction from the binary32
+ *                                      exponential: within 2^-22 of w / S
  * A NaN logit counts as -inf.  A row without a finite logit or with one of +inf, a temperature that
  * is negative, NaN or infinite, and at T > 0 a negative top_k, a top_p_milli outside [0, 1000], a
  * min_p outside [0, 1] or a uniform outside [0, 1), describe no draw: token -1, prob 0, kept 0 and
@@ -574,7 +577,8 @@ int sdv_kv_append(const sdv_cache* cache, int32_t B, int64_t n_draft_rows, const
  *   queries [n_draft_rows + B][n_q_heads][head_dim], rows query_stride elements apart, 16-byte aligned;
  *   out     [n_draft_rows + B][n_q_heads][head_dim] contiguous, 16-byte aligned, apart from every input
  * Scores, statistics and sums are binary32; with bf16 the probabilities are rounded to bf16 for their
- * product with the values (relative 2^-8 each).  The same call gives the same bits.
+ * product with the values (relative 2^-8 each; their sum, which divides it, is of the unrounded ones).  The same
+ * call gives the same bits.
  * workspace: sdv_attend_workspace_bytes(...), 16-byte aligned, not initialised.
  * Errors as sdv_kv_append, plus n_q_heads not a multiple of n_kv_heads, window < 0, sinks < 0, out at the
  * queries' address or a scale that is not finite -> SDV_ERR_INVALID_ARG; more than INT32_MAX - 1024 rows, or rows times

@@ -282,7 +282,7 @@ __device__ __forceinline__ void add_to(char* out, int d, float v) {
 //
 // The waves of a workgroup take every fourth tile of 32 tokens, keys and values loaded a tile ahead, and join their sums
 // at the end.  Bound by the reads of the cache: 64 requests of K in 0..8 on 4096 to 8192 tokens (window 4096, 8 heads of
-// 128, bf16) 220 us, 4.9 TB/s of 1.08 GB, with the second tile of requests of more than 32 columns read again.  Few units
+// 128, bf16) 232 us, 4.6 TB/s of 1.08 GB (a large copy reaches 4.9), with the second tile of requests of more than 32 columns read again.  Few units
 // are bound by what a compute unit loads (1000 tokens of a head, 512 KB, in about 8 us; 8 waves instead of 4 take as long).
 template <class E, int D, int QB, int kWaves, bool kWholePages>
 __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, QB, kWaves>& sh, const TileOf& at,
@@ -1253,7 +1253,9 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
 
 enum Mode { kUnits, kRanges, kSmallPages, kRows };
 
-// The rules, by the batch's means; times of 8 heads, D = 128, bf16, for one side and the other.
+// The rules, by what the host knows: the batch's mean rows, and for its lengths the page table's width (under a window, the
+// window).  A table wider than the lengths need takes short caches to ranges: 16 requests of 500 tokens without a
+// window 14.3 us there for 11.3 by units, 64 of them 27.6 for 24.0.  Times of 8 heads, D = 128, bf16, for one side and the other.
 //
 // attend_rows from this many columns of a request (its rows times the heads of a group) and this many workgroups on: 64
 // requests of 96 columns on 4000 tokens 258 us for 552, 16 of 128 on 1000 29 for 36, of 64 on 4000 260 for

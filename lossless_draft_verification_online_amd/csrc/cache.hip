@@ -53,8 +53,8 @@ __device__ __forceinline__ u32x4 pack(const float (&f)[E::kPerVec]) {
 }
 
 // One workgroup per row: the row's angles once, then its heads' vectors.  256 requests of K in 0..8 (48 heads of 128, bf16,
-// 33 MB in and out) 9.7 us, 3.4 TB/s: the offsets, length, angles and table entry are a chain of loads before a row moves.
-// Prompts of 10467 rows 21 to 24 us, at the rate of a copy.
+// 33 MB in and out) 9.8 us, 3.4 TB/s: the offsets, length, angles and table entry are loaded one after another, and the row's
+// own vectors behind them, though those depend on none of it.  Prompts of 10467 rows 22 to 26 us, at the rate of a copy.
 template <class E, bool kInterleaved>
 __global__ __launch_bounds__(kThreads) void append(AppendArgs a) {
   constexpr int P = E::kPerVec;
@@ -151,7 +151,7 @@ struct SettleArgs {
 // One workgroup per request and (layer, keys or values, head).  The accepted nodes ascend, so node_d
 // >= d: a source is never behind the places already written, and a group of rows that is
 // read, then (behind a barrier) written, cannot overwrite a row that a later group reads.  Bound by the chain of offsets,
-// lengths, nodes, pages and rows: 64 trees in four layers 7.1 us for 8 MB, one tree in one layer 2.8 us.
+// lengths, nodes, pages and rows: 64 trees in four layers 7.1 us for 8 MB, one tree in one layer 2.9 us.
 __global__ __launch_bounds__(kThreads) void settle(SettleArgs a) {
   __shared__ int64_t from_s[kMaxNodes], to_s[kMaxNodes];
   __shared__ int32_t ok_s;

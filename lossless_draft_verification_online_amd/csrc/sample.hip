@@ -1117,8 +1117,8 @@ __device__ __forceinline__ double draw(const Args& a, const Source& source, Shar
 }
 
 // The rest of a row: two passes over it where it is cut (counts, then the kept masses; from the last-level cache, 512 x
-// 151936 105 us, of which shared-memory atomics and the gathering of kept logits take most), none where it is not (256 x
-// 128256 8.5 us, the latency of the fold, the search of one chunk and its barriers).
+// 151936 103 us, of which shared-memory atomics and the gathering of kept logits take most), none where it is not (256 x
+// 128256 8.8 us, the latency of the fold, the search of one chunk and its barriers).
 template <class E, int kVpl, bool kCut>
 __global__ __launch_bounds__(kDrawThreads) void row_draw(Args a) {
   constexpr int kWaves = kDrawThreads / kWave, P = E::kPerVec;
