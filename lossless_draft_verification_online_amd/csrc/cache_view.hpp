@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/sdv.h"
+#include "launch.hpp"
 #include "sdv_device.hpp"
 
 namespace sdv {

@@ -22,6 +22,7 @@
 #include <type_traits>
 
 #include "../../include/sdv.h"
+#include "launch.hpp"
 #include "sdv_device.hpp"
 
 namespace sample_impl {

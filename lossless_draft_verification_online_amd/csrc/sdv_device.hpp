@@ -8,10 +8,6 @@
 namespace sdv {
 
 constexpr int kWave = 64;
-
-// A launch holds fewer than 2^32 threads.
-inline bool too_many(int64_t workgroups, int64_t threads) { return workgroups > (int64_t)UINT32_MAX / threads; }
-
 // One work unit of the row pass streams 16 KiB of one row: 16 vectors of 16 bytes per lane.
 constexpr int kChunkBytes = 16384;
 constexpr int kVecPerLane = kChunkBytes / (16 * kWave);
