@@ -609,6 +609,93 @@ int sdv_kv_settle(const sdv_cache* cache, int32_t n_layers, int32_t B, int64_t n
                   const int32_t* ragged_offsets, const int32_t* accepted_len, const int32_t* accepted_nodes,
                   int32_t* new_len, void* stream);
 
+/*
+ * The paged cache in 8 bits.  cache.keys and cache.values hold e4m3 codes (1 sign, 4 exponent and 3 mantissa bits, bias 7,
+ * largest 448, no infinities, NaN 0x7f and 0xff) in the layout of sdv_cache, with a scale for each block of `block`
+ * tokens of a page and head:
+ *   key_scales, value_scales [n_pages][n_kv_heads][page_size / block] uint8   a byte b is the scale 2^(b - 127)
+ * and a code stands for its number times its block's scale.  Bytes that the calls below write lie in [10, 246]; one
+ * below is read as 10, one above as 246.  A power of two as the scale loses nothing of a floating-point code, and codes
+ * change from one scale to another without rounding unless they leave e4m3's normal range (2^-6 scales and less).
+ * block is a power of two in [1, 64], at most page_size.  cache.dtype is the rows': of keys, values and queries that are given,
+ * and of results.  What the calls over sdv_cache say of pages, lengths, offsets, rows, errors and limits holds here;
+ * NULL scales or another block -> SDV_ERR_INVALID_ARG.
+ */
+typedef struct sdv_cache8 {
+  sdv_cache cache;
+  uint8_t* key_scales;
+  uint8_t* value_scales;
+  int32_t block;
+} sdv_cache8;
+
+/*
+ * sdv_kv_append into a cache in 8 bits.  In each block and head that a request's new rows reach, with `top` the largest
+ * finite magnitude of the block's new rows as given (keys: before the rotation, which makes a value larger by sqrt(2) at most):
+ *   e = the least exponent in [-117, 119] with top <= 316 * 2^e (keys), 448 * 2^e (values);
+ *   a block that holds cached tokens (slots below L_i) keeps its scale if that is larger; if it is smaller, it takes 2^e
+ *   and the cached tokens' codes are brought to it, rounded to the nearest (ties to even) where they become subnormal.
+ * A value's code is the e4m3 number nearest to value * 2^-e (ties to even; the largest beyond 448, which takes a value beyond
+ * 448 * 2^119), of a rotated key to the binary32 result of the rotation; NaN where the value is not finite.  Rotated queries
+ * are rounded to the rows' type.  Codes of a block behind its rows are left as they were, under the block's scale.
+ */
+int sdv_kv_append8(const sdv_cache8* cache, int32_t B, int64_t n_draft_rows, const int32_t* ragged_offsets,
+                   const int32_t* parents, const void* keys, int64_t key_stride, const void* values,
+                   int64_t value_stride, const float* inv_freq, int32_t rotary, int32_t interleaved,
+                   const void* queries, int64_t query_stride, int32_t n_q_heads, void* queries_out, void* stream);
+
+/*
+ * sdv_attend over a cache in 8 bits: keys and values are the codes times their scales, without rounding.  Rounding is that
+ * of sdv_attend; with binary32 rows every product takes a query's, or a probability's, 24 bits.
+ */
+size_t sdv_attend8_workspace_bytes(const sdv_cache8* cache, int32_t B, int64_t n_draft_rows, int32_t n_q_heads,
+                                   int32_t window, int32_t sinks);
+int sdv_attend8(const sdv_cache8* cache, int32_t B, int64_t n_draft_rows, const int32_t* ragged_offsets,
+                const int32_t* parents, const void* queries, int64_t query_stride, int32_t n_q_heads, float scale,
+                int32_t window, int32_t sinks, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * sdv_kv_settle in caches of 8 bits.  A block that accepted tokens come to (those that stay in place among them) takes the
+ * largest scale of what it then holds of the sequence: of the blocks that the tokens come from, and its own where it holds
+ * slots up to L_i.  Codes are brought to it as in sdv_kv_append8; other slots' are left as they were.  A token whose slot to
+ * come from has no page stays what its slot to come to holds.  Layer l's scales start l * n_pages * n_kv_heads * (page_size /
+ * block) bytes behind the scales'.
+ */
+int sdv_kv_settle8(const sdv_cache8* cache, int32_t n_layers, int32_t B, int64_t n_draft_rows,
+                   const int32_t* ragged_offsets, const int32_t* accepted_len, const int32_t* accepted_nodes,
+                   int32_t* new_len, void* stream);
+
+/*
+ * A round's pages, from the requests' lengths on the GPU (after a verification they are known nowhere else): pages that no row
+ * sees any more go back to the free ones, slots of the coming rows get pages, and the page table is brought up to that.
+ *   page_table [B][max_pages] int32, in place   as in sdv_cache: slot s of request i in page page_table[i][s / page_size]
+ *   cache_len [B] int32     L_i, the slots that request i holds; -1: the request has ended
+ *   ragged_offsets [B + 1]  the coming rows, K_i + 1 of request i at slots L_i .. L_i + K_i
+ *   free_pages [n_pages] int32, in place        a ring: free_state[1] pages from place free_state[0] on
+ *   free_state [2] int32, in place              first in [0, n_pages), count in [0, n_pages]
+ * Request by request, i ascending, pages of a request by slot:
+ *   1. A page is returned to the ring's end, its entry becoming -1, unless it holds a slot in [0, L_i + K_i] that is below
+ *      sinks or above L_i - window (window 0: any); all pages of a request that has ended.
+ *   2. A request whose rows' pages lie within max_pages takes a page from the ring's front for each page of its rows
+ *      that has none, if the requests up to it together take no more than the ring held before the call.  If they
+ *      take more it takes none, and no later request takes any.
+ * Pages that a call returns can be taken by the next call.
+ *   placed [B] int32   1 if all of the request's rows have pages now, 0 if it took too many or its rows lie beyond the table,
+ *                      -1 for one that has ended or is passed over
+ *   slots [n_draft_rows + B] int64, or NULL     page * page_size + place of each row of a placed request; -1 for other rows
+ * A page is one request's alone.  An entry outside [0, n_pages) is no page, and one taken from the ring is put down as it is, its slots -1.
+ * A request with offsets that are not valid, or L_i outside [-1, INT32_MAX - 1024 - K), is passed over and its entries left as
+ * they are; with a free_state outside its bounds all requests are.  Pages beyond a full ring are dropped.
+ * workspace: sdv_kv_pages_workspace_bytes(B) bytes (0 for B outside [1, 2^24)), 16-byte aligned, not initialised; it holds nothing
+ * between calls.  Errors: NULL required pointers, B < 1, n_draft_rows < 0, sizes < 1, an unsupported page_size, window < 0, sinks < 0,
+ * misaligned pointers (to their type), or an output that overlaps an input or another output -> SDV_ERR_INVALID_ARG; 2^24 requests or
+ * more, more than INT32_MAX - 1024 rows or pages of a request, or n_pages above INT32_MAX -> SDV_ERR_LIMIT; a small workspace -> SDV_ERR_WORKSPACE.
+ */
+size_t sdv_kv_pages_workspace_bytes(int32_t B);
+int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, int32_t page_size, const int32_t* cache_len,
+                 int64_t n_draft_rows, const int32_t* ragged_offsets, int64_t n_pages, int32_t* free_pages,
+                 int32_t* free_state, int32_t window, int32_t sinks, int32_t* placed, int64_t* slots, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage). */
 const char* sdv_status_string(int status);
 

@@ -84,6 +84,15 @@ class SdvCache(ctypes.Structure):
     ]
 
 
+class SdvCache8(ctypes.Structure):
+    _fields_ = [
+        ("cache", SdvCache),
+        ("key_scales", ctypes.c_void_p),
+        ("value_scales", ctypes.c_void_p),
+        ("block", ctypes.c_int32),
+    ]
+
+
 _LIB = None
 
 _VERIFY_ARGS = [
@@ -156,6 +165,17 @@ def lib(path: str = LIBRARY) -> ctypes.CDLL:
     L.sdv_kv_settle.restype = ctypes.c_int
     L.sdv_kv_settle.argtypes = [ctypes.POINTER(SdvCache), ctypes.c_int32, ctypes.c_int32, ctypes.c_int64] + \
         [ctypes.c_void_p] * 5
+    for name in ("sdv_kv_append", "sdv_attend_workspace_bytes", "sdv_attend", "sdv_kv_settle"):
+        plain = getattr(L, name)
+        f = getattr(L, name.replace("append", "append8").replace("attend", "attend8").replace("settle", "settle8"))
+        f.restype, f.argtypes = plain.restype, [ctypes.POINTER(SdvCache8)] + plain.argtypes[1:]
+    L.sdv_kv_pages_workspace_bytes.restype = ctypes.c_size_t
+    L.sdv_kv_pages_workspace_bytes.argtypes = [ctypes.c_int32]
+    L.sdv_kv_pages.restype = ctypes.c_int
+    L.sdv_kv_pages.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                               ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                               ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                               ctypes.c_size_t, ctypes.c_void_p]
     L.sdv_status_string.restype = ctypes.c_char_p
     L.sdv_read_yardstick.restype = ctypes.c_int
     L.sdv_read_yardstick.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]

@@ -3,34 +3,47 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", "sdv.hip"), os.path.join(PKG, "csrc", "commit.hip"),
            os.path.join(PKG, "csrc", "sample.hip"), os.path.join(PKG, "csrc", "cache.hip"),
-           os.path.join(PKG, "csrc", "attend.hip"), os.path.join(PKG, "csrc", "sdcp_uniforms.cpp")]
+           os.path.join(PKG, "csrc", "attend.hip"), os.path.join(PKG, "csrc", "cache8.hip"),
+           os.path.join(PKG, "csrc", "attend8.hip"), os.path.join(PKG, "csrc", "pages.hip"),
+           os.path.join(PKG, "csrc", "sdcp_uniforms.cpp")]
 DEPENDS = SOURCES + [os.path.join(PKG, "csrc", "sdv_device.hpp"), os.path.join(PKG, "csrc", "split.hpp"),
                      os.path.join(PKG, "csrc", "cache_view.hpp"), os.path.join(PKG, "csrc", "attend_unit.hpp"),
-                     os.path.join(PKG, "csrc", "launch.hpp"),
+                     os.path.join(PKG, "csrc", "cache8_view.hpp"), os.path.join(PKG, "csrc", "launch.hpp"),
                      os.path.join(ROOT, "include", "sdv.h")]
 LIBRARY = os.path.join(PKG, "libsdv.so")
 
 HIPCC_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared", "-Wall",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
     # packed fp32 instructions stay off: plain fp32 code only
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
 
 
+def _compile(cmd: list, what: str) -> str:
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"hipcc failed on {what} ({res.returncode}):\n{res.stderr}")
+    return res.stderr
+
+
 def build_library(out: str = LIBRARY, verbose: bool = False) -> str:
     hipcc = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
     tmp = out + ".tmp"
-    cmd = [hipcc, *HIPCC_FLAGS, f"-I{os.path.join(ROOT, 'include')}", *SOURCES, "-o", tmp]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{res.stderr}")
-    if verbose and res.stderr:
-        print(res.stderr)
+    with tempfile.TemporaryDirectory() as where:
+        objects = [os.path.join(where, os.path.basename(s) + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(max_workers=8) as pool:
+            said = list(pool.map(lambda job: _compile([hipcc, *HIPCC_FLAGS, f"-I{os.path.join(ROOT, 'include')}", "-c",
+                                                       job[0], "-o", job[1]], job[0]), zip(SOURCES, objects)))
+        said.append(_compile([hipcc, "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", tmp], out))
+    if verbose and any(said):
+        print("".join(said))
     os.replace(tmp, out)
     return out
 

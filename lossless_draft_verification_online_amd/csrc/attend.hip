@@ -230,9 +230,9 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
       u32x4* const mine = reinterpret_cast<u32x4*>(v_s + 16 * wave * kLine) + lane;
       bool bad = false;
 #pragma unroll
-      for (int x = 0; x < kLoads; ++x) bad |= not_finite(mine[64 * x]);
+      for (int x = 0; x < kLoads; ++x) bad |= not_finite<Bf16>(mine[64 * x]);
       if (__any(bad)) {
-        for (int x = 0; x < kLoads; ++x) mine[64 * x] = finite_of(mine[64 * x]);
+        for (int x = 0; x < kLoads; ++x) mine[64 * x] = finite_of<Bf16>(mine[64 * x]);
         odd_s = 1;
       }
     }
@@ -472,11 +472,11 @@ template <class E, int D, int QB>
 int launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
   const dim3 units((unsigned)(a.tiles * a.cache.n_heads)), threads(kStreamWaves * kWave);
   if (p.mode == kSmallPages) {
-    hipLaunchKernelGGL((attend_units<E, D, QB, kStreamWaves, false>), units, threads, 0, s, a);
+    hipLaunchKernelGGL((attend_units<E, D, QB, kStreamWaves, false, false>), units, threads, 0, s, a);
   } else if (p.mode == kUnits) {
-    hipLaunchKernelGGL((attend_units<E, D, QB, kStreamWaves, true>), units, threads, 0, s, a);
+    hipLaunchKernelGGL((attend_units<E, D, QB, kStreamWaves, true, false>), units, threads, 0, s, a);
   } else {
-    hipLaunchKernelGGL((attend_ranges<E, D, QB>), dim3((unsigned)a.ranges), threads, 0, s, a);
+    hipLaunchKernelGGL((attend_ranges<E, D, QB, false>), dim3((unsigned)a.ranges), threads, 0, s, a);
     if (p.pieces > 16)
       hipLaunchKernelGGL((join<E, D, QB, true>), dim3(units.x, 16 * QB), dim3(kJoinWaves * kWave), 0, s, a);
     else

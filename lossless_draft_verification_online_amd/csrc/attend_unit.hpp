@@ -16,7 +16,9 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "cache_view.hpp"
+#include <type_traits>
+
+#include "cache8_view.hpp"
 
 namespace attend_impl {
 
@@ -41,7 +43,48 @@ struct AttendArgs {
   char* out;
   float* part;   // [2 ranges][columns][D] sums of a piece of a unit, in the frame of its maxima
   float* stats;  // [2 ranges][columns][2] maximum and sum of weights
+  // a cache in 8 bits: bytes b of the scales 2^(b - 127), [pages][heads][page_size >> block_log2]
+  const uint8_t* key_scales;
+  const uint8_t* value_scales;
+  int32_t block_log2;
 };
+
+// A cache in 8 bits holds e4m3 codes with a power of two as the scale of a block of tokens and head.  A code times its
+// scale is a bf16 number without rounding (4 significant bits), so the products are those of bf16 caches, of
+// operands converted in registers.  Queries and probabilities of binary32 rows go into them as three bf16 numbers
+// whose sum they are: three products of the bf16 rate for eight of the binary32 instructions'.
+struct Codes8 {
+  static constexpr int kBytes = 1;
+  // What is finite adds nothing where this is used; a code of seven set bits is no number.
+  __device__ static __forceinline__ float at(const void* row, int64_t v) {
+    return (static_cast<const uint8_t*>(row)[v] & 0x7f) == 0x7f ? __builtin_nanf("") : 0.0f;
+  }
+};
+
+// 8 codes (two words) times their scale.
+__device__ __forceinline__ bf16x8 bf16_of_codes(uint32_t lo, uint32_t hi, float scale) {
+  const auto a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+  const auto b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+  const auto c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+  const auto d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+  bf16x8 v;
+  v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1], v[4] = c[0], v[5] = c[1], v[6] = d[0], v[7] = d[1];
+  return v;
+}
+
+// Codes that are no numbers, in a word of four.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t v) { return ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// x as three bf16 numbers, cut and not rounded: 3 times 8 bits are its 24.  One that is not finite is the first.
+__device__ __forceinline__ void three_of(float x, __bf16& a, __bf16& b, __bf16& c) {
+  const float h = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+  const float r = x - h;  // exact; NaN where x is infinite
+  const float m = __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+  const bool finite = r == r;
+  a = (__bf16)(finite ? h : x);
+  b = (__bf16)(finite ? m : 0.0f);
+  c = (__bf16)(finite ? r - m : 0.0f);
+}
 
 // First tile number of request i: its columns take at most ceil((K + 1) G / columns) tiles from there.
 __device__ __forceinline__ int64_t first_tile(const int32_t* cu, int32_t i, int32_t G, int32_t columns) {
@@ -199,10 +242,10 @@ struct TreeSight {
   bool last;
 };
 
-template <class E, int D, int QB, int kWaves>
+template <class E, int D, int QB, int kWaves, bool k8>
 struct Shape {
   static constexpr int kColumns = 16 * QB;
-  static constexpr bool kBf16 = E::kBytes == 2;
+  static constexpr bool kBf16 = E::kBytes == 2 || k8;  // of the products
   static constexpr int kValueStride = D * 2 + 32;  // bytes; rows 8 banks apart for the transposing reads
   static constexpr int kValueBytes = kBf16 ? kWaves * kTile * kValueStride : 0;
   static constexpr int kMergeStride = D + 4;
@@ -210,9 +253,9 @@ struct Shape {
   static constexpr int kBytes = kValueBytes > kMergeBytes ? kValueBytes : kMergeBytes;
 };
 
-template <class E, int D, int QB, int kWaves>
+template <class E, int D, int QB, int kWaves, bool k8>
 struct Scratch {
-  using S = Shape<E, D, QB, kWaves>;
+  using S = Shape<E, D, QB, kWaves, k8>;
   __align__(16) char smem[S::kBytes];
   float m_s[kWaves][S::kColumns], l_s[kWaves][S::kColumns];
   int32_t odd_s[kWaves];
@@ -225,23 +268,30 @@ struct Scratch {
 // the weight 0 for it, and 0 times NaN is NaN.  The tiles' products take 0 in their place, and where there were
 // some, a pass behind the unit adds them to the results of the columns that do see them (an infinity or NaN times a
 // positive weight is itself).
+template <class C>
 __device__ __forceinline__ bool not_finite(u32x4 v) {
+  if constexpr (C::kBytes == 1) return (nan_codes(v.x) | nan_codes(v.y) | nan_codes(v.z) | nan_codes(v.w)) != 0;
   typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
   u16x2 top = {0, 0};
 #pragma unroll
   for (int w = 0; w < 4; ++w) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[w] & 0x7fff7fffu));
   return top.x >= 0x7f80 || top.y >= 0x7f80;
 }
+template <class C>
 __device__ __forceinline__ u32x4 finite_of(u32x4 v) {
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
+    if constexpr (C::kBytes == 1) {
+      v[w] &= ~((nan_codes(v[w]) >> 7) * 255u);
+      continue;
+    }
     if ((v[w] & 0x7f80u) == 0x7f80u) v[w] &= 0xffff0000u;
     if ((v[w] & 0x7f800000u) == 0x7f800000u) v[w] &= 0xffffu;
   }
   return v;
 }
 // One wave, for its columns and the tiles of [lo, hi) that are not all_see(start): add(column, d, value).
-template <class E, int D, int kTokens, class Start, class AllSee, class Sees, class Add>
+template <class C, int D, int kTokens, class Start, class AllSee, class Sees, class Add>
 __device__ __forceinline__ void add_not_finite(const AttendArgs& a, int32_t i, int32_t head, int32_t lo, int32_t hi,
                                                int32_t columns, Start start, AllSee all_see, Sees sees, Add add) {
   const int lane = threadIdx.x & (kWave - 1);
@@ -251,10 +301,10 @@ __device__ __forceinline__ void add_not_finite(const AttendArgs& a, int32_t i, i
     for (int32_t s = start(n); s < start(n) + kTokens; ++s) {
       const int32_t page = a.cache.page(i, s);
       if (page < 0) continue;
-      const char* const row = a.cache.values + a.cache.row(page, head, s) * (D * E::kBytes);
+      const char* const row = a.cache.values + a.cache.row(page, head, s) * (D * C::kBytes);
 #pragma unroll 1
       for (int d = lane; d < D; d += kWave) {
-        const float v = E::at(row, d);
+        const float v = C::at(row, d);
         const bool bad = !(v - v == 0.0f);
         if (!__any(bad)) continue;
         for (int32_t c = 0; c < columns; ++c)
@@ -284,12 +334,15 @@ __device__ __forceinline__ void add_to(char* out, int d, float v) {
 // at the end.  Bound by the reads of the cache: 64 requests of K in 0..8 on 4096 to 8192 tokens (window 4096, 8 heads of
 // 128, bf16) 232 us, 4.6 TB/s of 1.08 GB (a large copy reaches 4.9), with the second tile of requests of more than 32 columns read again.  Few units
 // are bound by what a compute unit loads (1000 tokens of a head, 512 KB, in about 8 us; 8 waves instead of 4 take as long).
-template <class E, int D, int QB, int kWaves, bool kWholePages>
-__device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, QB, kWaves>& sh, const TileOf& at,
+template <class E, int D, int QB, int kWaves, bool kWholePages, bool k8>
+__device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, QB, kWaves, k8>& sh, const TileOf& at,
                                             int32_t len, int32_t head, bool pos_all, int32_t w_lo, int32_t w_hi, int64_t slot) {
-  using S = Shape<E, D, QB, kWaves>;
+  using S = Shape<E, D, QB, kWaves, k8>;
+  using C = typename std::conditional<k8, Codes8, E>::type;  // what the cache holds
   constexpr bool kBf16 = S::kBf16;
-  constexpr int kSteps = kBf16 ? D / 32 : D / 16;  // 16-byte pieces of a key row per lane
+  constexpr int kSteps = k8 ? D / 64 : (kBf16 ? D / 32 : D / 16);  // 16-byte pieces of a key row per lane
+  constexpr int kTerms = k8 && E::kBytes == 4 ? 3 : 1;             // of a query, or a probability
+  constexpr int kQ = k8 ? D / 32 : kSteps;                         // pieces of a query's operands
   constexpr int kDB = D / 16;                       // blocks of 16 output values
   char* const smem = sh.smem;
   auto& m_s = sh.m_s;
@@ -331,7 +384,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   int32_t jrow[QB];
   bool live[QB];
   TreeSight sight[QB];
-  u32x4 q[QB][kSteps];
+  u32x4 q[QB][kTerms][kQ];
 #pragma unroll
   for (int b = 0; b < QB; ++b) {
     const int32_t c = at.c0 + 16 * b + col;
@@ -341,13 +394,37 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
     sight[b].rows = a.parents && live[b] ? sight_s[jrow[b]] : 0;
     sight[b].last = a.parents && live[b] ? last_s[jrow[b]] != 0 : false;
     const int32_t h = head * a.G + (c - jrow[b] * a.G);
-    const char* src = a.queries + ((at.r.row0 + jrow[b]) * a.query_stride + h * D) * E::kBytes + 16 * g;
+    const char* src = a.queries + ((at.r.row0 + jrow[b]) * a.query_stride + h * D) * E::kBytes;
+    if constexpr (!k8) src += 16 * g;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
+    for (int s = 0; s < kQ; ++s) {
       u32x4 z;
       z.x = z.y = z.z = z.w = 0;
-      if (live[b]) z = *reinterpret_cast<const u32x4*>(src + 64 * s) ^ a.flip;
-      q[b][s] = z;
+      if constexpr (!k8) {
+        if (live[b]) z = *reinterpret_cast<const u32x4*>(src + 64 * s) ^ a.flip;
+        q[b][0][s] = z;
+      } else {  // the 8 values that lie opposite to half s % 2 of a lane's 16 codes
+        const char* const from = src + (64 * (s / 2) + 16 * g + 8 * (s % 2)) * E::kBytes;
+        if (live[b]) z = *reinterpret_cast<const u32x4*>(from) ^ a.flip;
+        if constexpr (kTerms == 1) {
+          q[b][0][s] = z;
+        } else {
+          u32x4 y;
+          y.x = y.y = y.z = y.w = 0;
+          if (live[b]) y = *reinterpret_cast<const u32x4*>(from + 16) ^ a.flip;
+          bf16x8 term[3];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            __bf16 t0, t1, t2;
+            three_of(__uint_as_float(e < 4 ? z[e & 3] : y[e & 3]), t0, t1, t2);
+            term[0][e] = t0;
+            term[1][e] = t1;
+            term[2][e] = t2;
+          }
+#pragma unroll
+          for (int x = 0; x < 3; ++x) q[b][x][s] = __builtin_bit_cast(u32x4, term[x]);
+        }
+      }
     }
   }
 
@@ -384,7 +461,11 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
 
   char* const v_lds = smem + wave * kTile * S::kValueStride;
   u32x4 kreg[2][kSteps];
-  u32x4 vreg[kBf16 ? D / 16 : 1];
+  constexpr int kLine = D * C::kBytes;
+  constexpr int kLoads = kLine / 32;  // 16-byte pieces per lane of a tile's values
+  u32x4 vreg[kBf16 ? kLoads : 1];
+  uint32_t byte_1 = 0;  // the next tile's scale of token lane & 31: of its keys, in the upper half of its values
+  float scale = 0.0f;
   float vf[kBf16 ? 1 : 8][kDB];
   // The table's entry of token lane & 31 as it is, checked when it is used: a check would wait for it, and for
   // the keys and values asked for before it.
@@ -394,11 +475,16 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
     return n < w_hi && (kWholePages || held(s)) && k < a.cache.max_pages ? table[k] : -1;
   };
   auto page_of = [&](int32_t entry) { return entry >= 0 && entry < a.cache.n_pages ? entry : -1; };
-  constexpr int kLine = D * E::kBytes;
   // the lane's byte offsets within 16 tokens' rows
   const uint32_t k_off = col * kLine + 16 * g;
-  constexpr int kLanes = D / 8, kRows = kWave / kLanes;  // lanes of a bf16 value row, rows of one load
+  constexpr int kLanes = kLine / 16, kRows = kWave / kLanes;  // lanes of a value row, rows of one load
   const uint32_t v_off = (lane / kLanes) * kLine + (lane % kLanes) * 16;
+  auto load_scales = [&](int32_t n, int32_t page) {
+    const int32_t s = start(n) + (lane & (kTile - 1)), in = s & ((1 << a.cache.page_log2) - 1);
+    const uint8_t* const from = lane < kTile ? a.key_scales : a.value_scales;
+    byte_1 = from[(((int64_t)(page < 0 ? 0 : page) * a.cache.n_heads + head) << (a.cache.page_log2 - a.block_log2)) +
+                  (in >> a.block_log2)];
+  };
   // Keys and values of a tile are asked for separately, each as soon as the registers of the tile before are free.
   auto load_keys = [&](int32_t n, int32_t page) {
     const int32_t s0 = start(n);
@@ -425,12 +511,12 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
           const int32_t p = lane_value(page, 16 * blk);
           const char* vs = a.cache.values + a.cache.row(p < 0 ? 0 : p, head, s0 + 16 * blk) * kLine + v_off;
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x)
-            vreg[blk * (D / 32) + x] = *reinterpret_cast<const u32x4*>(vs + x * kRows * kLine);
+          for (int x = 0; x < kLoads / 2; ++x)
+            vreg[blk * (kLoads / 2) + x] = *reinterpret_cast<const u32x4*>(vs + x * kRows * kLine);
         }
       } else {
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
+        for (int x = 0; x < kLoads; ++x) {
           const int k = x * kRows + lane / kLanes;
           const int32_t p = __shfl(page, k);
           vreg[x] = *reinterpret_cast<const u32x4*>(a.cache.values +
@@ -454,6 +540,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   // the pages of two tiles ahead: a page read behind a tile's loads would wait for them
   int32_t page = page_of(entry_at(n)), entry_1 = entry_at(n + kWaves);
   if (n < w_hi) {
+    if constexpr (k8) load_scales(n, page);
     load_keys(n, page);
     load_values(n, page);
   }
@@ -466,8 +553,28 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
     const bool paged = there == ~0u;
     const bool more = n + kWaves < w_hi;
     f32x4 sc[QB][2];
+    if constexpr (k8) {
+      scale = scale_of(byte_1);
 #pragma unroll
-    for (int b = 0; b < QB; ++b) {
+      for (int blk = 0; blk < 2; ++blk) {
+        const float by = __shfl(scale, 16 * blk + col);
+#pragma unroll
+        for (int b = 0; b < QB; ++b) sc[b][blk] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < kQ; ++s) {
+          const bf16x8 k = bf16_of_codes(kreg[blk][s / 2][2 * (s % 2)], kreg[blk][s / 2][2 * (s % 2) + 1], by);
+#pragma unroll
+          for (int b = 0; b < QB; ++b)
+#pragma unroll
+            for (int x = kTerms - 1; x >= 0; --x)
+              sc[b][blk] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, __builtin_bit_cast(bf16x8, q[b][x][s]), sc[b][blk],
+                                                                    0, 0, 0);
+        }
+      }
+      if (more) load_scales(n + kWaves, page_1);
+    }
+#pragma unroll
+    for (int b = 0; b < QB && !k8; ++b) {
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk) {
         sc[b][blk] = f32x4{0, 0, 0, 0};
@@ -475,12 +582,12 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
         for (int s = 0; s < kSteps; ++s) {
           if constexpr (kBf16) {
             sc[b][blk] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, kreg[blk][s]),
-                                                                  __builtin_bit_cast(bf16x8, q[b][s]), sc[b][blk], 0, 0, 0);
+                                                                  __builtin_bit_cast(bf16x8, q[b][0][s]), sc[b][blk], 0, 0, 0);
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               sc[b][blk] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kreg[blk][s][e]),
-                                                                __uint_as_float(q[b][s][e]), sc[b][blk], 0, 0, 0);
+                                                                __uint_as_float(q[b][0][s][e]), sc[b][blk], 0, 0, 0);
           }
         }
       }
@@ -489,27 +596,35 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
     if constexpr (kBf16) {
       if (!paged) {
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x)
+        for (int x = 0; x < kLoads; ++x)
           if (!((there >> (x * kRows + lane / kLanes)) & 1)) vreg[x].x = vreg[x].y = vreg[x].z = vreg[x].w = 0;
       }
       if (!all_see(s0)) {
         bool bad = false;
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) bad |= not_finite(vreg[x]);
+        for (int x = 0; x < kLoads; ++x) bad |= not_finite<C>(vreg[x]);
         if (__any(bad)) {
           odd = true;
 #pragma unroll
-          for (int x = 0; x < D / 16; ++x) vreg[x] = finite_of(vreg[x]);
+          for (int x = 0; x < kLoads; ++x) vreg[x] = finite_of<C>(vreg[x]);
         }
       }
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x)
-        *reinterpret_cast<u32x4*>(v_lds + (x * kRows + lane / kLanes) * S::kValueStride + (lane % kLanes) * 16) = vreg[x];
+      for (int x = 0; x < kLoads; ++x) {
+        char* const to = v_lds + (x * kRows + lane / kLanes) * S::kValueStride + (lane % kLanes) * (16 * 2 / C::kBytes);
+        if constexpr (k8) {
+          const float by = __shfl(scale, kTile + x * kRows + lane / kLanes);
+          *reinterpret_cast<bf16x8*>(to) = bf16_of_codes(vreg[x].x, vreg[x].y, by);
+          *reinterpret_cast<bf16x8*>(to + 16) = bf16_of_codes(vreg[x].z, vreg[x].w, by);
+        } else {
+          *reinterpret_cast<u32x4*>(to) = vreg[x];
+        }
+      }
       if (more) load_values(n + kWaves, page_1);
     }
 
     const bool whole = paged && all_see(s0);  // no masks
-    bf16x8 pb[QB];
+    bf16x8 pb[QB][kTerms];
     float pf[QB][8];
 #pragma unroll
     for (int b = 0; b < QB; ++b) {
@@ -551,10 +666,17 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
       for (int e = 0; e < 8; ++e) {
         const float p = fast_exp2(fmaf(sc[b][e >> 2][e & 3], a.scale2, -frame));
         sum += p;
-        if constexpr (kBf16)
-          pb[b][e] = (__bf16)p;
-        else
+        if constexpr (kTerms == 3) {
+          __bf16 t0, t1, t2;
+          three_of(p, t0, t1, t2);
+          pb[b][0][e] = t0;
+          pb[b][1][e] = t1;
+          pb[b][2][e] = t2;
+        } else if constexpr (kBf16) {
+          pb[b][0][e] = (__bf16)p;
+        } else {
           pf[b][e] = p;
+        }
       }
       l[b] += sum;
     }
@@ -570,7 +692,9 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
         const bf16x8 v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
         for (int b = 0; b < QB; ++b)
-          acc[b][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pb[b], acc[b][d], 0, 0, 0);
+#pragma unroll
+          for (int x = kTerms - 1; x >= 0; --x)
+            acc[b][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, pb[b][x], acc[b][d], 0, 0, 0);
       }
       __builtin_amdgcn_wave_barrier();
     } else {
@@ -677,7 +801,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
 #pragma unroll
       for (int d = 0; d < kDB; ++d) {
         const f32x4 o = acc[b][d] * inv;
-        if constexpr (kBf16) {
+        if constexpr (E::kBytes == 2) {
           bf16x4 w;
           for (int e = 0; e < 4; ++e) w[e] = (__bf16)o[e];
           *reinterpret_cast<bf16x4*>(dst + d * 32) = w;
@@ -690,7 +814,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   for (int w = 1; w < kWaves; ++w) odd |= sh.odd_s[w] != 0;
   if (odd) {
     auto row_of = [&](int32_t c) { return (int32_t)((uint32_t)(at.c0 + c) / (uint32_t)a.G); };
-    add_not_finite<E, D, kTile>(
+    add_not_finite<C, D, kTile>(
         a, i, head, w_lo, w_hi, c_last - at.c0 + 1, start, all_see,
         [&](int32_t c, int32_t s) {
           const int32_t j = row_of(c), pos_c = len + (a.parents ? depth_s[j] : j);
@@ -715,22 +839,22 @@ template <class E, int D, int QB>
 constexpr int kMinWaves = E::kBytes == 4 ? (D <= 128 ? 2 : 1) : (D * QB <= 256 ? 2 : 1);
 
 // A workgroup per unit.
-template <class E, int D, int QB, int kWaves, bool kWholePages>
+template <class E, int D, int QB, int kWaves, bool kWholePages, bool k8>
 __global__ __launch_bounds__(kWaves* kWave, (kMinWaves<E, D, QB>)) void attend_units(AttendArgs a) {
-  __shared__ Scratch<E, D, QB, kWaves> sh;
+  __shared__ Scratch<E, D, QB, kWaves, k8> sh;
   const int64_t block = unit_of_block(blockIdx.x, gridDim.x);
   const TileOf at = tile_of<16 * QB>(a, block / a.cache.n_heads);
   if (at.r.index < 0) return;
-  attend_unit<E, D, QB, kWaves, kWholePages>(a, sh, at, a.cache.len[at.r.index], (int32_t)(block % a.cache.n_heads),
+  attend_unit<E, D, QB, kWaves, kWholePages, k8>(a, sh, at, a.cache.len[at.r.index], (int32_t)(block % a.cache.n_heads),
                                              false, 0, 0, -1);
 }
 
 // A workgroup per range of the batch's work.
 constexpr int kStreamWaves = 4;
-template <class E, int D, int QB>
+template <class E, int D, int QB, bool k8>
 __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void attend_ranges(AttendArgs a) {
   constexpr int kColumns = 16 * QB;
-  __shared__ Scratch<E, D, QB, kStreamWaves> sh;
+  __shared__ Scratch<E, D, QB, kStreamWaves, k8> sh;
   const Stream s = stream_of(a, kColumns);
   const int64_t range = unit_of_block(blockIdx.x, gridDim.x);
   const int64_t end = (range + 1) * s.length < s.total ? (range + 1) * s.length : s.total;
@@ -755,7 +879,7 @@ __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void at
     at.r = request_with(w, i);
     at.c0 = (int32_t)(unit / (uint32_t)a.cache.n_heads) * kColumns;
     const bool first = q_lo == 0, whole = first && q_hi == w.n;
-    attend_unit<E, D, QB, kStreamWaves, true>(a, sh, at, w.len, (int32_t)(unit % (uint32_t)a.cache.n_heads), true,
+    attend_unit<E, D, QB, kStreamWaves, true, k8>(a, sh, at, w.len, (int32_t)(unit % (uint32_t)a.cache.n_heads), true,
                                               q_lo, q_hi,
                                               whole ? -1 : 2 * range + (first ? 1 : 0));
     p += q_hi - q_lo;

@@ -1,0 +1,295 @@
+// A round's pages from the requests' lengths: sdv_kv_pages.  Pages that no row sees any more go back to a ring of free
+// ones, and the coming rows' slots get pages from it, in the order of the requests.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "cache_view.hpp"
+
+namespace pages_impl {
+
+using namespace sdv;
+
+constexpr int kWaves = 4, kThreads = kWaves * kWave;
+
+struct PagesArgs {
+  int32_t* table;
+  const int32_t* len;
+  const int32_t* cu;
+  int32_t* ring;
+  int32_t* state;
+  int32_t* placed;
+  int64_t* slots;
+  int32_t* freed;   // [B][kWaves] entries that a wave's part of a request's row of the table returns
+  int32_t* wanted;  // [B] pages that a request takes
+  int32_t* before;  // [2] the ring's state before the call
+  int64_t n_d, n_pages;
+  int32_t B, max_pages, page_log2, window, sinks;
+};
+
+// What a request keeps of its row of the table: entries [0, near) and [lo, hi); those of its rows are [rows, hi).
+struct Keeps {
+  bool known, open;  // not passed over; not ended
+  int32_t near, lo, rows, hi;
+  __device__ __forceinline__ bool fits(const PagesArgs& a) const { return open && hi <= a.max_pages; }
+};
+__device__ __forceinline__ Keeps keeps_of(const PagesArgs& a, const Request& r, int32_t len) {
+  Keeps k;
+  k.known = r.index >= 0 && (len == -1 || len_fits(len, r.k));
+  k.open = k.known && len >= 0;
+  k.near = k.lo = k.rows = k.hi = 0;
+  if (!k.open) return k;
+  const int32_t end = len + r.k + 1, page = 1 << a.page_log2;
+  k.hi = (int32_t)(((int64_t)end + page - 1) >> a.page_log2);
+  k.rows = len >> a.page_log2;
+  if (a.window) {
+    const int32_t low = len - a.window + 1 > 0 ? len - a.window + 1 : 0, sinks = a.sinks < end ? a.sinks : end;
+    k.lo = low >> a.page_log2;
+    k.near = (int32_t)(((int64_t)sinks + page - 1) >> a.page_log2);
+  }
+  return k;
+}
+
+// A ring's state within its bounds.
+__device__ __forceinline__ bool ring_fits(const PagesArgs& a, int32_t first, int32_t count) {
+  return first >= 0 && first < a.n_pages && count >= 0 && count <= a.n_pages;
+}
+
+// The part of a request's row of the table that wave w takes.
+__device__ __forceinline__ void part_of(int32_t max_pages, int w, int32_t& lo, int32_t& hi) {
+  const int32_t part = ((max_pages + kWaves * kWave - 1) / (kWaves * kWave)) * kWave;
+  lo = w * part < max_pages ? w * part : max_pages;
+  hi = lo + part < max_pages ? lo + part : max_pages;
+}
+
+__device__ __forceinline__ void ask(const PagesArgs& a, const Keeps& k, int32_t at, int32_t entry, bool& free, bool& want) {
+  const bool have = entry >= 0 && entry < a.n_pages, in = at < a.max_pages;
+  const bool keep = at < k.near || (at >= k.lo && at < k.hi);
+  free = in && have && !keep;
+  want = in && !have && at >= k.rows && at < k.hi;
+}
+
+// What each request returns and takes; slots are -1 until they are known.
+__global__ __launch_bounds__(kThreads) void count(PagesArgs a) {
+  __shared__ int32_t wanted_s[kWaves];
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int32_t i = blockIdx.x;
+  if (a.slots)
+    for (int64_t x = (int64_t)i * kThreads + t; x < a.n_d + a.B; x += (int64_t)a.B * kThreads) a.slots[x] = -1;
+  const int32_t first = a.state[0], held = a.state[1];
+  if (i == 0 && t == 0) {
+    a.before[0] = first;
+    a.before[1] = held;
+  }
+  const Keeps k = keeps_of(a, request_at(a.cu, i, a.n_d), a.len[i]);
+  const bool works = k.known && ring_fits(a, first, held);
+  int32_t frees = 0, wants = 0, lo, hi;
+  part_of(a.max_pages, wave, lo, hi);
+  const int32_t* const row = a.table + (int64_t)i * a.max_pages;
+  if (works) {
+#pragma unroll 4
+    for (int32_t x = lo; x < hi; x += kWave) {
+      const int32_t at = x + lane;
+      bool free, want;
+      ask(a, k, at, at < a.max_pages ? row[at] : -1, free, want);
+      frees += __popcll(__ballot(free));
+      wants += __popcll(__ballot(want));
+    }
+  }
+  if (lane == 0) {
+    a.freed[(int64_t)i * kWaves + wave] = frees;
+    wanted_s[wave] = wants;
+  }
+  __syncthreads();
+  if (t == 0) {
+    int32_t n = 0;
+    for (int w = 0; w < kWaves; ++w) n += wanted_s[w];
+    a.wanted[i] = works && k.fits(a) ? n : 0;
+  }
+}
+
+template <class T>
+__device__ __forceinline__ T group_sum(T v, T* of_wave) {
+  v = lane_value(wave_inclusive_scan((uint64_t)v), kWave - 1);
+  __syncthreads();
+  if ((threadIdx.x & (kWave - 1)) == 0) of_wave[threadIdx.x / kWave] = v;
+  __syncthreads();
+  T sum = 0;
+  for (int w = 0; w < kWaves; ++w) sum += of_wave[w];
+  return sum;
+}
+
+// A workgroup per request returns its pages and takes those that it has a right to.
+__global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
+  __shared__ uint64_t sum_s[kWaves];
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int32_t i = blockIdx.x;
+  const int32_t first = a.before[0], held = a.before[1];
+  const Request r = request_at(a.cu, i, a.n_d);
+  const int32_t len = a.len[i];
+  const Keeps k = keeps_of(a, r, len);
+  const bool ring = ring_fits(a, first, held);
+  // pages returned and taken before this request
+  uint64_t returned = 0, taken = 0;
+  for (int32_t x = t; x < i; x += kThreads) {
+    for (int w = 0; w < kWaves; ++w) returned += (uint32_t)a.freed[(int64_t)x * kWaves + w];
+    taken += (uint32_t)a.wanted[x];
+  }
+  returned = group_sum(returned, sum_s);
+  taken = group_sum(taken, sum_s);
+  const int32_t wants = a.wanted[i];
+  const bool is_placed = ring && k.fits(a) && (wants == 0 || taken + wants <= (uint64_t)held);
+  if (t == 0) a.placed[i] = !ring || !k.open ? -1 : (is_placed ? 1 : 0);
+
+  if (i == 0 && ring) {  // the ring's state behind the call
+    uint64_t all = 0, sum = 0, most = 0;
+    for (int32_t x0 = 0; x0 < a.B; x0 += kThreads) {
+      const int32_t x = x0 + t;
+      uint64_t mine = 0, back = 0;
+      if (x < a.B) {
+        mine = (uint32_t)a.wanted[x];
+        for (int w = 0; w < kWaves; ++w) back += (uint32_t)a.freed[(int64_t)x * kWaves + w];
+      }
+      all += group_sum(back, sum_s);
+      const uint64_t inc = wave_inclusive_scan(mine);
+      __syncthreads();
+      if (lane == kWave - 1) sum_s[wave] = inc;
+      __syncthreads();
+      uint64_t here = sum + inc;
+      for (int w = 0; w < wave; ++w) here += sum_s[w];
+      for (int w = 0; w < kWaves; ++w) sum += sum_s[w];
+      // the largest sum that the ring held
+      const uint64_t fits = here <= (uint64_t)held ? here : 0;
+      uint64_t top = fits;
+#pragma unroll
+      for (int step = 1; step < kWave; step *= 2) {
+        const uint64_t o = __shfl_xor((unsigned long long)top, step);
+        top = o > top ? o : top;
+      }
+      __syncthreads();
+      if (lane == 0) sum_s[wave] = top;
+      __syncthreads();
+      for (int w = 0; w < kWaves; ++w) most = sum_s[w] > most ? sum_s[w] : most;
+      __syncthreads();
+    }
+    if (t == 0) {
+      // what a full ring has no room for is dropped
+      const uint64_t room = (uint64_t)a.n_pages - held, back = all < room ? all : room;
+      a.state[0] = (int32_t)((first + most) % (uint64_t)a.n_pages);
+      a.state[1] = (int32_t)((uint64_t)held + back - most);
+    }
+  }
+
+  if (!ring || !k.known) return;
+  int32_t lo, hi;
+  part_of(a.max_pages, wave, lo, hi);
+  for (int w = 0; w < wave; ++w) returned += (uint32_t)a.freed[(int64_t)i * kWaves + w];
+  int32_t* const row = a.table + (int64_t)i * a.max_pages;
+  // pages of its rows that lie in the parts before this wave's: counted again from the table as it was
+  // (entries are written behind the barrier)
+  if (is_placed) {
+    int32_t mine = 0;
+    const int32_t from = k.rows > lo ? k.rows : lo, to = k.hi < hi ? k.hi : hi;
+    for (int32_t x = from; x < to; x += kWave) {
+      const int32_t at = x + lane;
+      bool free = false, want = false;
+      if (at < to) ask(a, k, at, row[at], free, want);
+      mine += __popcll(__ballot(want));
+    }
+    __syncthreads();
+    if (lane == 0) sum_s[wave] = (uint32_t)mine;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) taken += sum_s[w];
+  }
+  const uint64_t below = ((uint64_t)1 << lane) - 1;
+#pragma unroll 4
+  for (int32_t x = lo; x < hi; x += kWave) {
+    const int32_t at = x + lane;
+    const int32_t entry = at < a.max_pages ? row[at] : -1;
+    bool free, want;
+    ask(a, k, at, entry, free, want);
+    want = want && is_placed;
+    const uint64_t frees = __ballot(free), wants_here = __ballot(want);
+    if (free) {
+      const uint64_t to = (uint64_t)held + returned + __popcll(frees & below);
+      if (to < (uint64_t)a.n_pages) a.ring[(first + to) % (uint64_t)a.n_pages] = entry;
+      row[at] = -1;
+    }
+    if (want) row[at] = a.ring[(first + taken + __popcll(wants_here & below)) % (uint64_t)a.n_pages];
+    returned += __popcll(frees);
+    taken += __popcll(wants_here);
+  }
+  if (!is_placed || !a.slots) return;
+  __syncthreads();
+  for (int32_t j = t; j <= r.k; j += kThreads) {
+    const int32_t s = len + j, page = row[s >> a.page_log2];
+    a.slots[r.row0 + j] = page >= 0 && page < a.n_pages
+                              ? ((int64_t)page << a.page_log2) + (s & ((1 << a.page_log2) - 1))
+                              : -1;
+  }
+}
+
+inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+constexpr int32_t kMostRequests = 1 << 24;
+
+}  // namespace pages_impl
+
+extern "C" size_t sdv_kv_pages_workspace_bytes(int32_t B) {
+  using namespace pages_impl;
+  if (B < 1 || B >= kMostRequests) return 0;
+  return up256((size_t)B * kWaves * 4) + up256((size_t)B * 4) + 256;
+}
+
+extern "C" int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, int32_t page_size,
+                            const int32_t* cache_len, int64_t n_draft_rows, const int32_t* ragged_offsets,
+                            int64_t n_pages, int32_t* free_pages, int32_t* free_state, int32_t window, int32_t sinks,
+                            int32_t* placed, int64_t* slots, void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace pages_impl;
+  auto aligned = [](const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; };
+  if (!page_table || !cache_len || !ragged_offsets || !free_pages || !free_state || !placed || B < 1 || n_draft_rows < 0 ||
+      max_pages < 1 || n_pages < 1 || page_size < 1 || page_size > 1024 || (page_size & (page_size - 1)) || window < 0 ||
+      sinks < 0 || !aligned(page_table, 4) || !aligned(cache_len, 4) || !aligned(ragged_offsets, 4) ||
+      !aligned(free_pages, 4) || !aligned(free_state, 4) || !aligned(placed, 4) || !aligned(slots, 8))
+    return SDV_ERR_INVALID_ARG;
+  if (B >= kMostRequests || too_many(B, kThreads) || n_draft_rows + B > INT32_MAX - 1024 || n_pages > INT32_MAX ||
+      max_pages > INT32_MAX - 1024)
+    return SDV_ERR_LIMIT;
+  // what is written lies apart from everything else
+  struct Span {
+    const void* at;
+    int64_t bytes;
+  };
+  const size_t need = sdv_kv_pages_workspace_bytes(B);
+  const Span span[] = {{page_table, (int64_t)B * max_pages * 4}, {free_pages, n_pages * 4}, {free_state, 8},
+                       {placed, (int64_t)B * 4}, {slots, slots ? (n_draft_rows + B) * 8 : 0},
+                       {workspace, workspace ? (int64_t)need : 0},
+                       {cache_len, (int64_t)B * 4}, {ragged_offsets, ((int64_t)B + 1) * 4}};
+  for (int x = 0; x < 6; ++x)
+    for (int y = x + 1; y < 8; ++y)
+      if (span[x].bytes && span[y].bytes && overlap(span[x].at, span[x].bytes, span[y].at, span[y].bytes))
+        return SDV_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return SDV_ERR_WORKSPACE;
+  PagesArgs a;
+  a.table = page_table;
+  a.len = cache_len;
+  a.cu = ragged_offsets;
+  a.ring = free_pages;
+  a.state = free_state;
+  a.placed = placed;
+  a.slots = slots;
+  a.freed = static_cast<int32_t*>(workspace);
+  a.wanted = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + up256((size_t)B * kWaves * 4));
+  a.before = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + up256((size_t)B * kWaves * 4) + up256((size_t)B * 4));
+  a.n_d = n_draft_rows;
+  a.n_pages = n_pages;
+  a.B = B;
+  a.max_pages = max_pages;
+  a.page_log2 = log2_of(page_size);
+  a.window = window;
+  a.sinks = sinks;
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  hipLaunchKernelGGL(count, dim3((unsigned)B), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL(place, dim3((unsigned)B), dim3(kThreads), 0, s, a);
+  return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
+}
