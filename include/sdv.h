@@ -679,8 +679,8 @@ int sdv_kv_settle8(const sdv_cache8* cache, int32_t n_layers, int32_t B, int64_t
  *      that has none, if the requests up to it together take no more than the ring held before the call.  If they
  *      take more it takes none, and no later request takes any.
  * Pages that a call returns can be taken by the next call.
- *   placed [B] int32   1 if all of the request's rows have pages now, 0 if it took too many or its rows lie beyond the table,
- *                      -1 for one that has ended or is passed over
+ *   placed [B] int32   1 if all of the request's rows have pages now, 0 if not (too few pages, rows beyond the table, or the
+ *                      request has ended), -1 for one that is passed over
  *   slots [n_draft_rows + B] int64, or NULL     page * page_size + place of each row of a placed request; -1 for other rows
  * A page is one request's alone.  An entry outside [0, n_pages) is no page, and one taken from the ring is put down as it is, its slots -1.
  * A request with offsets that are not valid, or L_i outside [-1, INT32_MAX - 1024 - K), is passed over and its entries left as

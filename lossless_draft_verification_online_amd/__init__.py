@@ -733,7 +733,7 @@ def kv_pages(page_table: torch.Tensor, cache_len: torch.Tensor, offsets: torch.T
     free_pages (int32 [n_pages]) and free_state (int32 [2]: its first place and how many pages it holds) are brought up to
     date in place: pages that no row sees under ``window`` and ``sinks`` go back to the ring, and the coming rows' slots
     (offsets as for kv_append, cache_len -1 for a request that has ended) get pages.  Returns (placed int32 [B]: 1 where
-    all rows of a request have pages, 0 where not, -1 for one that has ended or is not valid; slots int64 [n_draft_rows
+    all rows of a request have pages, 0 where not or where it has ended, -1 for one that is not valid; slots int64 [n_draft_rows
     + B]: page * page_size + place of each row of a placed request, else -1)."""
     index = page_table.get_device()
     if index < 0:

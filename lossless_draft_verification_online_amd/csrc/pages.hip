@@ -140,7 +140,7 @@ __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
   taken = group_sum(taken, sum_s);
   const int32_t wants = a.wanted[i];
   const bool is_placed = ring && k.fits(a) && (wants == 0 || taken + wants <= (uint64_t)held);
-  if (t == 0) a.placed[i] = !ring || !k.open ? -1 : (is_placed ? 1 : 0);
+  if (t == 0) a.placed[i] = !ring || !k.known ? -1 : (is_placed ? 1 : 0);
 
   if (i == 0 && ring) {  // the ring's state behind the call
     uint64_t all = 0, sum = 0, most = 0;

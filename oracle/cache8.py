@@ -181,8 +181,8 @@ def pages(table, page_size, cache_len, n_draft_rows, cu, ring, state, window=0, 
         back = [k for k in range(width) if is_page[k] and k not in needed]
         returned += [int(table[i, k]) for k in back]
         want = []
+        placed[i] = 0
         if L >= 0:
-            placed[i] = 0
             if last < width:
                 want = [k for k in range(L // page_size, last + 1) if not is_page[k]]
                 wanted += len(want)

@@ -71,7 +71,7 @@ def test_requests_that_end_and_that_are_rolled_back():
     p.check()
     p.len[:] = [41, -1, 20, 0, -1]  # drafts that were not taken, ended requests, one that starts again
     got = p.check()
-    assert got[3].tolist() == [1, -1, 1, 1, -1] and (got[0][[1, 4]] == -1).all()
+    assert got[3].tolist() == [1, 0, 1, 1, 0] and (got[0][[1, 4]] == -1).all()
     p.check()
 
 

@@ -58,7 +58,7 @@ def test_pages_by_hand():
     # request 0: 3 tokens, 3 more rows on pages of 4; request 1 rolled back to 2; request 2 ended
     t, r, s, placed, slots = oracle.pages(table, 4, [3, 2, -1], 2, [0, 2, 2, 2], ring, state)
     assert t.tolist() == [[4, 1, -1, -1], [2, -1, -1, -1], [-1, -1, -1, -1]]
-    assert placed.tolist() == [1, 1, -1] and slots.tolist() == [19, 4, 5, 10, -1]
+    assert placed.tolist() == [1, 1, 0] and slots.tolist() == [19, 4, 5, 10, -1]
     assert s.tolist() == [2, 6] and [int(r[(2 + x) % 10]) for x in range(6)] == [3, 8, 7, 0, 5, 6]
     # under a window of 2 and 1 sink: the page of slots 0 .. 3 stays, that of 4 .. 7 goes
     t, r, s, placed, slots = oracle.pages([[4, 5, 6, -1]], 4, [11], 1, [0, 1], ring, state, window=2, sinks=1)
