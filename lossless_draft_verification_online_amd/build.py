@@ -15,6 +15,7 @@ SOURCES = [os.path.join(PKG, "csrc", "sdv.hip"), os.path.join(PKG, "csrc", "comm
            os.path.join(PKG, "csrc", "sdcp_uniforms.cpp")]
 DEPENDS = SOURCES + [os.path.join(PKG, "csrc", "sdv_device.hpp"), os.path.join(PKG, "csrc", "split.hpp"),
                      os.path.join(PKG, "csrc", "cache_view.hpp"), os.path.join(PKG, "csrc", "attend_unit.hpp"),
+                     os.path.join(PKG, "csrc", "attend_rows.hpp"),
                      os.path.join(PKG, "csrc", "cache8_view.hpp"), os.path.join(PKG, "csrc", "launch.hpp"),
                      os.path.join(ROOT, "include", "sdv.h")]
 LIBRARY = os.path.join(PKG, "libsdv.so")

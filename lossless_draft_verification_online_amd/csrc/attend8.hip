@@ -2,20 +2,24 @@
 // head: sdv_attend8.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
 
-#include "attend_unit.hpp"
+#include "attend_rows.hpp"
 
 namespace attend8_impl {
 
 using namespace sdv;
 using namespace attend_impl;
 
-enum Mode { kUnits, kRanges, kSmallPages };
+enum Mode { kUnits, kRanges, kSmallPages, kRows };
+
+static int64_t kManyColumns_() { const char* e = getenv("KC"); return e ? atoll(e) : 96; }
+constexpr int64_t kManyWorkgroups = 128;
 
 constexpr int64_t kShort = 32, kSomeUnits = 64;
 constexpr int64_t kManyUnits = 2048;
 constexpr int64_t kFewUnits = 128;
-constexpr int64_t kPlaces = 512;
+static int64_t places() { const char* e = getenv("KP"); return e ? atoll(e) : 512; }
 
 struct Plan {
   int qb;
@@ -28,7 +32,8 @@ struct Plan {
 
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int32_t window, int32_t sinks) {
+inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int32_t window, int32_t sinks,
+                    bool tree) {
   const int64_t G = n_q / c->n_kv_heads, rows = n_d + B, mean = (rows * G + B - 1) / B;
   int64_t seen = (int64_t)c->max_pages * c->page_size;
   if (window && (int64_t)window + sinks + rows / B < seen) seen = (int64_t)window + sinks + rows / B;
@@ -36,6 +41,12 @@ inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int
   auto units_of = [&](int64_t columns) { return (mean + columns - 1) / columns * B * c->n_kv_heads; };
   Plan p = {};
   p.qb = 1;
+  if (!tree && c->dtype == SDV_BF16 && c->head_dim <= 128 && c->page_size >= 16 && mean >= kManyColumns_() &&
+      units_of(kRowsColumns) >= kManyWorkgroups) {
+    p.mode = kRows;
+    p.tiles = rows * G / kRowsColumns + B;
+    return p;
+  }
   const bool pairs = mean > 16 && !(c->dtype == SDV_FP32 && c->head_dim > 64);
   const bool split = tokens > (units_of(16) < kSomeUnits ? kShort : 2 * kShort) && B <= 512 &&
                      rows <= 64 * (int64_t)B && units_of(32) < kManyUnits;
@@ -44,7 +55,7 @@ inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int
   p.tiles = rows * G / (16 * p.qb) + B;
   if (p.mode == kRanges) {
     const int64_t units = units_of(16 * p.qb), groups = (units * tokens + kStreamWaves - 1) / kStreamWaves;
-    p.ranges = (int32_t)(groups < kPlaces ? groups : kPlaces);
+    p.ranges = (int32_t)(groups < places() ? groups : places());
     p.pieces = (int32_t)((p.ranges + units - 1) / units) + 1;
     const size_t n = (size_t)2 * p.ranges * 16 * p.qb;
     p.part_bytes = up256(n * c->head_dim * 4);
@@ -62,16 +73,23 @@ int launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
     hipLaunchKernelGGL((attend_units<E, D, QB, kStreamWaves, true, true>), units, threads, 0, s, a);
   } else {
     hipLaunchKernelGGL((attend_ranges<E, D, QB, true>), dim3((unsigned)a.ranges), threads, 0, s, a);
+    if (a.ranges == 1) return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
     if (p.pieces > 16)
-      hipLaunchKernelGGL((join<E, D, QB, true>), dim3(units.x, 16 * QB), dim3(kJoinWaves * kWave), 0, s, a);
+      hipLaunchKernelGGL((join<E, D, QB, true, true>), dim3(units.x, 16 * QB), dim3(kJoinWaves * kWave), 0, s, a);
     else
-      hipLaunchKernelGGL((join<E, D, QB, false>), dim3(units.x, 16 * QB / kJoin), dim3(kJoinWaves * kWave), 0, s, a);
+      hipLaunchKernelGGL((join<E, D, QB, false, true>), dim3((unsigned)a.ranges - 1, 16 * QB / kJoin), dim3(kJoinWaves * kWave), 0, s, a);
   }
   return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
 }
 
 template <class E, int D>
 int launch_columns(const AttendArgs& a, const Plan& p, hipStream_t s) {
+  if constexpr (E::kBytes == 2 && D <= 128) {
+    if (p.mode == kRows) {
+      hipLaunchKernelGGL((attend_rows<D, true>), dim3((unsigned)(a.tiles * a.cache.n_heads)), dim3(kRowsWaves * kWave), 0, s, a);
+      return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
+    }
+  }
   if constexpr (E::kBytes == 2 || D <= 64) {
     if (p.qb == 2) return launch<E, D, 2>(a, p, s);
   }
@@ -87,7 +105,7 @@ int launch_dim(const AttendArgs& a, int32_t D, const Plan& p, hipStream_t s) {
 inline int check(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int32_t window, int32_t sinks) {
   if (n_q < 1 || n_q % c->n_kv_heads || window < 0 || sinks < 0) return SDV_ERR_INVALID_ARG;
   if (n_q > 1024 || (n_d + B) * (n_q / c->n_kv_heads) > INT32_MAX - 1024) return SDV_ERR_LIMIT;
-  return plan_of(c, B, n_d, n_q, window, sinks).tiles * c->n_kv_heads > INT32_MAX ? SDV_ERR_LIMIT : SDV_OK;
+  return plan_of(c, B, n_d, n_q, window, sinks, true).tiles * c->n_kv_heads > INT32_MAX ? SDV_ERR_LIMIT : SDV_OK;
 }
 
 }  // namespace attend8_impl
@@ -99,7 +117,7 @@ extern "C" size_t sdv_attend8_workspace_bytes(const sdv_cache8* cache, int32_t B
       cache->cache.page_size < 1 || n_draft_rows + B > INT32_MAX ||
       check(&cache->cache, B, n_draft_rows, n_q_heads, window, sinks) != SDV_OK)
     return 0;
-  return plan_of(&cache->cache, B, n_draft_rows, n_q_heads, window, sinks).bytes;
+  return plan_of(&cache->cache, B, n_draft_rows, n_q_heads, window, sinks, true).bytes;  // without a tree: that or less
 }
 
 extern "C" int sdv_attend8(const sdv_cache8* cache, int32_t B, int64_t n_draft_rows, const int32_t* ragged_offsets,
@@ -117,8 +135,8 @@ extern "C" int sdv_attend8(const sdv_cache8* cache, int32_t B, int64_t n_draft_r
       query_stride < (int64_t)n_q_heads * c->head_dim || !(scale - scale == 0.0f))
     return SDV_ERR_INVALID_ARG;
   if (query_stride > ((int64_t)1 << 31)) return SDV_ERR_LIMIT;
-  const Plan p = plan_of(c, B, n_draft_rows, n_q_heads, window, sinks);
-  static_assert(kStreamWaves == kJoinWaves, "one bound for every launch");
+  const Plan p = plan_of(c, B, n_draft_rows, n_q_heads, window, sinks, parents != nullptr);
+  static_assert(kStreamWaves == kJoinWaves && kStreamWaves == kRowsWaves, "one bound for every launch");
   if (too_many(p.tiles * c->n_kv_heads, kStreamWaves * kWave)) return SDV_ERR_LIMIT;
   if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return SDV_ERR_WORKSPACE;
   AttendArgs a;

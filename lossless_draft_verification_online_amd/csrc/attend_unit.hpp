@@ -180,6 +180,7 @@ struct Stream {
   int64_t total;                 // items of the batch
   int64_t length;                // of a range
 };
+template <int kCost>
 __device__ __forceinline__ Stream stream_of(const AttendArgs& a, int32_t columns) {
   const int lane = threadIdx.x & (kWave - 1);
   Stream s;
@@ -191,7 +192,7 @@ __device__ __forceinline__ Stream stream_of(const AttendArgs& a, int32_t columns
     if (i >= a.B) break;
     const Work w = work_of(a, i, columns);
     if (k == 0) s.own = w;
-    items += (uint64_t)(w.units(a) * w.n);
+    items += (uint64_t)(w.units(a) * (w.n + kCost));
     units += (uint64_t)w.units(a);
   }
   const uint64_t inc = wave_inclusive_scan(items);
@@ -851,11 +852,17 @@ __global__ __launch_bounds__(kWaves* kWave, (kMinWaves<E, D, QB>)) void attend_u
 
 // A workgroup per range of the batch's work.
 constexpr int kStreamWaves = 4;
+//
+// A unit costs more than its tiles: its pages are found, its queries loaded and its waves joined.  For caches in 8 bits it
+// counts as that many tiles more, or a range of many short units would end long after the others (64 requests of 4096 visible
+// tokens and one that is empty: 190 us without, KKK with).
+template <bool k8>
+constexpr int kUnitCost = k8 ? 12 : 0;
 template <class E, int D, int QB, bool k8>
 __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void attend_ranges(AttendArgs a) {
-  constexpr int kColumns = 16 * QB;
+  constexpr int kColumns = 16 * QB, kCost = kUnitCost<k8>;
   __shared__ Scratch<E, D, QB, kStreamWaves, k8> sh;
-  const Stream s = stream_of(a, kColumns);
+  const Stream s = stream_of<kCost>(a, kColumns);
   const int64_t range = unit_of_block(blockIdx.x, gridDim.x);
   const int64_t end = (range + 1) * s.length < s.total ? (range + 1) * s.length : s.total;
   int64_t p = range * s.length;
@@ -866,15 +873,22 @@ __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void at
   int64_t base = (int64_t)lane_value((uint64_t)s.before, who);
   while (p < end && i < a.B) {
     const Work w = work_at(a, s, i, kColumns);
-    const int64_t items = w.units(a) * w.n;
+    const int32_t span = w.n + kCost;
+    const int64_t items = w.units(a) * span;
     if (p >= base + items) {
       base += items;
       ++i;
       continue;
     }
-    const uint32_t unit = (uint32_t)((p - base) / w.n);
-    const int32_t q_lo = (int32_t)(p - base - (int64_t)unit * w.n);
-    const int32_t q_hi = q_lo + (end - p) < w.n ? (int32_t)(q_lo + (end - p)) : w.n;
+    const uint32_t unit = (uint32_t)((p - base) / span);
+    int32_t q_lo = (int32_t)(p - base - (int64_t)unit * span);
+    int32_t q_hi = q_lo + (end - p) < span ? (int32_t)(q_lo + (end - p)) : span;
+    p += q_hi - q_lo;
+    if constexpr (kCost > 0) {  // the cost comes before the tiles
+      q_lo = q_lo > kCost ? q_lo - kCost : 0;
+      q_hi -= kCost;
+      if (q_hi <= 0) continue;
+    }
     TileOf at;
     at.r = request_with(w, i);
     at.c0 = (int32_t)(unit / (uint32_t)a.cache.n_heads) * kColumns;
@@ -882,7 +896,6 @@ __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void at
     attend_unit<E, D, QB, kStreamWaves, true, k8>(a, sh, at, w.len, (int32_t)(unit % (uint32_t)a.cache.n_heads), true,
                                               q_lo, q_hi,
                                               whole ? -1 : 2 * range + (first ? 1 : 0));
-    p += q_hi - q_lo;
     __syncthreads();
   }
 }
@@ -893,30 +906,52 @@ __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void at
 constexpr int kJoinWaves = 4;
 constexpr int kJoin = 8;
 
-template <class E, int D, int QB, bool kMany>
+template <class E, int D, int QB, bool kMany, bool k8>
 __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
   constexpr int kColumns = 16 * QB, kLanes = D / 4, kRows = kWave / kLanes;  // pieces a wave reads at once
   __shared__ float o_s[kJoinWaves][D], stat_s[kJoinWaves][2];
   const int t = threadIdx.x, lane = t & (kWave - 1), k = lane % kLanes;
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
-  const Stream s = stream_of(a, kColumns);
+  constexpr int kCost = kUnitCost<k8>;
+  const Stream s = stream_of<kCost>(a, kColumns);
   const int64_t u = blockIdx.x;
-  const int who = 63 - __builtin_clzll(__ballot(s.units_before <= u));
-  int64_t begin = (int64_t)lane_value((uint64_t)s.before, who);
-  int64_t unit = u - (int64_t)lane_value((uint64_t)s.units_before, who);
-  int32_t i = who * s.per;
+  int64_t begin, unit, r_lo;
+  int32_t i, pieces;
   Work w;
-  for (;; ++i) {
-    if (i >= a.B) return;
-    w = work_at(a, s, i, kColumns);
-    if (unit < w.units(a)) break;
-    unit -= w.units(a);
-    begin += w.units(a) * w.n;
+  if constexpr (k8 && !kMany) {  // a workgroup per end of a range: the unit that it is the first to cut, if it does
+    const int64_t cut = (u + 1) * s.length;
+    if (cut >= s.total) return;
+    const int who = 63 - __builtin_clzll(__ballot(s.before <= cut));
+    begin = (int64_t)lane_value((uint64_t)s.before, who);
+    for (i = who * s.per;; ++i) {
+      if (i >= a.B) return;
+      w = work_at(a, s, i, kColumns);
+      const int64_t items = w.units(a) * (w.n + kCost);
+      if (cut < begin + items) break;
+      begin += items;
+    }
+    unit = (cut - begin) / (w.n + kCost);
+    begin += unit * (w.n + kCost) + kCost;
+    if (cut <= begin) return;
+    r_lo = begin / s.length;
+    if (r_lo != u) return;
+    pieces = (int32_t)((begin + w.n - 1) / s.length - r_lo) + 1;
+  } else {
+    const int who = 63 - __builtin_clzll(__ballot(s.units_before <= u));
+    begin = (int64_t)lane_value((uint64_t)s.before, who);
+    unit = u - (int64_t)lane_value((uint64_t)s.units_before, who);
+    for (i = who * s.per;; ++i) {
+      if (i >= a.B) return;
+      w = work_at(a, s, i, kColumns);
+      if (unit < w.units(a)) break;
+      unit -= w.units(a);
+      begin += w.units(a) * (w.n + kCost);
+    }
+    begin += unit * (w.n + kCost) + kCost;
+    r_lo = begin / s.length;
+    pieces = (int32_t)((begin + w.n - 1) / s.length - r_lo) + 1;
+    if (pieces == 1) return;
   }
-  begin += unit * w.n;
-  const int64_t r_lo = begin / s.length;
-  const int32_t pieces = (int32_t)((begin + w.n - 1) / s.length - r_lo) + 1;
-  if (pieces == 1) return;
   const Request r = request_with(w, i);
   const int32_t head = (uint32_t)unit % (uint32_t)a.cache.n_heads;
   const int32_t c0 = (int32_t)((uint32_t)unit / (uint32_t)a.cache.n_heads) * kColumns, columns = (r.k + 1) * a.G;
