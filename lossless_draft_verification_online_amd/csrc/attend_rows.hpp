@@ -147,18 +147,23 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   };
   // The codes of the wave's rows, where direct loads put them at the front of the rows' place, and their bf16 values
   // in that place: both are the wave's own until the barrier.
+  // A lane's codes go to pieces p and p + 1 of its row, neighbours in the permuted order too (p is even, and so is what it is
+  // combined with); its rows are a multiple of 8 apart: one address serves all.
+  const int codes_off = 16 * wave * kLine + lane * 16;
+  const int wide_row = lane / kCachePieces;
+  const int wide_off = (16 * wave + wide_row) * kLine + piece_of<D>(wide_row, 2 * (lane % kCachePieces)) * 16;
   auto codes_at = [&](const char* to, u32x4 (&v)[kLoads]) {
 #pragma unroll
-    for (int x = 0; x < kLoads; ++x) v[x] = *reinterpret_cast<const u32x4*>(to + 16 * wave * kLine + x * 1024 + lane * 16);
+    for (int x = 0; x < kLoads; ++x) v[x] = *reinterpret_cast<const u32x4*>(to + codes_off + x * 1024);
   };
   auto widen = [&](const u32x4 (&v)[kLoads], float scale, int lane_0, char* to) {
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) {
-      const int row = x * kLoadRows + lane / kCachePieces, p = 2 * (lane % kCachePieces);
-      const float by = __shfl(scale, lane_0 + row);
-      char* const dst = to + (16 * wave + row) * kLine;
-      *reinterpret_cast<bf16x8*>(dst + piece_of<D>(row, p) * 16) = bf16_of_codes(v[x].x, v[x].y, by);
-      *reinterpret_cast<bf16x8*>(dst + piece_of<D>(row, p + 1) * 16) = bf16_of_codes(v[x].z, v[x].w, by);
+      const float by = __int_as_float(
+          __builtin_amdgcn_ds_bpermute(4 * wide_row + 4 * (lane_0 + x * kLoadRows), __float_as_int(scale)));
+      char* const dst = to + wide_off + x * kLoadRows * kLine;
+      *reinterpret_cast<bf16x8*>(dst) = bf16_of_codes(v[x].x, v[x].y, by);
+      *reinterpret_cast<bf16x8*>(dst + 16) = bf16_of_codes(v[x].z, v[x].w, by);
     }
   };
 
@@ -211,7 +216,15 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
 
   typedef f32x16 Scores[2];  // element e of a block: token 8 (e / 4) + 4 half + e mod 4
   const f32x16 none16 = {};
+  // 8 bits: a row's pieces differ in the bits above 2^5 (keys) or 2^6 (values), which the permutation flips: a step's address is
+  // made of one by an exclusive or.  `here` keeps the compiler from holding all of them, for which there are no registers (what is
+  // spilled and loaded again waits for the direct loads).
+  const int key_off = col * kLine + piece_of<D>(col, half) * 16;
+  const int value_token = 4 * half + ((lane & 15) >> 2);
+  const int value_off = value_token * kLine + piece_of<D>(value_token, 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1)) * 16 + (lane & 1) * 8;
+  int key_here = 0, value_here = 0;
   auto key = [&](const char* k_s, int blk, int s) {
+    if constexpr (k8) return *reinterpret_cast<const bf16x8*>(k_s + (key_here ^ (32 * s)) + 32 * blk * kLine);
     const int token = 32 * blk + col;
     return *reinterpret_cast<const bf16x8*>(k_s + token * kLine + piece_of<D>(token, 2 * s + half) * 16);
   };
@@ -221,6 +234,12 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     const int g = (lane >> 4) & 1, in = lane & 15, token = 16 * s + 4 * half + (in >> 2);
 #pragma unroll
     for (int d = 0; d < kDB; ++d) {
+      if constexpr (k8) {
+        char* const r = v_s + (value_here ^ (64 * d)) + 16 * s * kLine;
+        v[d][0] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)r);
+        v[d][1] = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4*)(r + 8 * kLine));
+        continue;
+      }
       const int pc = 4 * d + 2 * g + ((in >> 1) & 1);
       char* const r0 = v_s + token * kLine + piece_of<D>(token, pc) * 16 + (in & 1) * 8;
       char* const r1 = v_s + (token + 8) * kLine + piece_of<D>(token + 8, pc) * 16 + (in & 1) * 8;
@@ -234,6 +253,11 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   // of what its buffer holds, which nothing uses).
   auto tile = [&](int32_t n, Scores& sc, Scores& ahead, char* k_s, char* v_s, char* k_next, char* v_next) {
     const int32_t s0 = start(n);
+    if constexpr (k8) {
+      key_here = key_off;
+      value_here = value_off;
+      asm volatile("" : "+v"(key_here), "+v"(value_here));
+    }
     // a value no row sees is 0: what lies there may be NaN
     const int32_t first = s0 + 16 * wave;
     const bool held = page >= 0 && (first + 16 <= span.near_end || (first >= span.lo && first + 16 <= span.hi));
@@ -379,6 +403,7 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
   __builtin_amdgcn_s_waitcnt(0x0f70);  // the direct loads, of a request without tiles too: its zeros take their place
   if (n_tiles > 0) {
     Scores sc_0, sc_1;
+    key_here = key_off;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const char* const from = (s < kSteps / 2 ? k_1 : v_1) + 16 * wave * kLine;
