@@ -27,7 +27,8 @@ struct Plan {
   int32_t ranges;
   int32_t pieces;  // of a unit, about
   int64_t tiles;
-  size_t part_bytes, bytes;
+  bool many;  // cut into more than a few
+  size_t part_bytes, stat_bytes, bytes;
 };
 
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -59,7 +60,10 @@ inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int
     p.pieces = (int32_t)((p.ranges + units - 1) / units) + 1;
     const size_t n = (size_t)2 * p.ranges * 16 * p.qb;
     p.part_bytes = up256(n * c->head_dim * 4);
-    p.bytes = p.part_bytes + up256(n * 8);
+    p.stat_bytes = up256(n * 8);
+    p.many = p.pieces > 16;
+    const size_t cuts = (p.many ? (size_t)p.tiles * c->n_kv_heads : (size_t)p.ranges) + 1;
+    p.bytes = p.part_bytes + p.stat_bytes + up256(cuts * sizeof(Cut));
   }
   return p;
 }
@@ -74,7 +78,7 @@ int launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
   } else {
     hipLaunchKernelGGL((attend_ranges<E, D, QB, true>), dim3((unsigned)a.ranges), threads, 0, s, a);
     if (a.ranges == 1) return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
-    if (p.pieces > 16)
+    if (p.many)
       hipLaunchKernelGGL((join<E, D, QB, true, true>), dim3(units.x, 16 * QB), dim3(kJoinWaves * kWave), 0, s, a);
     else
       hipLaunchKernelGGL((join<E, D, QB, false, true>), dim3((unsigned)a.ranges - 1, 16 * QB / kJoin), dim3(kJoinWaves * kWave), 0, s, a);
@@ -158,6 +162,8 @@ extern "C" int sdv_attend8(const sdv_cache8* cache, int32_t B, int64_t n_draft_r
   a.out = static_cast<char*>(out);
   a.part = static_cast<float*>(workspace);
   a.stats = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.part_bytes);
+  a.many = p.many;
+  a.cuts = reinterpret_cast<Cut*>(static_cast<char*>(workspace) + p.part_bytes + p.stat_bytes);
   a.key_scales = cache->key_scales;
   a.value_scales = cache->value_scales;
   a.block_log2 = log2_of(cache->block);

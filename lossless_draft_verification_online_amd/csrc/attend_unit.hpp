@@ -47,6 +47,12 @@ struct AttendArgs {
   const uint8_t* key_scales;
   const uint8_t* value_scales;
   int32_t block_log2;
+  bool many;           // cuts are told by unit
+  struct Cut* cuts;    // [ranges + 1], or [units + 1]; the last of them the number of units
+};
+// A unit that ranges cut, as its first range tells the join.
+struct Cut {
+  int32_t pieces, first_range, row0, k, head, c0, pad[2];  // pieces 0 or 1: it is whole, or the range begins none
 };
 
 // A cache in 8 bits holds e4m3 codes with a power of two as the scale of a block of tokens and head.  A code times its
@@ -177,7 +183,7 @@ struct Stream {
   int32_t per;                   // requests per lane
   Work own;                      // of the lane's first
   int64_t before, units_before;  // items, and units, before the lane's requests
-  int64_t total;                 // items of the batch
+  int64_t total, units;          // items, and units, of the batch
   int64_t length;                // of a range
 };
 template <int kCost>
@@ -197,7 +203,9 @@ __device__ __forceinline__ Stream stream_of(const AttendArgs& a, int32_t columns
   }
   const uint64_t inc = wave_inclusive_scan(items);
   s.before = (int64_t)(inc - items);
-  s.units_before = (int64_t)(wave_inclusive_scan(units) - units);
+  const uint64_t inc_units = wave_inclusive_scan(units);
+  s.units_before = (int64_t)(inc_units - units);
+  s.units = (int64_t)lane_value(inc_units, kWave - 1);
   s.total = (int64_t)lane_value(inc, kWave - 1);
   s.length = (s.total + a.ranges - 1) / a.ranges;
   return s;
@@ -360,6 +368,33 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   const int32_t c_last = at.c0 + S::kColumns < columns ? at.c0 + S::kColumns - 1 : columns - 1;
   const int32_t j_lo = (uint32_t)at.c0 / (uint32_t)a.G, j_hi = (uint32_t)c_last / (uint32_t)a.G;  // rows of this tile
   bool ok = len_fits(len, K);
+  // the tiles are those of the rows, or of all the request's rows; what this tile's rows see of them is the same
+  const int32_t tail_lo = a.parents ? 0 : j_lo, tail_hi = a.parents ? K : j_hi;
+  const Span own = span_of(len, tail_lo, tail_hi, a.window, a.sinks);
+  const Span span = pos_all ? span_of(len, 0, K, a.window, a.sinks) : own;
+  const int32_t lo = own.lo, hi = own.hi, near_end = own.near_end, n_near = span.n_near, t_lo = span.t_lo;
+  if (!pos_all) {
+    w_lo = 0;
+    w_hi = span.n;
+  }
+  if (!ok) w_hi = w_lo;
+  auto start = [&](int32_t n) { return (n < n_near ? n : n - n_near + t_lo) * kTile; };
+  auto held = [&](int32_t s) { return (s >= lo && s < hi) || s < near_end; };
+  // The table's entry of token lane & 31 as it is, checked when it is used: a check would wait for it, and for
+  // the keys and values asked for before it.
+  const int32_t* const table = a.cache.table + (int64_t)i * a.cache.max_pages;
+  auto entry_at = [&](int32_t n) -> int32_t {
+    const int32_t s = start(n) + (lane & (kTile - 1)), k = s >> a.cache.page_log2;
+    return n < w_hi && (kWholePages || held(s)) && k < a.cache.max_pages ? table[k] : -1;
+  };
+  // Everything waits for the first pages: 8 bits ask for them before the queries (16 requests of 4096 tokens and one row
+  // 34.9 us for KKK behind them; caches of the rows' type as they were).
+  int32_t entry_0 = -1, entry_1 = -1;
+  if constexpr (k8) {
+    entry_0 = entry_at(w_lo + wave);
+    entry_1 = entry_at(w_lo + wave + kWaves);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   if (a.parents && ok) {
     ok = tree_depths(a.parents, at.r, parent_s, depth_s);
     if (ok) {
@@ -429,19 +464,8 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
     }
   }
 
-  // the tiles are those of the rows, or of all the request's rows; what this tile's rows see of them is the same
-  const int32_t tail_lo = a.parents ? 0 : j_lo, tail_hi = a.parents ? K : j_hi;
-  const Span own = span_of(len, tail_lo, tail_hi, a.window, a.sinks);
-  const Span span = pos_all ? span_of(len, 0, K, a.window, a.sinks) : own;
-  const int32_t lo = own.lo, hi = own.hi, near_end = own.near_end, n_near = span.n_near, t_lo = span.t_lo;
-  if (!pos_all) {
-    w_lo = 0;
-    w_hi = span.n;
-  }
   if (!ok) w_hi = w_lo;
   const int32_t far = len + tail_hi;  // the largest position
-  auto start = [&](int32_t n) { return (n < n_near ? n : n - n_near + t_lo) * kTile; };
-  auto held = [&](int32_t s) { return (s >= lo && s < hi) || s < near_end; };
 
   f32x4 acc[QB][kDB];
   float m[QB], l[QB];
@@ -468,13 +492,6 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   uint32_t byte_1 = 0;  // the next tile's scale of token lane & 31: of its keys, in the upper half of its values
   float scale = 0.0f;
   float vf[kBf16 ? 1 : 8][kDB];
-  // The table's entry of token lane & 31 as it is, checked when it is used: a check would wait for it, and for
-  // the keys and values asked for before it.
-  const int32_t* const table = a.cache.table + (int64_t)i * a.cache.max_pages;
-  auto entry_at = [&](int32_t n) -> int32_t {
-    const int32_t s = start(n) + (lane & (kTile - 1)), k = s >> a.cache.page_log2;
-    return n < w_hi && (kWholePages || held(s)) && k < a.cache.max_pages ? table[k] : -1;
-  };
   auto page_of = [&](int32_t entry) { return entry >= 0 && entry < a.cache.n_pages ? entry : -1; };
   // the lane's byte offsets within 16 tokens' rows
   const uint32_t k_off = col * kLine + 16 * g;
@@ -539,7 +556,11 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
 
   int32_t n = w_lo + wave;
   // the pages of two tiles ahead: a page read behind a tile's loads would wait for them
-  int32_t page = page_of(entry_at(n)), entry_1 = entry_at(n + kWaves);
+  if constexpr (!k8) {
+    entry_0 = entry_at(n);
+    entry_1 = entry_at(n + kWaves);
+  }
+  int32_t page = page_of(entry_0);
   if (n < w_hi) {
     if constexpr (k8) load_scales(n, page);
     load_keys(n, page);
@@ -866,17 +887,26 @@ __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void at
   const int64_t range = unit_of_block(blockIdx.x, gridDim.x);
   const int64_t end = (range + 1) * s.length < s.total ? (range + 1) * s.length : s.total;
   int64_t p = range * s.length;
+  Cut cut = {};
+  if constexpr (k8) {
+    // requests that do not lie in their order can have more units than there is room for
+    const int64_t room = a.tiles * a.cache.n_heads;
+    if (a.many && range == 0 && threadIdx.x == 0) a.cuts[room].pieces = (int32_t)(s.units < room ? s.units : room);
+    if (p >= end && !a.many && threadIdx.x == 0) a.cuts[range] = cut;
+  }
   if (p >= end) return;
   // the request of p, then on from one to the next
   const int who = 63 - __builtin_clzll(__ballot(s.before <= p));
   int32_t i = who * s.per;
   int64_t base = (int64_t)lane_value((uint64_t)s.before, who);
+  int64_t units = k8 ? (int64_t)lane_value((uint64_t)s.units_before, who) : 0;  // before the request
   while (p < end && i < a.B) {
     const Work w = work_at(a, s, i, kColumns);
     const int32_t span = w.n + kCost;
     const int64_t items = w.units(a) * span;
     if (p >= base + items) {
       base += items;
+      if constexpr (k8) units += w.units(a);
       ++i;
       continue;
     }
@@ -893,10 +923,25 @@ __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void at
     at.r = request_with(w, i);
     at.c0 = (int32_t)(unit / (uint32_t)a.cache.n_heads) * kColumns;
     const bool first = q_lo == 0, whole = first && q_hi == w.n;
+    if constexpr (k8) {
+      if (first) {
+        const int64_t begin = base + (int64_t)unit * span + kCost;
+        cut.pieces = whole ? 1 : (int32_t)((uint64_t)(begin + w.n - 1) / (uint64_t)s.length - range) + 1;
+        cut.first_range = (int32_t)range;
+        cut.row0 = w.first + i;
+        cut.k = w.k;
+        cut.head = (int32_t)(unit % (uint32_t)a.cache.n_heads);
+        cut.c0 = at.c0;
+        if (a.many && threadIdx.x == 0 && units + unit < a.tiles * a.cache.n_heads) a.cuts[units + unit] = cut;
+      }
+    }
     attend_unit<E, D, QB, kStreamWaves, true, k8>(a, sh, at, w.len, (int32_t)(unit % (uint32_t)a.cache.n_heads), true,
                                               q_lo, q_hi,
                                               whole ? -1 : 2 * range + (first ? 1 : 0));
     __syncthreads();
+  }
+  if constexpr (k8) {
+    if (!a.many && threadIdx.x == 0) a.cuts[range] = cut;  // the last unit that it begins: no other is cut
   }
 }
 
@@ -912,49 +957,43 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
   __shared__ float o_s[kJoinWaves][D], stat_s[kJoinWaves][2];
   const int t = threadIdx.x, lane = t & (kWave - 1), k = lane % kLanes;
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
-  constexpr int kCost = kUnitCost<k8>;
-  const Stream s = stream_of<kCost>(a, kColumns);
   const int64_t u = blockIdx.x;
-  int64_t begin, unit, r_lo;
-  int32_t i, pieces;
-  Work w;
-  if constexpr (k8 && !kMany) {  // a workgroup per end of a range: the unit that it is the first to cut, if it does
-    const int64_t cut = (u + 1) * s.length;
-    if (cut >= s.total) return;
-    const int who = 63 - __builtin_clzll(__ballot(s.before <= cut));
-    begin = (int64_t)lane_value((uint64_t)s.before, who);
-    for (i = who * s.per;; ++i) {
-      if (i >= a.B) return;
-      w = work_at(a, s, i, kColumns);
-      const int64_t items = w.units(a) * (w.n + kCost);
-      if (cut < begin + items) break;
-      begin += items;
-    }
-    unit = (cut - begin) / (w.n + kCost);
-    begin += unit * (w.n + kCost) + kCost;
-    if (cut <= begin) return;
-    r_lo = begin / s.length;
-    if (r_lo != u) return;
-    pieces = (int32_t)((begin + w.n - 1) / s.length - r_lo) + 1;
+  int64_t r_lo, row0;
+  int32_t pieces, head, c0, columns;
+  if constexpr (k8) {
+    const Cut cut = a.cuts[u];
+    if (kMany && u >= a.cuts[gridDim.x].pieces) return;
+    if (cut.pieces <= 1) return;
+    r_lo = cut.first_range;
+    pieces = cut.pieces;
+    row0 = cut.row0;
+    head = cut.head;
+    c0 = cut.c0;
+    columns = (cut.k + 1) * a.G;
   } else {
+    const Stream s = stream_of<0>(a, kColumns);
     const int who = 63 - __builtin_clzll(__ballot(s.units_before <= u));
-    begin = (int64_t)lane_value((uint64_t)s.before, who);
-    unit = u - (int64_t)lane_value((uint64_t)s.units_before, who);
-    for (i = who * s.per;; ++i) {
+    int64_t begin = (int64_t)lane_value((uint64_t)s.before, who);
+    int64_t unit = u - (int64_t)lane_value((uint64_t)s.units_before, who);
+    int32_t i = who * s.per;
+    Work w;
+    for (;; ++i) {
       if (i >= a.B) return;
       w = work_at(a, s, i, kColumns);
       if (unit < w.units(a)) break;
       unit -= w.units(a);
-      begin += w.units(a) * (w.n + kCost);
+      begin += w.units(a) * w.n;
     }
-    begin += unit * (w.n + kCost) + kCost;
+    begin += unit * w.n;
     r_lo = begin / s.length;
     pieces = (int32_t)((begin + w.n - 1) / s.length - r_lo) + 1;
     if (pieces == 1) return;
+    const Request r = request_with(w, i);
+    row0 = r.row0;
+    head = (uint32_t)unit % (uint32_t)a.cache.n_heads;
+    c0 = (int32_t)((uint32_t)unit / (uint32_t)a.cache.n_heads) * kColumns;
+    columns = (r.k + 1) * a.G;
   }
-  const Request r = request_with(w, i);
-  const int32_t head = (uint32_t)unit % (uint32_t)a.cache.n_heads;
-  const int32_t c0 = (int32_t)((uint32_t)unit / (uint32_t)a.cache.n_heads) * kColumns, columns = (r.k + 1) * a.G;
   // the piece with the unit's first tile is its range's second, the others their ranges' first
   auto at = [&](int32_t piece) { return (2 * (r_lo + piece) + (piece == 0 ? 1 : 0)) * kColumns; };
   const int x_lo = blockIdx.y * (kMany ? 1 : kJoin), x_hi = x_lo + (kMany ? 1 : kJoin);
@@ -964,10 +1003,12 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
     // this wave's pieces: all of them, or every kJoinWaves-th 64
     float top = -__builtin_inff(), sum = 0.0f;
     f32x4 o = f32x4{0, 0, 0, 0};
-    for (int32_t p0 = kMany ? wave * kWave : 0; p0 < pieces; p0 += kMany ? kJoinWaves * kWave : kWave) {
+    const int32_t share = k8 && kMany ? (pieces + kJoinWaves - 1) / kJoinWaves : kWave;  // 8 bits: in equal parts
+    const int32_t p_end = k8 && kMany ? (wave * share + share < pieces ? wave * share + share : pieces) : pieces;
+    for (int32_t p0 = kMany ? wave * share : 0; p0 < p_end; p0 += kMany && !k8 ? kJoinWaves * kWave : kWave) {
       const int32_t p = p0 + lane;
       float m = -__builtin_inff(), l = 0.0f;
-      if (p < pieces) {
+      if (p < p_end) {
         m = a.stats[2 * (at(p) + x)];
         l = a.stats[2 * (at(p) + x) + 1];
       }
@@ -976,7 +1017,7 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
       top = next;
       sum = sum * fade + wave_sum(l * scale);
       o *= fade;
-      const int32_t n = pieces - p0 < kWave ? pieces - p0 : kWave;
+      const int32_t n = p_end - p0 < kWave ? p_end - p0 : kWave;
 #pragma unroll 4
       for (int32_t q = 0; q < n; q += kRows) {
         const int32_t mine = q + lane / kLanes;
@@ -1013,7 +1054,7 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
     if (lane >= kLanes) continue;
     o *= sum > 0.0f ? 1.0f / sum : 0.0f;
     const int32_t j = (uint32_t)c / (uint32_t)a.G, h = head * a.G + (c - j * a.G);
-    char* dst = a.out + ((r.row0 + j) * a.n_q + h) * (D * E::kBytes) + k * 4 * E::kBytes;
+    char* dst = a.out + ((row0 + j) * a.n_q + h) * (D * E::kBytes) + k * 4 * E::kBytes;
     if constexpr (E::kBytes == 2) {
       bf16x4 v;
       for (int e = 0; e < 4; ++e) v[e] = (__bf16)o[e];
