@@ -55,14 +55,15 @@ inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int
   if (pairs && (p.mode == kRanges || units_of(16) > kFewUnits)) p.qb = 2;
   p.tiles = rows * G / (16 * p.qb) + B;
   if (p.mode == kRanges) {
-    const int64_t units = units_of(16 * p.qb), groups = (units * tokens + kStreamWaves - 1) / kStreamWaves;
-    p.ranges = (int32_t)(groups < places() ? groups : places());
+    const int64_t units = units_of(16 * p.qb) / c->n_kv_heads, groups = (units * tokens + kStreamWaves - 1) / kStreamWaves;
+    const int64_t most = places() / c->n_kv_heads > 0 ? places() / c->n_kv_heads : 1;
+    p.ranges = (int32_t)(groups < most ? groups : most);
     p.pieces = (int32_t)((p.ranges + units - 1) / units) + 1;
-    const size_t n = (size_t)2 * p.ranges * 16 * p.qb;
+    const size_t n = (size_t)2 * p.ranges * c->n_kv_heads * 16 * p.qb;
     p.part_bytes = up256(n * c->head_dim * 4);
     p.stat_bytes = up256(n * 8);
     p.many = p.pieces > 16;
-    const size_t cuts = (p.many ? (size_t)p.tiles * c->n_kv_heads : (size_t)p.ranges) + 1;
+    const size_t cuts = (size_t)(p.many ? p.tiles : p.ranges) * c->n_kv_heads + 1;
     p.bytes = p.part_bytes + p.stat_bytes + up256(cuts * sizeof(Cut));
   }
   return p;
@@ -76,12 +77,12 @@ int launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
   } else if (p.mode == kUnits) {
     hipLaunchKernelGGL((attend_units<E, D, QB, kStreamWaves, true, true>), units, threads, 0, s, a);
   } else {
-    hipLaunchKernelGGL((attend_ranges<E, D, QB, true>), dim3((unsigned)a.ranges), threads, 0, s, a);
+    hipLaunchKernelGGL((attend_ranges<E, D, QB, true>), dim3((unsigned)(a.ranges * a.cache.n_heads)), threads, 0, s, a);
     if (a.ranges == 1) return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
     if (p.many)
       hipLaunchKernelGGL((join<E, D, QB, true, true>), dim3(units.x, 16 * QB), dim3(kJoinWaves * kWave), 0, s, a);
     else
-      hipLaunchKernelGGL((join<E, D, QB, false, true>), dim3((unsigned)a.ranges - 1, 16 * QB / kJoin), dim3(kJoinWaves * kWave), 0, s, a);
+      hipLaunchKernelGGL((join<E, D, QB, false, true>), dim3((unsigned)(a.ranges * a.cache.n_heads), 16 * QB / kJoin), dim3(kJoinWaves * kWave), 0, s, a);
   }
   return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
 }

@@ -48,7 +48,7 @@ struct AttendArgs {
   const uint8_t* value_scales;
   int32_t block_log2;
   bool many;           // cuts are told by unit
-  struct Cut* cuts;    // [ranges + 1], or [units + 1]; the last of them the number of units
+  struct Cut* cuts;    // [ranges][heads], or [units][heads] and one more with the number of units
 };
 // A unit that ranges cut, as its first range tells the join.
 struct Cut {
@@ -160,12 +160,15 @@ __device__ __forceinline__ Span span_of(int32_t len, int32_t pos_lo, int32_t pos
 }
 
 // The batch's work is the list of its units (tile of columns, head), request by request, each of its token tiles.
-// The list is cut into equal ranges, one per workgroup: lengths differ between requests, and few units leave
+// The list is cut into equal ranges, one per workgroup (8 bits: one per workgroup and head, so that the heads of a page, which lie next
+// to each other, are read at about one time: 64 requests of K in 0 .. 8 KKK us for 145): lengths differ between requests, and few units leave
 // places empty (one request of 8 heads on 4000 tokens: 17 us by ranges, 42 by units).
 struct Work {
   int32_t first, k, len;      // the request
   int32_t tiles, n;           // column tiles; token tiles of a unit (those of all its rows)
-  __device__ int64_t units(const AttendArgs& a) const { return (int64_t)tiles * a.cache.n_heads; }
+  // of the list: those of 8 bits are cut alike for every head
+  template <bool k8>
+  __device__ int64_t units(const AttendArgs& a) const { return k8 ? tiles : (int64_t)tiles * a.cache.n_heads; }
 };
 __device__ __forceinline__ Work work_of(const AttendArgs& a, int32_t i, int32_t columns) {
   Work w;
@@ -186,7 +189,13 @@ struct Stream {
   int64_t total, units;          // items, and units, of the batch
   int64_t length;                // of a range
 };
-template <int kCost>
+// A unit costs more than its tiles: its pages are found, its queries loaded and its waves joined.  For caches in 8 bits it
+// counts as that many tiles more, or a range of many short units would end long after the others (64 requests of 4096 visible
+// tokens and one that is empty: 190 us without, 148 with).
+template <bool k8>
+constexpr int kUnitCost = k8 ? 12 : 0;
+
+template <bool k8>
 __device__ __forceinline__ Stream stream_of(const AttendArgs& a, int32_t columns) {
   const int lane = threadIdx.x & (kWave - 1);
   Stream s;
@@ -198,8 +207,8 @@ __device__ __forceinline__ Stream stream_of(const AttendArgs& a, int32_t columns
     if (i >= a.B) break;
     const Work w = work_of(a, i, columns);
     if (k == 0) s.own = w;
-    items += (uint64_t)(w.units(a) * (w.n + kCost));
-    units += (uint64_t)w.units(a);
+    items += (uint64_t)(w.units<k8>(a) * (w.n + kUnitCost<k8>));
+    units += (uint64_t)w.units<k8>(a);
   }
   const uint64_t inc = wave_inclusive_scan(items);
   s.before = (int64_t)(inc - items);
@@ -873,26 +882,22 @@ __global__ __launch_bounds__(kWaves* kWave, (kMinWaves<E, D, QB>)) void attend_u
 
 // A workgroup per range of the batch's work.
 constexpr int kStreamWaves = 4;
-//
-// A unit costs more than its tiles: its pages are found, its queries loaded and its waves joined.  For caches in 8 bits it
-// counts as that many tiles more, or a range of many short units would end long after the others (64 requests of 4096 visible
-// tokens and one that is empty: 190 us without, KKK with).
-template <bool k8>
-constexpr int kUnitCost = k8 ? 12 : 0;
 template <class E, int D, int QB, bool k8>
 __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void attend_ranges(AttendArgs a) {
   constexpr int kColumns = 16 * QB, kCost = kUnitCost<k8>;
   __shared__ Scratch<E, D, QB, kStreamWaves, k8> sh;
-  const Stream s = stream_of<kCost>(a, kColumns);
-  const int64_t range = unit_of_block(blockIdx.x, gridDim.x);
+  const Stream s = stream_of<k8>(a, kColumns);
+  const int64_t block = unit_of_block(blockIdx.x, gridDim.x);
+  const int64_t range = k8 ? (uint32_t)block / (uint32_t)a.cache.n_heads : block;
+  const int32_t own_head = k8 ? (int32_t)(block - range * a.cache.n_heads) : 0;
   const int64_t end = (range + 1) * s.length < s.total ? (range + 1) * s.length : s.total;
   int64_t p = range * s.length;
   Cut cut = {};
   if constexpr (k8) {
     // requests that do not lie in their order can have more units than there is room for
-    const int64_t room = a.tiles * a.cache.n_heads;
-    if (a.many && range == 0 && threadIdx.x == 0) a.cuts[room].pieces = (int32_t)(s.units < room ? s.units : room);
-    if (p >= end && !a.many && threadIdx.x == 0) a.cuts[range] = cut;
+    if (a.many && block == 0 && threadIdx.x == 0)
+      a.cuts[a.tiles * a.cache.n_heads].pieces = (int32_t)(s.units < a.tiles ? s.units : a.tiles);
+    if (p >= end && !a.many && threadIdx.x == 0) a.cuts[block] = cut;
   }
   if (p >= end) return;
   // the request of p, then on from one to the next
@@ -903,10 +908,10 @@ __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void at
   while (p < end && i < a.B) {
     const Work w = work_at(a, s, i, kColumns);
     const int32_t span = w.n + kCost;
-    const int64_t items = w.units(a) * span;
+    const int64_t items = w.units<k8>(a) * span;
     if (p >= base + items) {
       base += items;
-      if constexpr (k8) units += w.units(a);
+      if constexpr (k8) units += w.units<k8>(a);
       ++i;
       continue;
     }
@@ -921,7 +926,8 @@ __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void at
     }
     TileOf at;
     at.r = request_with(w, i);
-    at.c0 = (int32_t)(unit / (uint32_t)a.cache.n_heads) * kColumns;
+    const int32_t head = k8 ? own_head : (int32_t)(unit % (uint32_t)a.cache.n_heads);
+    at.c0 = (int32_t)(k8 ? unit : unit / (uint32_t)a.cache.n_heads) * kColumns;
     const bool first = q_lo == 0, whole = first && q_hi == w.n;
     if constexpr (k8) {
       if (first) {
@@ -930,18 +936,17 @@ __global__ __launch_bounds__(kStreamWaves* kWave, (kMinWaves<E, D, QB>)) void at
         cut.first_range = (int32_t)range;
         cut.row0 = w.first + i;
         cut.k = w.k;
-        cut.head = (int32_t)(unit % (uint32_t)a.cache.n_heads);
+        cut.head = head;
         cut.c0 = at.c0;
-        if (a.many && threadIdx.x == 0 && units + unit < a.tiles * a.cache.n_heads) a.cuts[units + unit] = cut;
+        if (a.many && threadIdx.x == 0 && units + unit < a.tiles) a.cuts[(units + unit) * a.cache.n_heads + head] = cut;
       }
     }
-    attend_unit<E, D, QB, kStreamWaves, true, k8>(a, sh, at, w.len, (int32_t)(unit % (uint32_t)a.cache.n_heads), true,
-                                              q_lo, q_hi,
-                                              whole ? -1 : 2 * range + (first ? 1 : 0));
+    attend_unit<E, D, QB, kStreamWaves, true, k8>(a, sh, at, w.len, head, true, q_lo, q_hi,
+                                                  whole ? -1 : 2 * block + (first ? 1 : 0));
     __syncthreads();
   }
   if constexpr (k8) {
-    if (!a.many && threadIdx.x == 0) a.cuts[range] = cut;  // the last unit that it begins: no other is cut
+    if (!a.many && threadIdx.x == 0) a.cuts[block] = cut;  // the last unit that it begins: no other is cut
   }
 }
 
@@ -962,7 +967,7 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
   int32_t pieces, head, c0, columns;
   if constexpr (k8) {
     const Cut cut = a.cuts[u];
-    if (kMany && u >= a.cuts[gridDim.x].pieces) return;
+    if (kMany && u >= (int64_t)a.cuts[gridDim.x].pieces * a.cache.n_heads) return;
     if (cut.pieces <= 1) return;
     r_lo = cut.first_range;
     pieces = cut.pieces;
@@ -971,7 +976,7 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
     c0 = cut.c0;
     columns = (cut.k + 1) * a.G;
   } else {
-    const Stream s = stream_of<0>(a, kColumns);
+    const Stream s = stream_of<false>(a, kColumns);
     const int who = 63 - __builtin_clzll(__ballot(s.units_before <= u));
     int64_t begin = (int64_t)lane_value((uint64_t)s.before, who);
     int64_t unit = u - (int64_t)lane_value((uint64_t)s.units_before, who);
@@ -980,9 +985,9 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
     for (;; ++i) {
       if (i >= a.B) return;
       w = work_at(a, s, i, kColumns);
-      if (unit < w.units(a)) break;
-      unit -= w.units(a);
-      begin += w.units(a) * w.n;
+      if (unit < w.units<false>(a)) break;
+      unit -= w.units<false>(a);
+      begin += w.units<false>(a) * w.n;
     }
     begin += unit * w.n;
     r_lo = begin / s.length;
@@ -995,7 +1000,10 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void join(AttendArgs a) {
     columns = (r.k + 1) * a.G;
   }
   // the piece with the unit's first tile is its range's second, the others their ranges' first
-  auto at = [&](int32_t piece) { return (2 * (r_lo + piece) + (piece == 0 ? 1 : 0)) * kColumns; };
+  auto at = [&](int32_t piece) {
+    const int64_t range = k8 ? (r_lo + piece) * a.cache.n_heads + head : r_lo + piece;
+    return (2 * range + (piece == 0 ? 1 : 0)) * kColumns;
+  };
   const int x_lo = blockIdx.y * (kMany ? 1 : kJoin), x_hi = x_lo + (kMany ? 1 : kJoin);
   for (int x = x_lo + (kMany ? 0 : wave); x < x_hi; x += kMany ? 1 : kJoinWaves) {
     const int32_t c = c0 + x;
