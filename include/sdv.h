@@ -635,8 +635,8 @@ typedef struct sdv_cache8 {
  *   a block that holds cached tokens (slots below L_i) keeps its scale if that is larger; if it is smaller, it takes 2^e
  *   and the cached tokens' codes are brought to it, rounded to the nearest (ties to even) where they become subnormal.
  * A value's code is the e4m3 number nearest to value * 2^-e (ties to even; the largest beyond 448, which takes a value beyond
- * 448 * 2^119), of a rotated key to the binary32 result of the rotation; NaN where the value is not finite.  Rotated queries
- * are rounded to the rows' type.  Codes of a block behind its rows are left as they were, under the block's scale.
+ * 448 * 2^119), of a rotated key to its rotation in binary64; NaN where the value, or one that it turns with, is not
+ * finite.  Queries are those of sdv_kv_append.  Codes of a block behind its rows are left as they were, under the block's scale.
  */
 int sdv_kv_append8(const sdv_cache8* cache, int32_t B, int64_t n_draft_rows, const int32_t* ragged_offsets,
                    const int32_t* parents, const void* keys, int64_t key_stride, const void* values,

@@ -41,11 +41,13 @@ __device__ __forceinline__ void load8(const char* src, float (&f)[8]) {
   }
 }
 
-// Values 8 at .. 8 at + 7 of a head, rotated: c and s are the position's cosines and sines.
+// Values 8 at .. 8 at + 7 of a head, rotated: c and s are the position's cosines and sines.  o: half of |a| + |b| of a value's pair.
 template <class E, bool kInterleaved>
 __device__ __forceinline__ void load_rotated(const char* head, int at, int rotary, const float* c, const float* s,
-                                             float (&f)[8]) {
+                                             float (&f)[8], float (&o)[8]) {
   load8<E>(head + at * 8 * E::kBytes, f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = 0.0f;
   if (at * 8 >= rotary) return;
   if constexpr (kInterleaved) {
 #pragma unroll
@@ -53,40 +55,70 @@ __device__ __forceinline__ void load_rotated(const char* head, int at, int rotar
       const float cs = c[at * 4 + e / 2], sn = s[at * 4 + e / 2], a = f[e], b = f[e + 1];
       f[e] = a * cs - b * sn;
       f[e + 1] = b * cs + a * sn;
+      o[e] = o[e + 1] = 0.5f * fabsf(a) + 0.5f * fabsf(b);
     }
   } else {
     const int half = rotary / 16;  // in pieces of 8
     const bool first = at < half;
-    float o[8];
     load8<E>(head + (first ? at + half : at - half) * 8 * E::kBytes, o);
     const int f0 = (first ? at : at - half) * 8;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float cs = c[f0 + e], sn = s[f0 + e];
-      f[e] = first ? f[e] * cs - o[e] * sn : f[e] * cs + o[e] * sn;
+      const float cs = c[f0 + e], sn = s[f0 + e], a = f[e];
+      f[e] = first ? a * cs - o[e] * sn : a * cs + o[e] * sn;
+      o[e] = 0.5f * fabsf(a) + 0.5f * fabsf(o[e]);
     }
   }
 }
 
-// The code of x: the number nearest to it, at most 448; NaN of what is not finite.
-__device__ __forceinline__ float within(float x) {
-  const float top = __builtin_copysignf(448.0f, x);
-  return fabsf(x) > 448.0f ? (x - x == 0.0f ? top : __builtin_nanf("")) : x;
+// Codes of two values, at most 448, in the lower half.
+__device__ __forceinline__ uint32_t codes_of(float x, float y) {
+  return __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_fmed3f(x, -448.0f, 448.0f), __builtin_amdgcn_fmed3f(y, -448.0f, 448.0f),
+                                         0, false) & 0xffffu;
 }
-__device__ __forceinline__ uint2 codes_of(const float (&f)[8], float by) {
-  uint2 v;
-  uint32_t w = __builtin_amdgcn_cvt_pk_fp8_f32(within(f[0] * by), within(f[1] * by), 0, false);
-  v.x = __builtin_amdgcn_cvt_pk_fp8_f32(within(f[2] * by), within(f[3] * by), w, true);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(within(f[4] * by), within(f[5] * by), 0, false);
-  v.y = __builtin_amdgcn_cvt_pk_fp8_f32(within(f[6] * by), within(f[7] * by), w, true);
-  return v;
+__device__ __forceinline__ uint2 codes_of(const float (&f)[8]) {
+  return make_uint2(codes_of(f[0], f[1]) | codes_of(f[2], f[3]) << 16, codes_of(f[4], f[5]) | codes_of(f[6], f[7]) << 16);
 }
 
-// The largest finite magnitude of 8 values, as bits of binary32.
+// Cosine and sine of an angle in turns, at most half a turn either way, to 2^-50: the series around the next quarter.  (The library's
+// take the registers of four waves.)
+__device__ __forceinline__ void cos_sin(double turns, double& c, double& s) {
+  const double quarter = rint(4.0 * turns), y = (turns - 0.25 * quarter) * 6.283185307179586, z = y * y;  // |y| <= pi / 4
+  double a = 1.0 / 6402373705728000.0, b = 1.0 / 121645100408832000.0;  // 1 / 18!, 1 / 19!
+  constexpr double kCos[] = {1.0 / 20922789888000.0, 1.0 / 87178291200.0, 1.0 / 479001600.0, 1.0 / 3628800.0,
+                             1.0 / 40320.0,          1.0 / 720.0,         1.0 / 24.0,        0.5,
+                             1.0};
+  constexpr double kSin[] = {1.0 / 355687428096000.0, 1.0 / 1307674368000.0, 1.0 / 6227020800.0, 1.0 / 39916800.0,
+                             1.0 / 362880.0,          1.0 / 5040.0,          1.0 / 120.0,        1.0 / 6.0,
+                             1.0};
+#pragma unroll
+  for (int k = 0; k < 9; ++k) {
+    a = kCos[k] - z * a;
+    b = kSin[k] - z * b;
+  }
+  b *= y;
+  const int q = (int)quarter & 3;
+  const double u = q & 1 ? b : a, v = q & 1 ? a : b;
+  c = q == 1 || q == 2 ? -u : u;
+  s = q >= 2 ? -v : v;
+}
+
+// The code of a value in binary64, at most 448.
+__device__ __forceinline__ uint32_t code_of(double x) {
+  // cut to binary32 with the lost bits in the last one: the next rounding sees on which side it lies
+  float f = __double2float_rz(x);
+  if ((double)f != x) f = __uint_as_float(__float_as_uint(f) | 1);
+  return __builtin_amdgcn_cvt_pk_fp8_f32(__builtin_amdgcn_fmed3f(f, -448.0f, 448.0f), 0.0f, 0, false) & 255u;
+}
+
+// The largest finite magnitude of 8 values, as bits of binary32; odd where one is not finite.
 template <class E>
-__device__ __forceinline__ uint32_t top_bits(const char* src) {
+__device__ __forceinline__ uint32_t top_bits(const char* src, bool& odd) {
   uint32_t top = 0;
-  auto take = [&](uint32_t bits) { top = bits < 0x7f800000u && bits > top ? bits : top; };
+  auto take = [&](uint32_t bits) {
+    top = bits < 0x7f800000u && bits > top ? bits : top;
+    odd |= bits >= 0x7f800000u;
+  };
   const u32x4 x = *reinterpret_cast<const u32x4*>(src);
   if constexpr (E::kBytes == 2) {
 #pragma unroll
@@ -123,7 +155,7 @@ constexpr int kTurns = 16;  // tokens whose angles are held at once
 
 // A workgroup takes some of the keys' and values' heads of a block of tokens (a wave each), or one row's queries.
 template <class E, bool kInterleaved>
-__global__ __launch_bounds__(kThreads) void append8(Append8Args a) {
+__global__ __launch_bounds__(kThreads, 8) void append8(Append8Args a) {
   __shared__ float cos_s[kTurns][128], sin_s[kTurns][128];
   __shared__ int32_t parent_s[kWave], depth_s[kMaxNodes + 1];
   const int t = threadIdx.x, lane = t & (kWave - 1);
@@ -167,15 +199,17 @@ __global__ __launch_bounds__(kThreads) void append8(Append8Args a) {
   }
   if (a.parents && !tree_depths(a.parents, r, parent_s, depth_s)) return;
 
+  // the angle of row j's pair f in turns, reduced in binary64: far positions keep their phase
+  auto turns_of = [&](int64_t j, int f) {
+    const double angle =
+        (double)(len + (a.parents ? (int64_t)depth_s[j] : j)) * (double)a.inv_freq[f] * 0.15915494309189535;
+    return angle - rint(angle);
+  };
   // cosines and sines of `n` tokens from row j on
   auto turn = [&](int64_t j, int n) {
     for (int x = t; x < n * half; x += kThreads) {
-      const int token = x / half, f = x - token * half;
-      const int64_t depth = a.parents ? depth_s[j + token] : j + token;
-      // the angle in turns, reduced in binary64: far positions keep their phase
-      const double turns = (double)(len + depth) * (double)a.inv_freq[f] * 0.15915494309189535;
-      const float p = (float)(turns - rint(turns));
-      sincospif(2.0f * p, &sin_s[token][f], &cos_s[token][f]);
+      const int token = (uint32_t)x / (uint32_t)half, f = x - token * half;
+      sincospif(2.0f * (float)turns_of(j + token, f), &sin_s[token][f], &cos_s[token][f]);
     }
     __syncthreads();
   };
@@ -185,9 +219,9 @@ __global__ __launch_bounds__(kThreads) void append8(Append8Args a) {
     const int64_t row = r.row0 + j0;
     for (int x = t; x < a.n_q * pieces; x += kThreads) {
       const int h = x / pieces, at = x - h * pieces;
-      float f[8];
+      float f[8], o[8];
       load_rotated<E, kInterleaved>(a.queries + (row * a.query_stride + (int64_t)h * a.D) * E::kBytes, at, a.rotary, cos_s[0],
-                                    sin_s[0], f);
+                                    sin_s[0], f, o);
       char* const dst = a.queries_out + ((row * a.n_q + h) * a.D + at * 8) * E::kBytes;
       u32x4 v, w;
       if constexpr (E::kBytes == 2) {
@@ -222,12 +256,14 @@ __global__ __launch_bounds__(kThreads) void append8(Append8Args a) {
   char* const line = (is_key ? cache.keys : cache.values) + cache.row(page, works ? head : 0, slot0) * a.D;
   uint8_t* const scale = (is_key ? a.view.key_scales : a.view.value_scales) + a.view.scale_at(page, works ? head : 0, slot0);
   int32_t byte = 0;
+  bool odd = false;
   if (works) {
     uint32_t top = 0;
     for (int x = token; x < n_rows; x += per) {
-      const uint32_t v = top_bits<E>(src + x * stride + at * 8 * E::kBytes);
+      const uint32_t v = top_bits<E>(src + x * stride + at * 8 * E::kBytes, odd);
       top = v > top ? v : top;
     }
+    odd = __any(odd);
     byte = least_byte(wave_max_bits(top), is_key ? kKeyLimit : kValueLimit);
     const int64_t first = slot0 >> a.view.block_log2 << a.view.block_log2;
     if (first < len) {  // (then slot0 is len)
@@ -255,13 +291,52 @@ __global__ __launch_bounds__(kThreads) void append8(Append8Args a) {
     if (turns) turn(j0 + x0, n);
     if (works) {
       for (int x = token; x < n; x += per) {
-        float f[8];
+        float f[8], o[8];
         const char* const from = src + (x0 + x) * stride;
-        if (is_key)
-          load_rotated<E, kInterleaved>(from, at, a.rotary, cos_s[x], sin_s[x], f);
-        else
+        uint2 codes, differ = make_uint2(0, 0);
+        if (is_key && half > 0) {
+          load_rotated<E, kInterleaved>(from, at, a.rotary, cos_s[x], sin_s[x], f, o);
+          // Off by less than 2^-21 (|a| + |b|): 2^-23.4 for the rounded angle, 2^-23 for its cosine and sine, and two roundings.
+          // What lies so near to a border between two codes that binary32 does not tell its side (about one value in 15 000)
+          // goes on in binary64.
+          const float slack = 0x1.2p-20f * by;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            f[e] = fmaf(f[e], by, -o[e] * slack);
+            o[e] = fmaf(o[e], 2.0f * slack, f[e]);
+          }
+          codes = codes_of(f);
+          differ = codes_of(o);
+          differ.x ^= codes.x;
+          differ.y ^= codes.y;
+        } else {
           load8<E>(from + at * 8 * E::kBytes, f);
-        *reinterpret_cast<uint2*>(line + (x0 + x) * a.D + at * 8) = codes_of(f, by);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= by;
+          codes = codes_of(f);
+        }
+        if (odd) differ = make_uint2(~0u, ~0u);
+        if (__builtin_expect((differ.x | differ.y) != 0, 0)) {
+          uint64_t word = codes.x | (uint64_t)codes.y << 32, again = differ.x | (uint64_t)differ.y << 32;
+          while (again) {
+            const int e = (__ffsll((unsigned long long)again) - 1) / 8, i = at * 8 + e;
+            again &= ~((uint64_t)255 << (8 * e));
+            const float p = E::at(from, i);
+            float q = 0.0f;
+            double v = p;
+            if (is_key && i < a.rotary) {
+              const bool one = kInterleaved ? i % 2 == 0 : i < half;
+              q = E::at(from, kInterleaved ? i ^ 1 : (one ? i + half : i - half));
+              double c, s;
+              cos_sin(turns_of(j0 + x0 + x, kInterleaved ? i / 2 : (one ? i : i - half)), c, s);
+              v = one ? p * c - q * s : p * c + q * s;
+            }
+            const uint64_t code = p - p == 0.0f && q - q == 0.0f ? code_of(v * (double)by) : 0x7fu;
+            word = (word & ~((uint64_t)255 << (8 * e))) | code << (8 * e);
+          }
+          codes = make_uint2((uint32_t)word, (uint32_t)(word >> 32));
+        }
+        *reinterpret_cast<uint2*>(line + (x0 + x) * a.D + at * 8) = codes;
       }
     }
     if (turns) __syncthreads();

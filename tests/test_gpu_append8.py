@@ -1,8 +1,9 @@
 """Appending to the paged cache in 8 bits, on the GPU against the oracle.
 
-Scales come from the rows as given and codes of values from exact products, so both are the oracle's.  A rotated key is off by
-2^-20 (|a| + |b|) before it becomes a code (the bound of test_gpu_kv_cache's tolerances), and a code by half a step: 2^-4 of the
-binade's lower end, 2^-10 below 2^-6.  Queries: that rotation, and one rounding to their type (bf16 2^-8, binary32 2^-24).
+Scales come from the rows as given, and a code is that of the value in binary64: the kernel goes on in binary64 where binary32 does
+not tell on which side of a border it lies (its angles are off by 2^-53 of a position, 1e-9 at the farthest here, so that no value of a
+test lies within its error of a border but by a chance of 1e-3 in all), so both are the oracle's.  Queries: off by 2^-20 (|a| + |b|)
+(the bound of test_gpu_kv_cache), and one rounding to their type (bf16 2^-8, binary32 2^-24).
 """
 import numpy as np
 import pytest
@@ -29,18 +30,7 @@ def compare(b, caches, q_out, rotary, interleaved):
     gk, gv, gks, gvs = (host(t) for t in caches)
     assert np.array_equal(gks, rks) and np.array_equal(gvs, rvs)
     assert same(gv, rv)
-    finite = np.isfinite(exact)
-    if rotary == 0:
-        assert same(gk, rk)
-    else:
-        assert same(gk[~finite], rk[~finite])
-        scale = np.repeat(oracle.scales(rks), b.block, -1)[..., None]
-        pair = 2 * max(float(b.k[torch.isfinite(b.k)].abs().max()), 1e-38)
-        err = (2.0 ** -20 * pair / scale + np.zeros_like(exact))[finite]
-        x = np.clip(exact[finite], -448, 448)
-        half = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x) + err, 2.0 ** -6))) - 4)
-        bad = ~(np.abs(oracle.DECODED[gk[finite]] - x) <= half + err)
-        assert not bad.any(), (bad.sum(), x[bad][:4], oracle.DECODED[gk[finite]][bad][:4])
+    assert same(gk, rk), (np.argwhere(gk != rk)[:4], gk[gk != rk][:4], rk[gk != rk][:4], exact[gk != rk][:4])
     if q_out is not None:
         seen = np.isfinite(rq)
         big = 2 * max(float(b.q[torch.isfinite(b.q)].abs().max()), 1.0)
