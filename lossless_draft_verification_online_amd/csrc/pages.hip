@@ -68,6 +68,131 @@ __device__ __forceinline__ void ask(const PagesArgs& a, const Keeps& k, int32_t 
   want = in && !have && at >= k.rows && at < k.hi;
 }
 
+// Entries of [lo, hi) of a request's row of the table that go back, and that its rows need.  kAhead loads at once.
+constexpr int kAhead = 4;
+__device__ __forceinline__ void count_part(const PagesArgs& a, const Keeps& k, const int32_t* row, int32_t lo, int32_t hi,
+                                           int32_t& frees, int32_t& wants) {
+  const int lane = threadIdx.x & (kWave - 1);
+  for (int32_t x0 = lo; x0 < hi; x0 += kAhead * kWave) {
+    int32_t entry[kAhead];
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const int32_t at = x0 + y * kWave + lane;
+      entry[y] = at < hi ? row[at] : -1;
+    }
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const int32_t at = x0 + y * kWave + lane;
+      bool free, want;
+      ask(a, k, at, entry[y], free, want);
+      frees += __popcll(__ballot(free && at < hi));
+      wants += __popcll(__ballot(want && at < hi));
+    }
+  }
+}
+
+// Returns and takes them: `returned` and `taken` pages went before, in the ring as it was.
+__device__ __forceinline__ void place_part(const PagesArgs& a, const Keeps& k, int32_t* row, int32_t lo, int32_t hi,
+                                           int32_t first, int32_t held, uint64_t returned, uint64_t taken, bool is_placed) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const uint64_t below = ((uint64_t)1 << lane) - 1;
+  // a place of the ring, whose sum with `first` is below 2^33
+  auto place_of = [&](uint64_t x) { return x < (uint64_t)a.n_pages ? x : x - (uint64_t)a.n_pages; };
+  for (int32_t x0 = lo; x0 < hi; x0 += kAhead * kWave) {
+    int32_t entry[kAhead];
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const int32_t at = x0 + y * kWave + lane;
+      entry[y] = at < hi ? row[at] : -1;
+    }
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      const int32_t at = x0 + y * kWave + lane;
+      bool free, want;
+      ask(a, k, at, entry[y], free, want);
+      free = free && at < hi;
+      want = want && at < hi && is_placed;
+      const uint64_t frees = __ballot(free), wants = __ballot(want);
+      if (free) {
+        const uint64_t to = (uint64_t)held + returned + __popcll(frees & below);
+        if (to < (uint64_t)a.n_pages) a.ring[place_of(first + to)] = entry[y];
+        row[at] = -1;
+      }
+      if (want) row[at] = a.ring[place_of(first + taken + __popcll(wants & below))];
+      returned += __popcll(frees);
+      taken += __popcll(wants);
+    }
+  }
+}
+
+// The slots of a placed request's rows, by `threads` threads.
+__device__ __forceinline__ void write_slots(const PagesArgs& a, const Request& r, const int32_t* row, int32_t len, int t,
+                                            int threads) {
+  for (int32_t j = t; j <= r.k; j += threads) {
+    const int32_t s = len + j, page = row[s >> a.page_log2];
+    a.slots[r.row0 + j] = page >= 0 && page < a.n_pages
+                              ? ((int64_t)page << a.page_log2) + (s & ((1 << a.page_log2) - 1))
+                              : -1;
+  }
+}
+
+// The ring behind a call that returns `all` pages and takes `most`; what a full ring has no room for is dropped.
+__device__ __forceinline__ void write_state(const PagesArgs& a, int32_t first, int32_t held, uint64_t all, uint64_t most) {
+  const uint64_t room = (uint64_t)a.n_pages - held, back = all < room ? all : room, to = first + most;
+  a.state[0] = (int32_t)(to < (uint64_t)a.n_pages ? to : to - (uint64_t)a.n_pages);
+  a.state[1] = (int32_t)((uint64_t)held + back - most);
+}
+
+// Few requests with short rows of the table: one workgroup, a wave per request.  Two calls after one another, by this and by the two
+// launches: one request of 66 entries 7.4 us and 12.6, 4 of 515 10.1 and 14.0, 16 of 260 10.7 and 14.2, but 16 of 1028 20.7 and
+// 14.8, one of 4100 26.8 and 17.6, and 64 of 67 (four to a wave) 29 and 14.2.
+constexpr int kFewWaves = 16, kFewPages = 640;
+__global__ __launch_bounds__(kFewWaves* kWave) void place_few(PagesArgs a) {
+  __shared__ int32_t freed_s[kWave], wanted_s[kWave];
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int32_t first = a.state[0], held = a.state[1];
+  const bool ring = ring_fits(a, first, held);
+  if (t < kWave) freed_s[t] = wanted_s[t] = 0;
+  if (a.slots)
+    for (int64_t x = t; x < a.n_d + a.B; x += kFewWaves * kWave) a.slots[x] = -1;
+  __syncthreads();
+  for (int32_t i = wave; i < a.B; i += kFewWaves) {
+    const Keeps k = keeps_of(a, request_at(a.cu, i, a.n_d), a.len[i]);
+    int32_t frees = 0, wants = 0;
+    if (k.known && ring) count_part(a, k, a.table + (int64_t)i * a.max_pages, 0, a.max_pages, frees, wants);
+    if (lane == 0) {
+      freed_s[i] = frees;
+      wanted_s[i] = k.fits(a) ? wants : 0;
+    }
+  }
+  __syncthreads();
+  const uint64_t frees = freed_s[lane], wants = wanted_s[lane];
+  const uint64_t returned = wave_inclusive_scan(frees), taken = wave_inclusive_scan(wants);
+  const bool has_room = taken <= (uint64_t)held;
+  if (wave == 0 && ring) {
+    const uint64_t served = __ballot(has_room);  // the sums ascend: a run of leading lanes
+    const uint64_t most = served ? lane_value(taken, 63 - __builtin_clzll(served)) : 0;
+    const uint64_t all = lane_value(returned, kWave - 1);
+    if (lane == 0) write_state(a, first, held, all, most);
+  }
+  for (int32_t i = wave; i < a.B; i += kFewWaves) {
+    const Request r = request_at(a.cu, i, a.n_d);
+    const int32_t len = a.len[i];
+    const Keeps k = keeps_of(a, r, len);
+    const uint64_t mine = lane_value(wants, i);
+    const bool is_placed = ring && k.fits(a) && (mine == 0 || lane_value(taken, i) <= (uint64_t)held);
+    if (lane == 0) a.placed[i] = !ring || !k.known ? -1 : (is_placed ? 1 : 0);
+    if (!ring || !k.known) continue;
+    int32_t* const row = a.table + (int64_t)i * a.max_pages;
+    place_part(a, k, row, 0, a.max_pages, first, held, lane_value(returned, i) - lane_value(frees, i),
+               lane_value(taken, i) - mine, is_placed);
+    if (!is_placed || !a.slots) continue;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the wave's entries
+    write_slots(a, r, row, len, lane, kWave);
+  }
+}
+
 // What each request returns and takes; slots are -1 until they are known.
 __global__ __launch_bounds__(kThreads) void count(PagesArgs a) {
   __shared__ int32_t wanted_s[kWaves];
@@ -85,17 +210,7 @@ __global__ __launch_bounds__(kThreads) void count(PagesArgs a) {
   const bool works = k.known && ring_fits(a, first, held);
   int32_t frees = 0, wants = 0, lo, hi;
   part_of(a.max_pages, wave, lo, hi);
-  const int32_t* const row = a.table + (int64_t)i * a.max_pages;
-  if (works) {
-#pragma unroll 4
-    for (int32_t x = lo; x < hi; x += kWave) {
-      const int32_t at = x + lane;
-      bool free, want;
-      ask(a, k, at, at < a.max_pages ? row[at] : -1, free, want);
-      frees += __popcll(__ballot(free));
-      wants += __popcll(__ballot(want));
-    }
-  }
+  if (works) count_part(a, k, a.table + (int64_t)i * a.max_pages, lo, hi, frees, wants);
   if (lane == 0) {
     a.freed[(int64_t)i * kWaves + wave] = frees;
     wanted_s[wave] = wants;
@@ -108,20 +223,27 @@ __global__ __launch_bounds__(kThreads) void count(PagesArgs a) {
   }
 }
 
-template <class T>
-__device__ __forceinline__ T group_sum(T v, T* of_wave) {
-  v = lane_value(wave_inclusive_scan((uint64_t)v), kWave - 1);
+// The workgroup's sums of two values, in every thread.
+__device__ __forceinline__ void group_sums(uint64_t& x, uint64_t& y, uint64_t (*of_wave)[2]) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  x = wave_inclusive_scan(x);
+  y = wave_inclusive_scan(y);
   __syncthreads();
-  if ((threadIdx.x & (kWave - 1)) == 0) of_wave[threadIdx.x / kWave] = v;
+  if (lane == kWave - 1) {
+    of_wave[wave][0] = x;
+    of_wave[wave][1] = y;
+  }
   __syncthreads();
-  T sum = 0;
-  for (int w = 0; w < kWaves; ++w) sum += of_wave[w];
-  return sum;
+  x = y = 0;
+  for (int w = 0; w < kWaves; ++w) {
+    x += of_wave[w][0];
+    y += of_wave[w][1];
+  }
 }
 
 // A workgroup per request returns its pages and takes those that it has a right to.
 __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
-  __shared__ uint64_t sum_s[kWaves];
+  __shared__ uint64_t sum_s[kWaves][2];
   const int t = threadIdx.x, lane = t & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int32_t i = blockIdx.x;
@@ -130,14 +252,17 @@ __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
   const int32_t len = a.len[i];
   const Keeps k = keeps_of(a, r, len);
   const bool ring = ring_fits(a, first, held);
+  auto freed_of = [&](int32_t x) {
+    const int4 n = reinterpret_cast<const int4*>(a.freed)[x];
+    return (uint64_t)(uint32_t)n.x + (uint32_t)n.y + (uint32_t)n.z + (uint32_t)n.w;
+  };
   // pages returned and taken before this request
   uint64_t returned = 0, taken = 0;
   for (int32_t x = t; x < i; x += kThreads) {
-    for (int w = 0; w < kWaves; ++w) returned += (uint32_t)a.freed[(int64_t)x * kWaves + w];
+    returned += freed_of(x);
     taken += (uint32_t)a.wanted[x];
   }
-  returned = group_sum(returned, sum_s);
-  taken = group_sum(taken, sum_s);
+  group_sums(returned, taken, sum_s);
   const int32_t wants = a.wanted[i];
   const bool is_placed = ring && k.fits(a) && (wants == 0 || taken + wants <= (uint64_t)held);
   if (t == 0) a.placed[i] = !ring || !k.known ? -1 : (is_placed ? 1 : 0);
@@ -146,39 +271,29 @@ __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
     uint64_t all = 0, sum = 0, most = 0;
     for (int32_t x0 = 0; x0 < a.B; x0 += kThreads) {
       const int32_t x = x0 + t;
-      uint64_t mine = 0, back = 0;
-      if (x < a.B) {
-        mine = (uint32_t)a.wanted[x];
-        for (int w = 0; w < kWaves; ++w) back += (uint32_t)a.freed[(int64_t)x * kWaves + w];
-      }
-      all += group_sum(back, sum_s);
+      const uint64_t mine = x < a.B ? (uint32_t)a.wanted[x] : 0;
+      uint64_t back = x < a.B ? freed_of(x) : 0;
       const uint64_t inc = wave_inclusive_scan(mine);
-      __syncthreads();
-      if (lane == kWave - 1) sum_s[wave] = inc;
-      __syncthreads();
+      uint64_t whole = mine;
+      group_sums(back, whole, sum_s);
+      all += back;
       uint64_t here = sum + inc;
-      for (int w = 0; w < wave; ++w) here += sum_s[w];
-      for (int w = 0; w < kWaves; ++w) sum += sum_s[w];
+      for (int w = 0; w < wave; ++w) here += sum_s[w][1];
+      sum += whole;
       // the largest sum that the ring held
-      const uint64_t fits = here <= (uint64_t)held ? here : 0;
-      uint64_t top = fits;
+      uint64_t top = here <= (uint64_t)held ? here : 0;
 #pragma unroll
       for (int step = 1; step < kWave; step *= 2) {
         const uint64_t o = __shfl_xor((unsigned long long)top, step);
         top = o > top ? o : top;
       }
       __syncthreads();
-      if (lane == 0) sum_s[wave] = top;
+      if (lane == 0) sum_s[wave][0] = top;
       __syncthreads();
-      for (int w = 0; w < kWaves; ++w) most = sum_s[w] > most ? sum_s[w] : most;
+      for (int w = 0; w < kWaves; ++w) most = sum_s[w][0] > most ? sum_s[w][0] : most;
       __syncthreads();
     }
-    if (t == 0) {
-      // what a full ring has no room for is dropped
-      const uint64_t room = (uint64_t)a.n_pages - held, back = all < room ? all : room;
-      a.state[0] = (int32_t)((first + most) % (uint64_t)a.n_pages);
-      a.state[1] = (int32_t)((uint64_t)held + back - most);
-    }
+    if (t == 0) write_state(a, first, held, all, most);
   }
 
   if (!ring || !k.known) return;
@@ -186,48 +301,19 @@ __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
   part_of(a.max_pages, wave, lo, hi);
   for (int w = 0; w < wave; ++w) returned += (uint32_t)a.freed[(int64_t)i * kWaves + w];
   int32_t* const row = a.table + (int64_t)i * a.max_pages;
-  // pages of its rows that lie in the parts before this wave's: counted again from the table as it was
-  // (entries are written behind the barrier)
+  // what the parts before this wave's take: counted from the table as it was (entries are written behind the barrier)
   if (is_placed) {
-    int32_t mine = 0;
-    const int32_t from = k.rows > lo ? k.rows : lo, to = k.hi < hi ? k.hi : hi;
-    for (int32_t x = from; x < to; x += kWave) {
-      const int32_t at = x + lane;
-      bool free = false, want = false;
-      if (at < to) ask(a, k, at, row[at], free, want);
-      mine += __popcll(__ballot(want));
-    }
+    int32_t none = 0, mine = 0;
+    count_part(a, k, row, k.rows > lo ? k.rows : lo, k.hi < hi ? k.hi : hi, none, mine);
     __syncthreads();
-    if (lane == 0) sum_s[wave] = (uint32_t)mine;
+    if (lane == 0) sum_s[wave][0] = (uint32_t)mine;
     __syncthreads();
-    for (int w = 0; w < wave; ++w) taken += sum_s[w];
+    for (int w = 0; w < wave; ++w) taken += sum_s[w][0];
   }
-  const uint64_t below = ((uint64_t)1 << lane) - 1;
-#pragma unroll 4
-  for (int32_t x = lo; x < hi; x += kWave) {
-    const int32_t at = x + lane;
-    const int32_t entry = at < a.max_pages ? row[at] : -1;
-    bool free, want;
-    ask(a, k, at, entry, free, want);
-    want = want && is_placed;
-    const uint64_t frees = __ballot(free), wants_here = __ballot(want);
-    if (free) {
-      const uint64_t to = (uint64_t)held + returned + __popcll(frees & below);
-      if (to < (uint64_t)a.n_pages) a.ring[(first + to) % (uint64_t)a.n_pages] = entry;
-      row[at] = -1;
-    }
-    if (want) row[at] = a.ring[(first + taken + __popcll(wants_here & below)) % (uint64_t)a.n_pages];
-    returned += __popcll(frees);
-    taken += __popcll(wants_here);
-  }
+  place_part(a, k, row, lo, hi, first, held, returned, taken, is_placed);
   if (!is_placed || !a.slots) return;
   __syncthreads();
-  for (int32_t j = t; j <= r.k; j += kThreads) {
-    const int32_t s = len + j, page = row[s >> a.page_log2];
-    a.slots[r.row0 + j] = page >= 0 && page < a.n_pages
-                              ? ((int64_t)page << a.page_log2) + (s & ((1 << a.page_log2) - 1))
-                              : -1;
-  }
+  write_slots(a, r, row, len, t, kThreads);
 }
 
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -289,6 +375,10 @@ extern "C" int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, i
   a.window = window;
   a.sinks = sinks;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (B <= kFewWaves && max_pages <= kFewPages) {
+    hipLaunchKernelGGL(place_few, dim3(1), dim3(kFewWaves * kWave), 0, s, a);
+    return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
+  }
   hipLaunchKernelGGL(count, dim3((unsigned)B), dim3(kThreads), 0, s, a);
   hipLaunchKernelGGL(place, dim3((unsigned)B), dim3(kThreads), 0, s, a);
   return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
