@@ -21,8 +21,6 @@ __all__ = ["verify", "verify_ex", "verify_tree", "commit", "repad", "sample", "k
            "TERM_BAD", "TERM_BONUS", "TERM_GREEDY", "TERM_NONE", "TERM_RESIDUAL", "TERM_RESIDUAL_EMPTY", "library_path"]
 
 _DTYPES = {torch.bfloat16: SDV_BF16, torch.float32: SDV_FP32}
-_CODES = torch.float8_e4m3fn
-_SCALES = (torch.uint8, torch.float8_e8m0fnu)
 _WORKSPACE: dict = {}
 
 
@@ -545,27 +543,19 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, temperature=1.0, *, top_
     return tokens, prob, extra
 
 
-def _cache(key_cache, value_cache, page_table, cache_len, offsets, layers=False, scales=None, rows_dtype=None):
-    """Checks one layer's cache (or, with layers, [L, ...] of them) and marshals it: (sdv_cache or, with scales = (key_scales,
-    value_scales), sdv_cache8, device index, B, address of the offsets, n_kv_heads, head_dim)."""
-    dtype = key_cache.dtype
-    if scales is not None:
-        if dtype is not _CODES:
-            raise TypeError("a cache with scales must be float8_e4m3fn")
-        dt = _DTYPES.get(rows_dtype)
-        if dt is None:
-            raise TypeError("rows over a cache in 8 bits must be bfloat16 or float32")
-    else:
-        dt = _DTYPES.get(dtype)
-        if dt is None:
-            raise TypeError("the cache must be bfloat16 or float32, or float8_e4m3fn with key_scales and value_scales")
+def _cache(key_cache, value_cache, page_table, cache_len, offsets, layers=False):
+    """Checks one layer's cache (or, with layers, [L, ...] of them) and marshals it: (sdv_cache, device
+    index, B, address of the offsets, n_kv_heads, head_dim)."""
+    dt = _DTYPES.get(key_cache.dtype)
+    if dt is None:
+        raise TypeError("the cache must be bfloat16 or float32, or float8_e4m3fn with key_scales and value_scales")
     index = key_cache.get_device()
     if index < 0:
         raise ValueError("the cache must be on the GPU")
     shape = key_cache.shape
     if len(shape) != 4 and not (layers and len(shape) == 5) or not key_cache.is_contiguous():
         raise ValueError("key_cache must be a contiguous [n_pages, n_kv_heads, page_size, head_dim] tensor")
-    if value_cache.dtype is not dtype or value_cache.get_device() != index or value_cache.shape != shape \
+    if value_cache.dtype is not key_cache.dtype or value_cache.get_device() != index or value_cache.shape != shape \
             or not value_cache.is_contiguous():
         raise ValueError("value_cache must be like key_cache")
     B = offsets.shape[0] - 1
@@ -578,24 +568,15 @@ def _cache(key_cache, value_cache, page_table, cache_len, offsets, layers=False,
     n_pages, heads, page_size, head_dim = shape[-4:]
     if max(B, table[1], heads, page_size, head_dim) > _INT32_MAX:
         raise ValueError("sizes of the cache beyond 32 bits")
-    c = _native.SdvCache(key_cache.data_ptr(), value_cache.data_ptr(), page_table.data_ptr(), p_len, n_pages, table[1],
-                         page_size, heads, head_dim, dt)
-    if scales is not None:
-        key_scales, value_scales = scales
-        blocks = key_scales.shape[-1] if key_scales.dim() else 0
-        for t in scales:
-            if t.dtype not in _SCALES or t.get_device() != index or blocks < 1 or page_size % blocks \
-                    or t.shape != shape[:-2] + (blocks,) or not t.is_contiguous():
-                raise ValueError("key_scales and value_scales must be contiguous uint8 or float8_e8m0fnu tensors "
-                                 "[n_pages, n_kv_heads, page_size / block] on the cache's device")
-        c = _native.SdvCache8(c, key_scales.data_ptr(), value_scales.data_ptr(), page_size // blocks)
-    return c, index, B, p_offsets, heads, head_dim
+    return (_native.SdvCache(key_cache.data_ptr(), value_cache.data_ptr(), page_table.data_ptr(), p_len, n_pages,
+                             table[1], page_size, heads, head_dim, dt), index, B, p_offsets, heads, head_dim)
 
 
-def _both_scales(key_scales, value_scales):
+def _scaled(key_scales, value_scales) -> bool:
+    """Whether the cache is in 8 bits."""
     if (key_scales is None) != (value_scales is None):
         raise ValueError("key_scales and value_scales are given together")
-    return None if key_scales is None else (key_scales, value_scales)
+    return key_scales is not None
 
 
 def _rows(t, name, rows, heads, head_dim, dtype, index):
@@ -624,10 +605,11 @@ def kv_append(keys: torch.Tensor, values: torch.Tensor, key_cache: torch.Tensor,
 
     sdv_kv_append8, with key_scales and value_scales: the cache holds float8_e4m3fn codes, and the scales (uint8, or
     float8_e8m0fnu, [n_pages, n_kv_heads, page_size / block]) a power of two for each block of tokens and head."""
-    scales = _both_scales(key_scales, value_scales)
-    dtype, rows = key_cache.dtype if scales is None else keys.dtype, keys.shape[0]
-    c, index, B, p_offsets, heads, head_dim = _cache(key_cache, value_cache, page_table, cache_len, offsets,
-                                                     scales=scales, rows_dtype=dtype)
+    if _scaled(key_scales, value_scales):
+        return _native.marshal().kv_append8(keys, values, key_cache, value_cache, page_table, cache_len, offsets, key_scales,
+                                            value_scales, parents, inv_freq, interleaved, queries, queries_out)
+    c, index, B, p_offsets, heads, head_dim = _cache(key_cache, value_cache, page_table, cache_len, offsets)
+    dtype, rows = key_cache.dtype, keys.shape[0]
     if rows < B:
         raise ValueError("keys must have n_draft_rows + B rows")
     ks = _rows(keys, "keys", rows, heads, head_dim, dtype, index)
@@ -649,12 +631,11 @@ def kv_append(keys: torch.Tensor, values: torch.Tensor, key_cache: torch.Tensor,
         p_qo = queries_out.data_ptr()
     elif queries_out is not None:
         raise ValueError("queries_out without queries")
-    append = _native.lib().sdv_kv_append if scales is None else _native.lib().sdv_kv_append8
-    rc = _on(index, lambda stream: append(
+    rc = _on(index, lambda stream: _native.lib().sdv_kv_append(
         ctypes.byref(c), B, rows - B, p_offsets, p_parents, keys.data_ptr(), ks, values.data_ptr(), vs, p_freq, rotary,
         1 if interleaved else 0, p_q, qs, n_q, p_qo, stream))
     if rc != 0:
-        raise SdvError(rc, "sdv_kv_append" if scales is None else "sdv_kv_append8")
+        raise SdvError(rc, "sdv_kv_append")
     return queries_out
 
 
@@ -667,10 +648,12 @@ def attend(queries: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Te
     that kv_append wrote (arguments as there), each row over the slots before it (in a tree, the cached
     slots and its ancestors) within window positions (0: all) or among the first ``sinks`` slots.  scale
     defaults to head_dim ** -0.5.  Returns [n_draft_rows + B, n_q_heads, head_dim]."""
-    scales = _both_scales(key_scales, value_scales)
-    dtype, rows = key_cache.dtype if scales is None else queries.dtype, queries.shape[0]
-    c, index, B, p_offsets, heads, head_dim = _cache(key_cache, value_cache, page_table, cache_len, offsets,
-                                                     scales=scales, rows_dtype=dtype)
+    if _scaled(key_scales, value_scales):
+        return _native.marshal().attend8(queries, key_cache, value_cache, page_table, cache_len, offsets, key_scales,
+                                         value_scales, parents, scale, window, sinks, out, workspace, _scratch,
+                                         key_cache.device)
+    c, index, B, p_offsets, heads, head_dim = _cache(key_cache, value_cache, page_table, cache_len, offsets)
+    dtype, rows = key_cache.dtype, queries.shape[0]
     qs = _rows(queries, "queries", rows, None, head_dim, dtype, index)
     n_q = queries.shape[1]
     if rows < B:
@@ -684,8 +667,6 @@ def attend(queries: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Te
     elif out.dtype is not dtype or out.get_device() != index or out.shape != queries.shape or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor like queries")
     lib = _native.lib()
-    need, launch = (lib.sdv_attend_workspace_bytes, lib.sdv_attend) if scales is None else \
-        (lib.sdv_attend8_workspace_bytes, lib.sdv_attend8)
     p_c = ctypes.byref(c)
     scale = head_dim ** -0.5 if scale is None else float(scale)
     window, sinks = _int32(window), _int32(sinks)  # slots are numbered below 2^31: what is larger sees no more
@@ -693,13 +674,13 @@ def attend(queries: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Te
     def call(stream):
         ws = workspace
         if ws is None:
-            ws = _scratch(need(p_c, B, rows - B, n_q, window, sinks), dev, index, stream)
-        return launch(p_c, B, rows - B, p_offsets, p_parents, queries.data_ptr(), qs, n_q, scale, window, sinks,
-                      out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), stream)
+            ws = _scratch(lib.sdv_attend_workspace_bytes(p_c, B, rows - B, n_q, window, sinks), dev, index, stream)
+        return lib.sdv_attend(p_c, B, rows - B, p_offsets, p_parents, queries.data_ptr(), qs, n_q, scale, window, sinks,
+                              out.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), stream)
 
     rc = _on(index, call)
     if rc != 0:
-        raise SdvError(rc, "sdv_attend" if scales is None else "sdv_attend8")
+        raise SdvError(rc, "sdv_attend")
     return out
 
 
@@ -709,19 +690,19 @@ def kv_settle(key_cache: torch.Tensor, value_cache: torch.Tensor, page_table: to
     """sdv_kv_settle, or with the scales of caches in 8 bits sdv_kv_settle8: moves the accepted path of verified token trees (accepted_len and accepted_nodes of
     verify_tree) to the slots where the sequences continue, in one layer's cache or in all of
     [n_layers, n_pages, n_kv_heads, page_size, head_dim].  Returns the new cache lengths, int32 [B]."""
-    scales = _both_scales(key_scales, value_scales)
-    c, index, B, p_offsets, _, _ = _cache(key_cache, value_cache, page_table, cache_len, offsets, layers=True,
-                                          scales=scales, rows_dtype=torch.bfloat16)
+    if _scaled(key_scales, value_scales):
+        return _native.marshal().kv_settle8(key_cache, value_cache, page_table, cache_len, offsets, accepted_len,
+                                            accepted_nodes, key_scales, value_scales)
+    c, index, B, p_offsets, _, _ = _cache(key_cache, value_cache, page_table, cache_len, offsets, layers=True)
     n_d = accepted_nodes.numel()
     p_acc = _vector(accepted_len, torch.int32, B, index, "accepted_len")
     p_nodes = _vector(accepted_nodes, torch.int32, n_d, index, "accepted_nodes")
     new_len = torch.empty(B, dtype=torch.int32, device=key_cache.device)
     layers = key_cache.shape[0] if key_cache.dim() == 5 else 1
-    settle = _native.lib().sdv_kv_settle if scales is None else _native.lib().sdv_kv_settle8
-    rc = _on(index, lambda stream: settle(
+    rc = _on(index, lambda stream: _native.lib().sdv_kv_settle(
         ctypes.byref(c), layers, B, n_d, p_offsets, p_acc, p_nodes if n_d else None, new_len.data_ptr(), stream))
     if rc != 0:
-        raise SdvError(rc, "sdv_kv_settle" if scales is None else "sdv_kv_settle8")
+        raise SdvError(rc, "sdv_kv_settle")
     return new_len
 
 
@@ -735,40 +716,5 @@ def kv_pages(page_table: torch.Tensor, cache_len: torch.Tensor, offsets: torch.T
     (offsets as for kv_append, cache_len -1 for a request that has ended) get pages.  Returns (placed int32 [B]: 1 where
     all rows of a request have pages, 0 where not or where it has ended, -1 for one that is not valid; slots int64 [n_draft_rows
     + B]: page * page_size + place of each row of a placed request, else -1)."""
-    index = page_table.get_device()
-    if index < 0:
-        raise ValueError("page_table must be on the GPU")
-    shape = page_table.shape
-    if page_table.dtype is not torch.int32 or len(shape) != 2 or not page_table.is_contiguous():
-        raise ValueError("page_table must be a contiguous int32 [B, max_pages] tensor")
-    B, max_pages = shape
-    n_d, n_pages = int(n_draft_rows), free_pages.numel()
-    if B < 1 or n_d < 0:
-        raise ValueError("B >= 1 requests and n_draft_rows >= 0 rows are needed")
-    if max(B, max_pages, n_pages, n_d + B) > _INT32_MAX:
-        raise ValueError("sizes beyond 32 bits")
-    p_len = _vector(cache_len, torch.int32, B, index, "cache_len")
-    p_offsets = _vector(offsets, torch.int32, B + 1, index, "offsets")
-    p_free = _vector(free_pages, torch.int32, n_pages, index, "free_pages")
-    p_state = _vector(free_state, torch.int32, 2, index, "free_state")
-    dev = page_table.device
-    if placed is None:
-        placed = torch.empty(B, dtype=torch.int32, device=dev)
-    if slots is None:
-        slots = torch.empty(n_d + B, dtype=torch.int64, device=dev)
-    p_placed = _vector(placed, torch.int32, B, index, "placed")
-    p_slots = _vector(slots, torch.int64, n_d + B, index, "slots")
-    lib = _native.lib()
-
-    def call(stream):
-        ws = workspace
-        if ws is None:
-            ws = _scratch(lib.sdv_kv_pages_workspace_bytes(B), dev, index, stream)
-        return lib.sdv_kv_pages(page_table.data_ptr(), B, max_pages, _int32(page_size), p_len, n_d, p_offsets, n_pages,
-                                p_free, p_state, _int32(window), _int32(sinks), p_placed, p_slots, _ptr(ws),
-                                0 if ws is None else ws.numel() * ws.element_size(), stream)
-
-    rc = _on(index, call)
-    if rc != 0:
-        raise SdvError(rc, "sdv_kv_pages")
-    return placed, slots
+    return _native.marshal().kv_pages(page_table, cache_len, offsets, n_draft_rows, free_pages, free_state, page_size, window,
+                                      sinks, slots, placed, workspace, _scratch, page_table.device)

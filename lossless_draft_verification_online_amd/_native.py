@@ -104,6 +104,23 @@ _VERIFY_ARGS = [
 ]
 
 
+_MARSHAL = None
+
+
+def marshal():
+    """The module that marshals the calls over a cache in 8 bits and the pages' call.  No fallback, as for the library."""
+    global _MARSHAL
+    if _MARSHAL is None:
+        lib()
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise RuntimeError("_marshal.so is not built; run __graft_entry__.build()") from e
+        _marshal.bind(SdvError)
+        _MARSHAL = _marshal
+    return _MARSHAL
+
+
 def lib(path: str = LIBRARY) -> ctypes.CDLL:
     """Load libsdv.so.  There is no fallback: a missing library is an error."""
     global _LIB

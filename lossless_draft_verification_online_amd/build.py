@@ -19,6 +19,9 @@ DEPENDS = SOURCES + [os.path.join(PKG, "csrc", "sdv_device.hpp"), os.path.join(P
                      os.path.join(PKG, "csrc", "cache8_view.hpp"), os.path.join(PKG, "csrc", "launch.hpp"),
                      os.path.join(ROOT, "include", "sdv.h")]
 LIBRARY = os.path.join(PKG, "libsdv.so")
+# The Python module that marshals the newer calls' tensors: host code, on torch's C++ interface.
+MARSHAL_SOURCE = os.path.join(PKG, "csrc", "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
@@ -30,7 +33,7 @@ HIPCC_FLAGS = [
 def _compile(cmd: list, what: str) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed on {what} ({res.returncode}):\n{res.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed on {what} ({res.returncode}):\n{res.stderr}")
     return res.stderr
 
 
@@ -49,6 +52,25 @@ def build_library(out: str = LIBRARY, verbose: bool = False) -> str:
     return out
 
 
+def build_marshal(out: str = MARSHAL) -> str:
+    """_marshal.so, beside libsdv.so, which it is linked with."""
+    import sysconfig
+
+    import torch
+    where = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    includes = [os.path.join(where, "include"), os.path.join(where, "include", "torch", "csrc", "api", "include"),
+                os.path.join(rocm, "include"), sysconfig.get_paths()["include"]]
+    tmp = out + ".tmp"
+    _compile(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+              f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+              *[x for i in includes for x in ("-isystem", i)], MARSHAL_SOURCE, "-o", tmp,
+              f"-L{os.path.join(where, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip",
+              LIBRARY, "-Wl,-rpath,$ORIGIN"], MARSHAL_SOURCE)
+    os.replace(tmp, out)
+    return out
+
+
 def is_stale(path: str = LIBRARY) -> bool:
     if not os.path.exists(path):
         return True
@@ -57,4 +79,4 @@ def is_stale(path: str = LIBRARY) -> bool:
 
 
 if __name__ == "__main__":
-    print(build_library(verbose=True))
+    print(build_library(verbose=True), build_marshal())
