@@ -11,14 +11,18 @@ namespace attend8_impl {
 using namespace sdv;
 using namespace attend_impl;
 
-enum Mode { kUnits, kRanges, kSmallPages, kRows };
+enum Mode { kUnits, kFewUnits, kRanges, kSmallPages, kRows };
 
 static int64_t kManyColumns_() { const char* e = getenv("KC"); return e ? atoll(e) : 96; }
 constexpr int64_t kManyWorkgroups = 128;
 
 constexpr int64_t kShort = 32, kSomeUnits = 64;
 constexpr int64_t kManyUnits = 2048;
-constexpr int64_t kFewUnits = 128;
+constexpr int64_t kUnpaired = 128;
+// Eight waves for a unit instead of four, up to as many units of 16 columns: a wave waits 1 us for each of its tiles (one row of 17 tiles
+// 9.3 us for 10.2, 16 trees of 33 tiles 14.5 for 17.3, 64 units of 32 tiles 11.6 for 13.8; 256 units of 16 tiles 17.7 for 13.0).
+constexpr int64_t kEightWaves = 128;
+constexpr int kFewWaves = 8;
 static int64_t places() { const char* e = getenv("KP"); return e ? atoll(e) : 512; }
 
 struct Plan {
@@ -52,7 +56,8 @@ inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int
   const bool split = tokens > (units_of(16) < kSomeUnits ? kShort : 2 * kShort) && B <= 512 &&
                      rows <= 64 * (int64_t)B && units_of(32) < kManyUnits;
   p.mode = c->page_size < 16 ? kSmallPages : (split ? kRanges : kUnits);
-  if (pairs && (p.mode == kRanges || units_of(16) > kFewUnits)) p.qb = 2;
+  if (pairs && (p.mode == kRanges || units_of(16) > kUnpaired)) p.qb = 2;
+  if (p.mode == kUnits && p.qb == 1 && c->head_dim <= 128 && units_of(16) <= kEightWaves) p.mode = kFewUnits;
   p.tiles = rows * G / (16 * p.qb) + B;
   if (p.mode == kRanges) {
     const int64_t units = units_of(16 * p.qb) / c->n_kv_heads, groups = (units * tokens + kStreamWaves - 1) / kStreamWaves;
@@ -72,6 +77,12 @@ inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int
 template <class E, int D, int QB>
 int launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
   const dim3 units((unsigned)(a.tiles * a.cache.n_heads)), threads(kStreamWaves * kWave);
+  if constexpr (QB == 1 && D <= 128) {
+    if (p.mode == kFewUnits) {
+      hipLaunchKernelGGL((attend_units<E, D, QB, kFewWaves, true, true>), units, dim3(kFewWaves * kWave), 0, s, a);
+      return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
+    }
+  }
   if (p.mode == kSmallPages) {
     hipLaunchKernelGGL((attend_units<E, D, QB, kStreamWaves, false, true>), units, threads, 0, s, a);
   } else if (p.mode == kUnits) {
@@ -142,7 +153,7 @@ extern "C" int sdv_attend8(const sdv_cache8* cache, int32_t B, int64_t n_draft_r
   if (query_stride > ((int64_t)1 << 31)) return SDV_ERR_LIMIT;
   const Plan p = plan_of(c, B, n_draft_rows, n_q_heads, window, sinks, parents != nullptr);
   static_assert(kStreamWaves == kJoinWaves && kStreamWaves == kRowsWaves, "one bound for every launch");
-  if (too_many(p.tiles * c->n_kv_heads, kStreamWaves * kWave)) return SDV_ERR_LIMIT;
+  if (too_many(p.tiles * c->n_kv_heads, (p.mode == kFewUnits ? kFewWaves : kStreamWaves) * kWave)) return SDV_ERR_LIMIT;
   if (p.bytes > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < p.bytes)) return SDV_ERR_WORKSPACE;
   AttendArgs a;
   a.cache = view_of(c);
@@ -171,3 +182,4 @@ extern "C" int sdv_attend8(const sdv_cache8* cache, int32_t B, int64_t n_draft_r
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   return c->dtype == SDV_BF16 ? launch_dim<Bf16>(a, c->head_dim, p, s) : launch_dim<F32>(a, c->head_dim, p, s);
 }
+

@@ -132,6 +132,35 @@ __device__ __forceinline__ TileOf tile_of(const AttendArgs& a, int64_t tile) {
   return tile_in<kColumns>(a, r, tile);
 }
 
+// tile_of, and the request's cached length: the lengths are loaded beside the offsets, where one wave holds those of all requests, since
+// a workgroup has nothing to do until its pages are known.
+template <int kColumns>
+__device__ __forceinline__ TileOf tile_and_length(const AttendArgs& a, int64_t tile, int32_t& len) {
+  if (a.B > kWave) {
+    const TileOf t = tile_of<kColumns>(a, tile);
+    len = t.r.index >= 0 ? a.cache.len[t.r.index] : -1;
+    return t;
+  }
+  const int lane = threadIdx.x & (kWave - 1);
+  const bool in = lane < a.B;
+  const int32_t mine = in ? lane : a.B - 1;
+  const int32_t lo = a.cu[mine], hi = a.cu[mine + 1], n = a.cache.len[mine];
+  const int64_t first = (uint32_t)(lo + mine) * (uint32_t)a.G / (uint32_t)kColumns + mine;  // first_tile
+  const uint64_t who = __ballot(in && first <= tile);
+  const int src = who ? 63 - __builtin_clzll(who) : 0;
+  Request r;
+  r.index = src;
+  r.first = lane_value(lo, src);
+  r.k = lane_value(hi, src) - r.first;
+  r.row0 = (int64_t)r.first + src;
+  len = lane_value(n, src);
+  if (__builtin_expect(!who || (who & (who + 1)) || r.first < 0 || r.k < 0 || (int64_t)r.first + r.k > a.n_d, 0)) {
+    r = request_at(a.cu, tile_among<kColumns>(a, tile), a.n_d);  // some offsets are not valid
+    len = r.index >= 0 ? a.cache.len[r.index] : -1;
+  }
+  return tile_in<kColumns>(a, r, tile);
+}
+
 // Workgroups go to the 8 XCDs in turn.  Each XCD takes a run of neighbouring units instead: the heads of one page
 // lie next to each other, so an XCD then reads whole pages (paged reads 5.0 -> 6.0 TB/s), and tiles
 // of one request share its L2.
@@ -874,10 +903,15 @@ template <class E, int D, int QB, int kWaves, bool kWholePages, bool k8>
 __global__ __launch_bounds__(kWaves* kWave, (kMinWaves<E, D, QB>)) void attend_units(AttendArgs a) {
   __shared__ Scratch<E, D, QB, kWaves, k8> sh;
   const int64_t block = unit_of_block(blockIdx.x, gridDim.x);
-  const TileOf at = tile_of<16 * QB>(a, block / a.cache.n_heads);
+  TileOf at;
+  int32_t len = 0;
+  if constexpr (k8)
+    at = tile_and_length<16 * QB>(a, block / a.cache.n_heads, len);
+  else
+    at = tile_of<16 * QB>(a, block / a.cache.n_heads);
   if (at.r.index < 0) return;
-  attend_unit<E, D, QB, kWaves, kWholePages, k8>(a, sh, at, a.cache.len[at.r.index], (int32_t)(block % a.cache.n_heads),
-                                             false, 0, 0, -1);
+  attend_unit<E, D, QB, kWaves, kWholePages, k8>(a, sh, at, k8 ? len : a.cache.len[at.r.index],
+                                                 (int32_t)(block % a.cache.n_heads), false, 0, 0, -1);
 }
 
 // A workgroup per range of the batch's work.

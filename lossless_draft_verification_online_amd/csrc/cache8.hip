@@ -350,15 +350,16 @@ struct Settle8Args {
   const int32_t* accepted_len;
   const int32_t* accepted_nodes;
   int32_t* new_len;
-  int32_t D;
 };
 
-// One workgroup per request and (layer, keys or values, head): all accepted tokens' codes are read before any is written, and
-// the scales of the blocks that they come from before those of the blocks that they go to.
-__global__ __launch_bounds__(kThreads) void settle8(Settle8Args a) {
+// One wave per request and (layer, keys or values, head): all accepted tokens' codes are read before any is written, and the
+// scales of the blocks that they come from before those of the blocks that they go to.  Bound by the chain of offsets and lengths,
+// nodes, pages, scales and rows: 64 trees in four layers 5.0 us, one in one layer 3.5 (by workgroups of four waves, of which most had nothing to move, 9.4 and 4.2).
+template <int D>
+__global__ __launch_bounds__(kWave) void settle8(Settle8Args a) {
+  constexpr int kVecs = D / 16, kRows = kWave / kVecs, kGroups = kMaxNodes / kRows;  // of 16 bytes; rows that the wave moves at once
   __shared__ int64_t from_s[kMaxNodes], to_s[kMaxNodes];
-  __shared__ int32_t byte_s[kMaxNodes], most_s[kMaxNodes + 1];
-  __shared__ int32_t ok_s, old_s;
+  __shared__ int32_t shift_s[kMaxNodes], most_s[kMaxNodes];
   const CacheView& cache = a.view.cache;
   const int t = threadIdx.x;
   const int32_t i = blockIdx.x;
@@ -368,84 +369,73 @@ __global__ __launch_bounds__(kThreads) void settle8(Settle8Args a) {
   const Request r = request_at(a.cu, i, a.n_d);
   const int32_t len = cache.len[i], acc = a.accepted_len[i];
   bool ok = r.index >= 0 && len_fits(len, r.k) && acc >= 0 && acc <= r.k && r.k <= kMaxNodes;
+  int32_t node = t;
+  if (ok && t < acc) node = a.accepted_nodes[r.first + t];
+  const int32_t before = __shfl_up(node, 1);
+  ok = ok && __ballot(t < acc && !(node > (t ? before : -1) && node < r.k)) == 0;
+  if (t == 0 && blockIdx.y == 0) a.new_len[i] = ok ? len + 1 + acc : len;
+  if (!ok || acc == 0) return;
+
   const int32_t log2 = a.view.block_log2, block_0 = (len + 1) >> log2;  // of blocks of the sequence
   const int32_t first = block_0 << log2;                                // first slot of the block that acceptance begins in
-  if (t < kMaxNodes + 1) most_s[t] = 0;
-  __syncthreads();
-  if (t < kWave) {
-    bool fine = true;
-    int64_t from = -1, to = -1;
-    int32_t byte = 0;
-    if (ok && t < acc) {
-      const int32_t node = a.accepted_nodes[r.first + t];
-      const int32_t before = t > 0 ? a.accepted_nodes[r.first + t - 1] : -1;
-      fine = node > before && node < r.k && before >= -1;
-      if (fine) {
-        const int64_t src = (int64_t)len + 1 + node, dst = (int64_t)len + 1 + t;
-        const int32_t sp = cache.page(i, src), dp = cache.page(i, dst);
-        if (dp >= 0) {
-          to = cache.row(dp, head, dst);
-          from = sp >= 0 ? cache.row(sp, head, src) : to;
-          byte = scale_byte(scales[sp >= 0 ? a.view.scale_at(sp, head, src) : a.view.scale_at(dp, head, dst)]);
-          atomicMax(&most_s[((len + 1 + t) >> log2) - block_0], byte);
-        }
-      }
-    }
-    fine = __ballot(!fine) == 0;
-    from_s[t] = from;
-    to_s[t] = to;
-    byte_s[t] = byte;
-    if (t == 0) {
-      ok_s = ok && fine;
-      old_s = 0;
-      if (ok && fine && to >= 0 && first <= len) {  // the first block holds slots up to len
-        old_s = scale_byte(scales[a.view.scale_at(cache.page(i, first), head, first)]);
-        atomicMax(&most_s[0], old_s);
-      }
+  const int64_t src = (int64_t)len + 1 + node, dst = (int64_t)len + 1 + t;
+  const int32_t block = (int32_t)(dst >> log2) - block_0;
+  most_s[t] = 0;
+  int64_t from = -1, to = -1, scale_to = -1;
+  int32_t byte = 0, old = 0;
+  if (t < acc) {
+    const int32_t sp = cache.page(i, src), dp = cache.page(i, dst);
+    if (dp >= 0) {
+      to = cache.row(dp, head, dst);
+      from = sp >= 0 ? cache.row(sp, head, src) : to;  // without a page to come from it stays what is there
+      scale_to = a.view.scale_at(dp, head, dst);
+      byte = scale_byte(scales[sp >= 0 ? a.view.scale_at(sp, head, src) : scale_to]);
+      if (t == 0 && first <= len) old = scale_byte(scales[scale_to]);  // the first block holds slots up to len
     }
   }
   __syncthreads();
-  ok = ok_s;
-  if (t == 0 && blockIdx.y == 0) a.new_len[i] = ok ? len + 1 + acc : len;
-  if (!ok) return;
-  const int vecs = a.D / 16;         // 4 to 16, a power of two
-  const int rows = kThreads / vecs;  // 16 to 64: at most four groups of rows
-  const int k = t & (vecs - 1), d0 = t / vecs;
-  u32x4 v[4];
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int32_t d = g * rows + d0;
-    if (d < acc && from_s[d < kMaxNodes ? d : 0] >= 0)
-      v[g] = *reinterpret_cast<const u32x4*>(base + from_s[d] * a.D + k * 16);
-  }
+  if (to >= 0) atomicMax(&most_s[block], byte > old ? byte : old);
   __syncthreads();
+  const int32_t most = t < acc ? most_s[block] : 0;
+  from_s[t] = from;
+  to_s[t] = to;
+  shift_s[t] = to >= 0 ? most - byte : 0;
+  __syncthreads();
+  const int k = t % kVecs, d0 = t / kVecs;
+  u32x4 v[kGroups];
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int32_t d = g * rows + d0;
-    if (d >= acc || from_s[d < kMaxNodes ? d : 0] < 0) continue;
-    const int32_t shift = most_s[((len + 1 + d) >> log2) - block_0] - byte_s[d];
+  for (int g = 0; g < kGroups; ++g) {
+    if (g * kRows >= acc) break;
+    const int32_t d = g * kRows + d0;
+    if (from_s[d] >= 0) v[g] = *reinterpret_cast<const u32x4*>(base + from_s[d] * D + k * 16);
+  }
+  __syncthreads();  // all are read
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    if (g * kRows >= acc) break;
+    const int32_t d = g * kRows + d0;
+    if (from_s[d] < 0) continue;
+    const int32_t shift = shift_s[d];
     if (shift > 0) {
 #pragma unroll
       for (int w = 0; w < 4; ++w) v[g][w] = shifted_codes(v[g][w], shift);
     }
-    if (shift > 0 || from_s[d] != to_s[d]) *reinterpret_cast<u32x4*>(base + to_s[d] * a.D + k * 16) = v[g];
+    if (shift > 0 || from_s[d] != to_s[d]) *reinterpret_cast<u32x4*>(base + to_s[d] * D + k * 16) = v[g];
   }
   // what the first block held up to len
-  const int32_t old = old_s, shift = most_s[0] - old;
-  if (old > 0 && shift > 0) {
-    char* const from = base + (to_s[0] - (len + 1 - first)) * a.D;
-    for (int x = t; x < (len + 1 - first) * vecs; x += kThreads) {
-      u32x4* const p = reinterpret_cast<u32x4*>(from + x * 16);
+  const int32_t held = lane_value(old, 0), up = lane_value(most, 0) - held;
+  if (held > 0 && up > 0) {
+    char* const at = base + (to_s[0] - (len + 1 - first)) * D;
+    for (int x = t; x < (len + 1 - first) * kVecs; x += kWave) {
+      u32x4* const p = reinterpret_cast<u32x4*>(at + x * 16);
       u32x4 w = *p;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = shifted_codes(w[e], shift);
+      for (int e = 0; e < 4; ++e) w[e] = shifted_codes(w[e], up);
       *p = w;
     }
   }
   // a block's scale, by its first token
-  if (t < acc && to_s[t] >= 0 && (t == 0 || ((len + 1 + t) >> log2) != ((len + t) >> log2)))
-    scales[a.view.scale_at(cache.page(i, (int64_t)len + 1 + t), head, (int64_t)len + 1 + t)] =
-        (uint8_t)most_s[((len + 1 + t) >> log2) - block_0];
+  if (to >= 0 && (t == 0 || block != (int32_t)((dst - 1) >> log2) - block_0)) scales[scale_to] = (uint8_t)most;
 }
 
 }  // namespace cache8_impl
@@ -526,14 +516,19 @@ extern "C" int sdv_kv_settle8(const sdv_cache8* cache, int32_t n_layers, int32_t
   Settle8Args a;
   a.view = view_of(cache);
   a.n_d = n_draft_rows;
-  a.D = c.head_dim;
   a.layer_bytes = c.n_pages * c.n_kv_heads * (int64_t)c.page_size * c.head_dim;
   a.layer_scales = c.n_pages * c.n_kv_heads * (int64_t)(c.page_size / cache->block);
   a.cu = ragged_offsets;
   a.accepted_len = accepted_len;
   a.accepted_nodes = accepted_nodes;
   a.new_len = new_len;
-  hipLaunchKernelGGL(settle8, dim3((unsigned)B, (unsigned)(n_layers * c.n_kv_heads * 2)), dim3(kThreads), 0,
-                     reinterpret_cast<hipStream_t>(stream), a);
+  const dim3 grid((unsigned)B, (unsigned)(n_layers * c.n_kv_heads * 2)), threads(kWave);
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  if (c.head_dim == 64)
+    hipLaunchKernelGGL(settle8<64>, grid, threads, 0, s, a);
+  else if (c.head_dim == 128)
+    hipLaunchKernelGGL(settle8<128>, grid, threads, 0, s, a);
+  else
+    hipLaunchKernelGGL(settle8<256>, grid, threads, 0, s, a);
   return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
 }
