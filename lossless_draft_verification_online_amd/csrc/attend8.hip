@@ -2,7 +2,6 @@
 // head: sdv_attend8.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
-#include <stdlib.h>
 
 #include "attend_rows.hpp"
 
@@ -13,17 +12,44 @@ using namespace attend_impl;
 
 enum Mode { kUnits, kFewUnits, kRanges, kSmallPages, kRows };
 
-static int64_t kManyColumns_() { const char* e = getenv("KC"); return e ? atoll(e) : 96; }
-constexpr int64_t kManyWorkgroups = 128;
+// The rules, by what the host knows: the batch's mean columns of a request, and for its lengths the page table's width (under a
+// window, the window).  Times of 8 heads of 128 values, bf16 rows, for one side and the other; a tile is of 32 tokens, a unit of 16
+// columns on one head.
+//
+// attend_rows from this many columns of a request and this many workgroups on: 16 requests of 256 columns on 1000 tokens 47.9 us for
+// 50.6 by units, of 512 on 4000 181 for 293, one of 4096 on 1000 59 for 86; 64 of 128 on 4000 340 for 316, 4 of 512 on 4000
+// (128 workgroups) 113 for 76 by ranges.
+constexpr int64_t kManyColumns = 256, kManyWorkgroups = 256;
 
-constexpr int64_t kShort = 32, kSomeUnits = 64;
-constexpr int64_t kManyUnits = 2048;
-constexpr int64_t kUnpaired = 128;
-// Eight waves for a unit instead of four, up to as many units of 16 columns: a wave waits 1 us for each of its tiles (one row of 17 tiles
-// 9.3 us for 10.2, 16 trees of 33 tiles 14.5 for 17.3, 64 units of 32 tiles 11.6 for 13.8; 256 units of 16 tiles 17.7 for 13.0).
-constexpr int64_t kEightWaves = 128;
+// Eight waves for a unit instead of four, up to as many units: a wave waits 1 us for each of its tiles (one request of 47 tiles 15.2 us
+// for 18.0, 16 of 63 20.3 for 25.9, 24 of 63 22.1 for 31.0).  A second round of such workgroups costs more than they gain (32
+// requests of 12 or 20 columns on 16 tiles, over 256 units, 17.7 for 13.0).
+constexpr int64_t kEightWaves = 192;
 constexpr int kFewWaves = 8;
-static int64_t places() { const char* e = getenv("KP"); return e ? atoll(e) : 512; }
+
+// Units of 16 columns up to which they are not paired (32 requests of 32 columns on 1000 tokens, 512 units, 21.0 us for 25.3 in
+// pairs, 40 of them 25.5 for 26.2, 64 42.3 for 31.3).  Ranges are in pairs: they read the cache again for each column tile (64 of 20
+// columns on 4000 tokens 105 us for 190).  Heads of 256 values never are: a pair takes the registers of all waves (16 of 64 columns
+// on 4000 tokens 72 us for 106 by ranges, 84 for 93 by units), nor are binary32 ones above 64.
+constexpr int64_t kUnpaired = 640;
+
+// Ranges from more tiles on than this: one request on 47 tiles 15.6 us for 15.2 by units, on 63 12.5 for 17.9; 16 (128 units) on 126
+// 34.3 for 33.7, on 94 29.1 for 26.4; 32 (256 units) on 63 35.0 for 32.1, on 126 61 for 66; 64 (512 units) on 31 30.2 for 28.9, on 63
+// 58.0 for 60.6; 256 (2048 units) on 31 122 either way, on 63 213 for 228.
+inline int64_t short_of(int64_t units) {
+  if (units <= kEightWaves) return units > 48 ? units : 48;
+  return units < 512 ? 96 : 48;
+}
+
+// Requests of several column tiles run by units, whose tiles read the cache at one time, but for few of them (64 of 64 columns on 4000
+// tokens 167 us for 214 by ranges, 16 of 128 74 for 80; 16 of 64 69 for 57, 4 of 512 111 for 76, one of 512 57 for 41).
+constexpr int64_t kFewPairs = 256, kFewRequests = 4;
+
+// Ranges take all of a request's tokens for each of its rows: rows up to this part of the tokens.
+constexpr int64_t kRowsOfTokens = 8;
+
+// Workgroups at once: two per compute unit.
+constexpr int64_t kPlaces = 512;
 
 struct Plan {
   int qb;
@@ -46,24 +72,26 @@ inline Plan plan_of(const sdv_cache* c, int32_t B, int64_t n_d, int32_t n_q, int
   auto units_of = [&](int64_t columns) { return (mean + columns - 1) / columns * B * c->n_kv_heads; };
   Plan p = {};
   p.qb = 1;
-  if (!tree && c->dtype == SDV_BF16 && c->head_dim <= 128 && c->page_size >= 16 && mean >= kManyColumns_() &&
+  if (!tree && c->dtype == SDV_BF16 && c->head_dim <= 128 && c->page_size >= 16 && mean >= kManyColumns &&
       units_of(kRowsColumns) >= kManyWorkgroups) {
     p.mode = kRows;
     p.tiles = rows * G / kRowsColumns + B;
     return p;
   }
-  const bool pairs = mean > 16 && !(c->dtype == SDV_FP32 && c->head_dim > 64);
-  const bool split = tokens > (units_of(16) < kSomeUnits ? kShort : 2 * kShort) && B <= 512 &&
-                     rows <= 64 * (int64_t)B && units_of(32) < kManyUnits;
+  const int64_t units = units_of(16);
+  const bool pairs = mean > 16 && c->head_dim <= (c->dtype == SDV_FP32 ? 64 : 128);
+  const bool split = tokens > short_of(units) && B <= 512 && rows * kRowsOfTokens <= tokens * kTile * B &&
+                     (mean <= 32 || units_of(32) <= kFewPairs || B <= kFewRequests);
   p.mode = c->page_size < 16 ? kSmallPages : (split ? kRanges : kUnits);
-  if (pairs && (p.mode == kRanges || units_of(16) > kUnpaired)) p.qb = 2;
-  if (p.mode == kUnits && p.qb == 1 && c->head_dim <= 128 && units_of(16) <= kEightWaves) p.mode = kFewUnits;
+  if (pairs && (p.mode == kRanges || units > kUnpaired)) p.qb = 2;
+  if (p.mode == kUnits && p.qb == 1 && c->head_dim <= 128 && units <= kEightWaves) p.mode = kFewUnits;
   p.tiles = rows * G / (16 * p.qb) + B;
   if (p.mode == kRanges) {
-    const int64_t units = units_of(16 * p.qb) / c->n_kv_heads, groups = (units * tokens + kStreamWaves - 1) / kStreamWaves;
-    const int64_t most = places() / c->n_kv_heads > 0 ? places() / c->n_kv_heads : 1;
+    const int64_t per_head = units_of(16 * p.qb) / c->n_kv_heads;
+    const int64_t groups = (per_head * tokens + kStreamWaves - 1) / kStreamWaves;
+    const int64_t most = kPlaces / c->n_kv_heads > 0 ? kPlaces / c->n_kv_heads : 1;
     p.ranges = (int32_t)(groups < most ? groups : most);
-    p.pieces = (int32_t)((p.ranges + units - 1) / units) + 1;
+    p.pieces = (int32_t)((p.ranges + per_head - 1) / per_head) + 1;
     const size_t n = (size_t)2 * p.ranges * c->n_kv_heads * 16 * p.qb;
     p.part_bytes = up256(n * c->head_dim * 4);
     p.stat_bytes = up256(n * 8);
@@ -106,7 +134,7 @@ int launch_columns(const AttendArgs& a, const Plan& p, hipStream_t s) {
       return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
     }
   }
-  if constexpr (E::kBytes == 2 || D <= 64) {
+  if constexpr (D <= (E::kBytes == 2 ? 128 : 64)) {
     if (p.qb == 2) return launch<E, D, 2>(a, p, s);
   }
   return launch<E, D, 1>(a, p, s);

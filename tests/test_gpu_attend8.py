@@ -97,24 +97,24 @@ def test_prompts_under_windows(window, sinks):
     check(b, window, sinks)
 
 
-# Batches of many columns of a request and many workgroups of 128 columns.
+# Batches of 256 columns of a request and more, and 256 workgroups of 128 of them, which the prompts' kernel takes.
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("length", [0, 1, 29, 64, 128, 129])
 def test_many_heads_of_few_tiles(length, D):
-    check(Batch8([27, 31, 33], [length, length + 37, length + 64], 48, D, 16, 4, "bf16", length, Hq=192))
+    check(Batch8([27, 31, 33], [length, length + 37, length + 64], 24, D, 16, 4, "bf16", length, Hq=384))
 
 
 @pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (1, 3), (64, 0), (100, 40), (90, 200), (5000, 3)])
 def test_many_heads_under_windows(window, sinks):
-    check(Batch8([127, 300, 64], [33, 500, 0], 4, 128, 16, 16, "bf16", window, Hq=32), window, sinks)
-    b = Batch8([127, 300, 64], [33, 500, 0], 8, 64, 64, 32, "bf16", window, Hq=32)
+    check(Batch8([127, 300, 64], [33, 500, 0], 8, 128, 16, 16, "bf16", window, Hq=64), window, sinks)
+    b = Batch8([127, 300, 64], [33, 500, 0], 16, 64, 64, 32, "bf16", window, Hq=64)
     b.table[1, 2:4] = [-1, b.n_pages]  # pages that are missing
     check(b, window, sinks, scale=-0.2)
 
 
 @pytest.mark.parametrize("D,page,block", [(64, 16, 1), (128, 32, 2), (128, 128, 64), (64, 1024, 8)])
 def test_many_heads_of_other_blocks(D, page, block):
-    b = Batch8([127, 300, 64], [33, 200, 0], 4, D, page, block, "bf16", page, Hq=32)
+    b = Batch8([127, 300, 64], [33, 200, 0], 8, D, page, block, "bf16", page, Hq=64)
     rng = np.random.default_rng(page)
     b.ks8[:], b.vs8[:] = rng.integers(112, 122, b.ks8.shape), rng.integers(110, 130, b.vs8.shape)
     check(b, 150, 5)
@@ -136,6 +136,21 @@ def test_long_caches_are_split():
     check(Batch8([4, 0], [5000, 20], 1, 64, 16, 4, "fp32", 5, Hq=4), 4096, 4)
     check(Batch8([0, 1], [6000, 0], 1, 256, 64, 32, "bf16", 6, Hq=4))
     check(Batch8([2, 1], [6000, 40], 1, 128, 128, 64, "fp32", 7, Hq=20))
+    check(Batch8([2, 1, 8], [1700, 40, 1600], 3, 128, 16, 16, "bf16", 8, Hq=12))
+    check(Batch8([70], [3000], 2, 64, 16, 16, "bf16", 9, Hq=8), 0, 0)  # many columns of one request
+    check(Batch8([0, 0], [20000, 7], 1, 128, 64, 64, "bf16", 10, Hq=4))  # units of many pieces
+    check(Batch8([20, 64], [2500, 3000], 1, 64, 16, 8, "fp32", 11, tree=True, Hq=4), 2000, 3)
+
+
+def test_long_caches_of_many_requests():
+    """More requests than a wave has lanes, some of them empty or not valid, in ranges."""
+    rng = np.random.default_rng(9)
+    for B, dtype in ((70, "bf16"), (100, "fp32"), (130, "bf16")):
+        lens = np.where(rng.random(B) < 0.08, rng.integers(3000, 4500, B), rng.integers(0, 60, B))
+        lens[-1] = 6500
+        b = Batch8(rng.integers(0, 4, B), lens, 1, 64, 16, 16, dtype, B, Hq=4)
+        b.len[5] = -1
+        check(b)
 
 
 def test_many_requests():
@@ -150,7 +165,7 @@ def test_strided_queries_and_scales():
     wide[:, :4] = b.q
     check(b, q=wide.to(DEV)[:, :4])
     prompt = Batch8([130, 70], [50, 20], 2, 64, 16, 16, "bf16", 9, Hq=4)
-    many = Batch8([130, 70], [50, 20], 16, 64, 16, 16, "bf16", 9, Hq=128)
+    many = Batch8([130, 70], [50, 20], 24, 64, 16, 16, "bf16", 9, Hq=192)
     for scale in (0.0, 1.0, -0.5):
         check(b, scale=scale)
         check(prompt, 60, 3, scale=scale)
@@ -288,7 +303,7 @@ def test_offsets_that_are_not_valid(bad, dtype, Hq, page):
 
 @pytest.mark.parametrize("at,bad", [(1, -5), (1, 10 ** 6), (2, -5), (2, 2 ** 31 - 1), (3, -1), (0, -5)])
 def test_prompts_beside_an_offset(at, bad):
-    b = Batch8([27, 31, 33], [20, 57, 84], 48, 64, 16, 16, "bf16", at, Hq=192)
+    b = Batch8([27, 31, 33], [20, 57, 84], 24, 64, 16, 16, "bf16", at, Hq=384)
     b.cu[at] = bad
     check_offsets(b)
     ks = [(5 * i) % 40 + 8 for i in range(150)]
@@ -300,7 +315,7 @@ def test_prompts_beside_an_offset(at, bad):
 @pytest.mark.parametrize("ks,lens,dtype", [([3, 0, 7], [20, 90, 5], "bf16"), ([3, 0, 7], [20, 90, 5], "fp32"),
                                            ([3, 0, 7], [20, 1900, 5], "bf16"), ([200, 130, 70], [20, 90, 5], "bf16")])
 def test_rows_behind_the_last_request_stay(ks, lens, dtype):
-    b = Batch8(ks, lens, 8, 64, 16, 16, dtype, 40, Hq=64)
+    b = Batch8(ks, lens, 16, 64, 16, 16, dtype, 40, Hq=128)
     want = b.attend()
     out = torch.full((b.rows + 9,) + b.q.shape[1:], 5.0, dtype=DT[dtype], device=DEV)
     b.attend(torch.cat([b.q, b.q[:9]]).to(DEV), out=out)
@@ -311,7 +326,7 @@ def test_rows_behind_the_last_request_stay(ks, lens, dtype):
 @pytest.mark.parametrize("ks,lens,dtype", [([3, 0, 7], [20, 90, 5], "bf16"), ([3, 0, 7], [20, 90, 5], "fp32"),
                                            ([3, 0, 7], [20, 1900, 5], "bf16"), ([400, 230, 170], [20, 90, 5], "bf16")])
 def test_caches_of_more_than_32_bit_offsets(ks, lens, dtype):
-    b = Batch8(ks, lens, 8, 128, 16, 4, dtype, 41, Hq=32)
+    b = Batch8(ks, lens, 8, 128, 16, 4, dtype, 41, Hq=64)
     want = b.attend()
     first = (2 ** 32 + 2 ** 31) // (8 * 16 * 128)  # pages from 6 GiB on
     big = []
@@ -335,7 +350,7 @@ def test_it_is_the_attention_over_a_bf16_cache_of_the_same_values():
 
 @pytest.mark.parametrize("ks,lens", [([4, 0, 2], [3000, 50, 30]), ([130, 100, 90], [300, 50, 30])])
 def test_graph_replays(ks, lens):
-    b = Batch8(ks, lens, 16, 128, 16, 16, "bf16", 18, Hq=64)
+    b = Batch8(ks, lens, 16, 128, 16, 16, "bf16", 18, Hq=128)
     table, length, cu = b.index_args()
     q = b.q.to(DEV)
     kc, vc, ks8, vs8 = b.caches()
