@@ -187,7 +187,7 @@ def lib(path: str = LIBRARY) -> ctypes.CDLL:
         f = getattr(L, name.replace("append", "append8").replace("attend", "attend8").replace("settle", "settle8"))
         f.restype, f.argtypes = plain.restype, [ctypes.POINTER(SdvCache8)] + plain.argtypes[1:]
     L.sdv_kv_pages_workspace_bytes.restype = ctypes.c_size_t
-    L.sdv_kv_pages_workspace_bytes.argtypes = [ctypes.c_int32]
+    L.sdv_kv_pages_workspace_bytes.argtypes = [ctypes.c_int32, ctypes.c_int32]
     L.sdv_kv_pages.restype = ctypes.c_int
     L.sdv_kv_pages.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
                                ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,

@@ -342,7 +342,7 @@ PyObject* kv_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t page_size = int32_of(a[6]), window = int32_of(a[7]), sinks = int32_of(a[8]);
     const int rc = on(index, [&](void* stream) {
       Workspace ws;
-      ws.take(a[11], a[12], sdv_kv_pages_workspace_bytes((int32_t)B), a[13], index, stream);
+      ws.take(a[11], a[12], sdv_kv_pages_workspace_bytes((int32_t)B, (int32_t)max_pages), a[13], index, stream);
       return sdv_kv_pages(static_cast<int32_t*>(table.data_ptr()), (int32_t)B, (int32_t)max_pages, page_size, p_len, n_d, p_offsets,
                           n_pages, p_ring, p_state, window, sinks, p_placed, p_slots, ws.at, ws.bytes, stream);
     });

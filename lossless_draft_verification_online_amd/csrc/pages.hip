@@ -318,12 +318,13 @@ __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
 
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr int32_t kMostRequests = 1 << 24;
+inline bool is_few(int32_t B, int32_t max_pages) { return B <= kFewWaves && max_pages <= kFewPages; }
 
 }  // namespace pages_impl
 
-extern "C" size_t sdv_kv_pages_workspace_bytes(int32_t B) {
+extern "C" size_t sdv_kv_pages_workspace_bytes(int32_t B, int32_t max_pages) {
   using namespace pages_impl;
-  if (B < 1 || B >= kMostRequests) return 0;
+  if (B < 1 || B >= kMostRequests || max_pages < 1 || is_few(B, max_pages)) return 0;
   return up256((size_t)B * kWaves * 4) + up256((size_t)B * 4) + 256;
 }
 
@@ -346,7 +347,7 @@ extern "C" int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, i
     const void* at;
     int64_t bytes;
   };
-  const size_t need = sdv_kv_pages_workspace_bytes(B);
+  const size_t need = sdv_kv_pages_workspace_bytes(B, max_pages);
   const Span span[] = {{page_table, (int64_t)B * max_pages * 4}, {free_pages, n_pages * 4}, {free_state, 8},
                        {placed, (int64_t)B * 4}, {slots, slots ? (n_draft_rows + B) * 8 : 0},
                        {workspace, workspace ? (int64_t)need : 0},
@@ -355,7 +356,7 @@ extern "C" int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, i
     for (int y = x + 1; y < 8; ++y)
       if (span[x].bytes && span[y].bytes && overlap(span[x].at, span[x].bytes, span[y].at, span[y].bytes))
         return SDV_ERR_INVALID_ARG;
-  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return SDV_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return SDV_ERR_WORKSPACE;
   PagesArgs a;
   a.table = page_table;
   a.len = cache_len;
@@ -375,7 +376,7 @@ extern "C" int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, i
   a.window = window;
   a.sinks = sinks;
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  if (B <= kFewWaves && max_pages <= kFewPages) {
+  if (is_few(B, max_pages)) {
     hipLaunchKernelGGL(place_few, dim3(1), dim3(kFewWaves * kWave), 0, s, a);
     return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
   }

@@ -125,8 +125,8 @@ def test_new_lengths_apart_from_what_is_read(lib, at):  # noqa: F811
                                 dict(placed=None), dict(B=0), dict(n_d=-1), dict(max_pages=0), dict(n_pages=0), dict(page=0),
                                 dict(page=12), dict(page=2048), dict(window=-1), dict(sinks=-1), dict(table=P + 2),
                                 dict(slots=P + 6 * FAR + 4), dict(placed=P + FAR), dict(placed=P + FAR + 8),
-                                dict(state=P + 3 * FAR + 36), dict(slots=P), dict(table=P + 2 * FAR), dict(ws=P, bytes=FAR),
-                                dict(ws=P + 6 * FAR - 16, bytes=FAR)])
+                                dict(state=P + 3 * FAR + 36), dict(slots=P), dict(table=P + 2 * FAR), dict(B=300, ws=P, bytes=FAR),
+                                dict(B=300, ws=P + 6 * FAR - 16, bytes=FAR)])
 def test_pages_invalid(lib, kw):  # noqa: F811
     assert _pages(lib, **kw) == INVALID
 
@@ -137,7 +137,9 @@ def test_pages_limits_and_workspace(lib):  # noqa: F811
     assert _pages(lib, n_d=2 ** 31 - 1024, **big) == LIMIT
     assert _pages(lib, n_pages=2 ** 31, **big) == LIMIT
     assert _pages(lib, max_pages=2 ** 31 - 1, **big) == LIMIT
-    need = lib.sdv_kv_pages_workspace_bytes(3)
-    assert need > 0 and lib.sdv_kv_pages_workspace_bytes(0) == 0 and lib.sdv_kv_pages_workspace_bytes(2 ** 24) == 0
+    need = lib.sdv_kv_pages_workspace_bytes(3, 1000)
+    assert need > 0
+    for bad in ((0, 1000), (2 ** 24, 1000), (100, 0), (3, 4)):  # the last: few requests with short rows need none
+        assert lib.sdv_kv_pages_workspace_bytes(*bad) == 0
     for kw in (dict(), dict(ws=P + 9 * FAR, bytes=need - 1), dict(ws=P + 9 * FAR + 4, bytes=need)):
-        assert _pages(lib, **kw) == WORKSPACE
+        assert _pages(lib, max_pages=1000, **kw) == WORKSPACE

@@ -165,7 +165,7 @@ def test_without_slots():
     p = Pages([3, 2, 9], [30, 7, 60], 4, 14, spare=20)
     table, length, cu, ring, state = p.args()
     placed = torch.empty(3, dtype=torch.int32, device=DEV)
-    ws = torch.empty(_native.lib().sdv_kv_pages_workspace_bytes(3), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(_native.lib().sdv_kv_pages_workspace_bytes(300, 64), dtype=torch.uint8, device=DEV)
     at = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
     rc = _native.lib().sdv_kv_pages(at(table), 3, p.width, 4, at(length), p.n_d, at(cu), len(p.ring), at(ring), at(state), 0, 0,
                                     at(placed), None, at(ws), ws.numel(), torch.cuda.current_stream().cuda_stream)
@@ -221,8 +221,12 @@ def test_refusals():
         with pytest.raises(ValueError):
             call(**kw)
     for kw in (dict(page=0), dict(page=12), dict(page=2048), dict(window=-1), dict(sinks=-1), dict(placed=length),
-               dict(state=ring[:2]), dict(length=state),
-               dict(workspace=torch.empty(16, dtype=torch.uint8, device=DEV))):
+               dict(state=ring[:2]), dict(length=state)):
         with pytest.raises(sdv.SdvError):
             call(**kw)
     call()
+    many = Pages([0] * 40, [9] * 40, 4, 16)
+    table, length, cu, ring, state = many.args()
+    with pytest.raises(sdv.SdvError):
+        call(table=table, length=length, cu=cu, n_d=0, ring=ring, state=state,
+             workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
