@@ -682,13 +682,15 @@ int sdv_kv_settle8(const sdv_cache8* cache, int32_t n_layers, int32_t B, int64_t
  *   placed [B] int32   1 if all of the request's rows have pages now, 0 if not (too few pages, rows beyond the table, or the
  *                      request has ended), -1 for one that is passed over
  *   slots [n_draft_rows + B] int64, or NULL     page * page_size + place of each row of a placed request; -1 for other rows
- * A page is one request's alone.  An entry outside [0, n_pages) is no page, and one taken from the ring is put down as it is, its slots -1.
- * A request with offsets that are not valid, or L_i outside [-1, INT32_MAX - 1024 - K), is passed over and its entries left as
- * they are; with a free_state outside its bounds all requests are.  Pages beyond a full ring are dropped.
+ * A page is one request's alone.  An entry outside [0, n_pages) is no page, and one taken from the ring is put down as it is, its
+ * slots -1.  A request with offsets that are not valid, or L_i outside [-1, INT32_MAX - 1024 - K), is passed over and its entries
+ * left as they are; with a free_state outside its bounds all requests are.  Pages beyond a full ring are dropped.
  * workspace: sdv_kv_pages_workspace_bytes(B, max_pages) bytes, 16-byte aligned, not initialised; it holds nothing between calls (0
- * bytes, and NULL will do, for few requests with short rows of the table, and for B outside [1, 2^24) or max_pages < 1).  Errors: NULL required pointers, B < 1, n_draft_rows < 0, sizes < 1, an unsupported page_size, window < 0, sinks < 0,
- * misaligned pointers (to their type), or an output that overlaps an input or another output -> SDV_ERR_INVALID_ARG; 2^24 requests or
- * more, more than INT32_MAX - 1024 rows or pages of a request, or n_pages above INT32_MAX -> SDV_ERR_LIMIT; a small workspace -> SDV_ERR_WORKSPACE.
+ * bytes, and NULL will do, for few requests with short rows of the table, and for B outside [1, 2^24) or max_pages < 1).
+ * Errors: NULL required pointers, B < 1, n_draft_rows < 0, sizes < 1, an unsupported page_size, window < 0, sinks < 0, misaligned
+ * pointers (to their type), or an output that overlaps an input or another output -> SDV_ERR_INVALID_ARG; 2^24 requests or more,
+ * more than INT32_MAX - 1024 rows or pages of a request, or n_pages above INT32_MAX -> SDV_ERR_LIMIT; a small workspace ->
+ * SDV_ERR_WORKSPACE.
  */
 size_t sdv_kv_pages_workspace_bytes(int32_t B, int32_t max_pages);
 int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, int32_t page_size, const int32_t* cache_len,

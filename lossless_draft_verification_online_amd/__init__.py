@@ -644,9 +644,9 @@ def attend(queries: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Te
            value_scales: torch.Tensor | None = None, parents: torch.Tensor | None = None, scale: float | None = None,
            window: int = 0, sinks: int = 0, out: torch.Tensor | None = None,
            workspace: torch.Tensor | None = None) -> torch.Tensor:
-    """sdv_attend, or with the scales of a cache in 8 bits sdv_attend8: attention of the batch's queries [n_draft_rows + B, n_q_heads, head_dim] over the cache
-    that kv_append wrote (arguments as there), each row over the slots before it (in a tree, the cached
-    slots and its ancestors) within window positions (0: all) or among the first ``sinks`` slots.  scale
+    """sdv_attend, or with the scales of a cache in 8 bits sdv_attend8: attention of the batch's queries [n_draft_rows + B,
+    n_q_heads, head_dim] over the cache that kv_append wrote (arguments as there), each row over the slots before it (in a tree,
+    the cached slots and its ancestors) within window positions (0: all) or among the first ``sinks`` slots.  scale
     defaults to head_dim ** -0.5.  Returns [n_draft_rows + B, n_q_heads, head_dim]."""
     if _scaled(key_scales, value_scales):
         return _native.marshal().attend8(queries, key_cache, value_cache, page_table, cache_len, offsets, key_scales,
@@ -687,8 +687,8 @@ def attend(queries: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Te
 def kv_settle(key_cache: torch.Tensor, value_cache: torch.Tensor, page_table: torch.Tensor, cache_len: torch.Tensor,
               offsets: torch.Tensor, accepted_len: torch.Tensor, accepted_nodes: torch.Tensor, *,
               key_scales: torch.Tensor | None = None, value_scales: torch.Tensor | None = None) -> torch.Tensor:
-    """sdv_kv_settle, or with the scales of caches in 8 bits sdv_kv_settle8: moves the accepted path of verified token trees (accepted_len and accepted_nodes of
-    verify_tree) to the slots where the sequences continue, in one layer's cache or in all of
+    """sdv_kv_settle, or with the scales of caches in 8 bits sdv_kv_settle8: moves the accepted path of verified token trees
+    (accepted_len and accepted_nodes of verify_tree) to the slots where the sequences continue, in one layer's cache or in all of
     [n_layers, n_pages, n_kv_heads, page_size, head_dim].  Returns the new cache lengths, int32 [B]."""
     if _scaled(key_scales, value_scales):
         return _native.marshal().kv_settle8(key_cache, value_cache, page_table, cache_len, offsets, accepted_len,

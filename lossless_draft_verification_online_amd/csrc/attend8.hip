@@ -121,7 +121,8 @@ int launch(const AttendArgs& a, const Plan& p, hipStream_t s) {
     if (p.many)
       hipLaunchKernelGGL((join<E, D, QB, true, true>), dim3(units.x, 16 * QB), dim3(kJoinWaves * kWave), 0, s, a);
     else
-      hipLaunchKernelGGL((join<E, D, QB, false, true>), dim3((unsigned)(a.ranges * a.cache.n_heads), 16 * QB / kJoin), dim3(kJoinWaves * kWave), 0, s, a);
+      hipLaunchKernelGGL((join<E, D, QB, false, true>), dim3((unsigned)(a.ranges * a.cache.n_heads), 16 * QB / kJoin),
+                         dim3(kJoinWaves * kWave), 0, s, a);
   }
   return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
 }
@@ -130,7 +131,8 @@ template <class E, int D>
 int launch_columns(const AttendArgs& a, const Plan& p, hipStream_t s) {
   if constexpr (E::kBytes == 2 && D <= 128) {
     if (p.mode == kRows) {
-      hipLaunchKernelGGL((attend_rows<D, true>), dim3((unsigned)(a.tiles * a.cache.n_heads)), dim3(kRowsWaves * kWave), 0, s, a);
+      hipLaunchKernelGGL((attend_rows<D, true>), dim3((unsigned)(a.tiles * a.cache.n_heads)), dim3(kRowsWaves * kWave), 0, s,
+                         a);
       return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
     }
   }

@@ -14,6 +14,10 @@ namespace attend_impl {
 // exponentials of this one, whose cycles they fill: without, two waves per SIMD wait for each other (954 TF/s at
 // the same shape).
 //
+// 8 bits: a wave turns the codes of its 16 rows into bf16 numbers in their place before the barrier, so that the products read
+// what they read of a bf16 cache.  Those conversions are the difference: 16 x 2501 rows on 4000 tokens 874 to 884 TF/s, under a
+// window of 1024 550.  Among the exponentials, or behind the products, they took longer (registers, and waits for the loads).
+//
 // A row of a tile keeps its 16-byte pieces in the order p ^ 2 (token mod 8) (for D = 64, of 8 pieces, p ^ 2 (token
 // / 2 mod 4)): the 32 rows that a key read takes, and the 8 that a transposing value read takes, then lie in
 // different banks.  A direct load writes its lanes' 16 bytes in lane order, so the permutation is in the addresses

@@ -189,9 +189,9 @@ __device__ __forceinline__ Span span_of(int32_t len, int32_t pos_lo, int32_t pos
 }
 
 // The batch's work is the list of its units (tile of columns, head), request by request, each of its token tiles.
-// The list is cut into equal ranges, one per workgroup (8 bits: one per workgroup and head, so that the heads of a page, which lie next
-// to each other, are read at about one time: 64 requests of K in 0 .. 8 KKK us for 145): lengths differ between requests, and few units leave
-// places empty (one request of 8 heads on 4000 tokens: 17 us by ranges, 42 by units).
+// The list is cut into equal ranges, one per workgroup (8 bits: one per workgroup and head, so that the heads
+// of a page, which lie next to each other, are read at about one time: 64 requests of K in 0 .. 8 137 us for 145): lengths differ
+// between requests, and few units leave places empty (one request of 8 heads on 4000 tokens: 17 us by ranges, 42 by units).
 struct Work {
   int32_t first, k, len;      // the request
   int32_t tiles, n;           // column tiles; token tiles of a unit (those of all its rows)
@@ -381,6 +381,10 @@ __device__ __forceinline__ void add_to(char* out, int d, float v) {
 // at the end.  Bound by the reads of the cache: 64 requests of K in 0..8 on 4096 to 8192 tokens (window 4096, 8 heads of
 // 128, bf16) 232 us, 4.6 TB/s of 1.08 GB (a large copy reaches 4.9), with the second tile of requests of more than 32 columns read again.  Few units
 // are bound by what a compute unit loads (1000 tokens of a head, 512 KB, in about 8 us; 8 waves instead of 4 take as long).
+//
+// 8 bits: a code times its scale is a bf16 number, converted in registers (keys) or on the way to shared memory (values).  The
+// same 64 requests 123 us, 4.4 TB/s of 0.53 GB, and 6.5 for the join; three of 200 000 tokens in all 75 us, 5.4 TB/s.  Binary32
+// rows take three bf16 products for one (16 trees 14.6 us, of a binary32 cache 24.8).
 template <class E, int D, int QB, int kWaves, bool kWholePages, bool k8>
 __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, QB, kWaves, k8>& sh, const TileOf& at,
                                             int32_t len, int32_t head, bool pos_all, int32_t w_lo, int32_t w_hi, int64_t slot) {
@@ -425,8 +429,8 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
     const int32_t s = start(n) + (lane & (kTile - 1)), k = s >> a.cache.page_log2;
     return n < w_hi && (kWholePages || held(s)) && k < a.cache.max_pages ? table[k] : -1;
   };
-  // Everything waits for the first pages: 8 bits ask for them before the queries (16 requests of 4096 tokens and one row
-  // 34.9 us for KKK behind them; caches of the rows' type as they were).
+  // Everything waits for the first pages: 8 bits ask for them before the queries (16 requests of one row on up to 4096 tokens
+  // 35.7 us for 37.1 behind them; caches of the rows' type as they were).
   int32_t entry_0 = -1, entry_1 = -1;
   if constexpr (k8) {
     entry_0 = entry_at(w_lo + wave);

@@ -154,6 +154,17 @@ __device__ __forceinline__ int64_t first_block(const int32_t* cu, int32_t i, int
 constexpr int kTurns = 16;  // tokens whose angles are held at once
 
 // A workgroup takes some of the keys' and values' heads of a block of tokens (a wave each), or one row's queries.
+//
+// A block's scale is the least power of two that its largest magnitude fits under, which one pass over its rows finds; the
+// second, which turns and rounds them, finds them in a cache.  That a wave holds the whole block of a head makes the scale its
+// own: no atomics, no second launch, and codes that were there are brought to a larger scale by the same wave.  The scale is
+// that of the values as given, since a rotation is not needed to know it (316 sqrt(2) < 448).
+//
+// Many rows are bound by memory: 4 prompts of 4096 rows at most, 100 MB, 20.8 us, 4.8 TB/s (a large copy's rate).  Few are bound by
+// the chain of offsets, length, page, and rows: 256 requests of K in 0 .. 8, 27 MB, 14 us (5.7 at a copy's rate); one 5.3.
+// Slower: rows held in registers between the passes (with the rotation's operands they leave fewer waves), several heads to a
+// wave, the tables of angles in binary64 (in the place of the few values that need it computing their own), the list of
+// units in shared memory.
 template <class E, bool kInterleaved>
 __global__ __launch_bounds__(kThreads, 8) void append8(Append8Args a) {
   __shared__ float cos_s[kTurns][128], sin_s[kTurns][128];
@@ -354,7 +365,8 @@ struct Settle8Args {
 
 // One wave per request and (layer, keys or values, head): all accepted tokens' codes are read before any is written, and the
 // scales of the blocks that they come from before those of the blocks that they go to.  Bound by the chain of offsets and lengths,
-// nodes, pages, scales and rows: 64 trees in four layers 5.0 us, one in one layer 3.5 (by workgroups of four waves, of which most had nothing to move, 9.4 and 4.2).
+// nodes, pages, scales and rows: 64 trees in four layers 5.0 us, one in one layer 3.3 (by workgroups of four waves, of which most
+// had nothing to move, 9.4 and 4.2).
 template <int D>
 __global__ __launch_bounds__(kWave) void settle8(Settle8Args a) {
   constexpr int kVecs = D / 16, kRows = kWave / kVecs, kGroups = kMaxNodes / kRows;  // of 16 bytes; rows that the wave moves at once

@@ -1,5 +1,11 @@
 // A round's pages from the requests' lengths: sdv_kv_pages.  Pages that no row sees any more go back to a ring of free
 // ones, and the coming rows' slots get pages from it, in the order of the requests.
+//
+// What request i returns and takes follows from its own length and its row of the table alone; where its pages lie in the ring
+// are sums over the requests before it.  So its row is read twice, once to count and once to place, with the sums between: a
+// workgroup per request and a launch each, where every workgroup adds up the counts before its own.  Nothing is atomic, and
+// the ring's order is that of the requests.  Bound by two chains of length, entries and counts: 512 rows of 4100
+// entries (8.5 MB, 1.8 us at a copy's rate) take 5.3 + 8.0 us, one request's 66 entries 3.7 in one launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

@@ -406,3 +406,11 @@ def test_refusals():
     with pytest.raises(sdv.SdvError):
         long.attend(workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     assert host(ks).shape == (b.n_pages, 2, 2)
+
+
+def test_a_workspace_that_the_gpu_does_not_hold_as_one_piece():
+    b = Batch8([0], [9000], 1, 128, 16, 16, "bf16", 4, Hq=8)
+    for ws in (torch.empty(1 << 24, dtype=torch.uint8), torch.empty(1 << 24, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError):
+            b.attend(workspace=ws)
+    assert torch.equal(b.attend(workspace=torch.empty(1 << 24, dtype=torch.uint8, device=DEV)), b.attend())

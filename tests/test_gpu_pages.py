@@ -230,3 +230,6 @@ def test_refusals():
     with pytest.raises(sdv.SdvError):
         call(table=table, length=length, cu=cu, n_d=0, ring=ring, state=state,
              workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, dtype=torch.uint8, device=DEV)[::2]):
+        with pytest.raises(ValueError):
+            call(table=table, length=length, cu=cu, n_d=0, ring=ring, state=state, workspace=ws)
