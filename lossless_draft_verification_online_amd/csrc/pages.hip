@@ -88,6 +88,7 @@ __device__ __forceinline__ void count_part(const PagesArgs& a, const Keeps& k, c
     }
 #pragma unroll
     for (int y = 0; y < kAhead; ++y) {
+      if (x0 + y * kWave >= hi) break;
       const int32_t at = x0 + y * kWave + lane;
       bool free, want;
       ask(a, k, at, entry[y], free, want);
@@ -113,6 +114,7 @@ __device__ __forceinline__ void place_part(const PagesArgs& a, const Keeps& k, i
     }
 #pragma unroll
     for (int y = 0; y < kAhead; ++y) {
+      if (x0 + y * kWave >= hi) break;
       const int32_t at = x0 + y * kWave + lane;
       bool free, want;
       ask(a, k, at, entry[y], free, want);
