@@ -25,9 +25,10 @@ struct PagesArgs {
   int32_t* state;
   int32_t* placed;
   int64_t* slots;
-  int32_t* freed;   // [B][kWaves] entries that a wave's part of a request's row of the table returns
-  int32_t* wanted;  // [B] pages that a request takes
-  int32_t* before;  // [2] the ring's state before the call
+  int32_t* freed;    // [B][kWaves] entries that a wave's part of a request's row of the table returns
+  int32_t* wanted;   // [B][kWaves] and takes; none if its rows are beyond the table
+  uint64_t* events;  // [B][kWaves] where
+  int32_t* before;   // [2] the ring's state before the call
   int64_t n_d, n_pages;
   int32_t B, max_pages, page_log2, window, sinks;
 };
@@ -60,13 +61,6 @@ __device__ __forceinline__ bool ring_fits(const PagesArgs& a, int32_t first, int
   return first >= 0 && first < a.n_pages && count >= 0 && count <= a.n_pages;
 }
 
-// The part of a request's row of the table that wave w takes.
-__device__ __forceinline__ void part_of(int32_t max_pages, int w, int32_t& lo, int32_t& hi) {
-  const int32_t part = ((max_pages + kWaves * kWave - 1) / (kWaves * kWave)) * kWave;
-  lo = w * part < max_pages ? w * part : max_pages;
-  hi = lo + part < max_pages ? lo + part : max_pages;
-}
-
 __device__ __forceinline__ void ask(const PagesArgs& a, const Keeps& k, int32_t at, int32_t entry, bool& free, bool& want) {
   const bool have = entry >= 0 && entry < a.n_pages, in = at < a.max_pages;
   const bool keep = at < k.near || (at >= k.lo && at < k.hi);
@@ -74,62 +68,88 @@ __device__ __forceinline__ void ask(const PagesArgs& a, const Keeps& k, int32_t 
   want = in && !have && at >= k.rows && at < k.hi;
 }
 
-// Entries of [lo, hi) of a request's row of the table that go back, and that its rows need.  kAhead loads at once.
-constexpr int kAhead = 4;
-__device__ __forceinline__ void count_part(const PagesArgs& a, const Keeps& k, const int32_t* row, int32_t lo, int32_t hi,
-                                           int32_t& frees, int32_t& wants) {
-  const int lane = threadIdx.x & (kWave - 1);
-  for (int32_t x0 = lo; x0 < hi; x0 += kAhead * kWave) {
-    int32_t entry[kAhead];
-#pragma unroll
-    for (int y = 0; y < kAhead; ++y) {
-      const int32_t at = x0 + y * kWave + lane;
-      entry[y] = at < hi ? row[at] : -1;
-    }
-#pragma unroll
-    for (int y = 0; y < kAhead; ++y) {
-      if (x0 + y * kWave >= hi) break;
-      const int32_t at = x0 + y * kWave + lane;
-      bool free, want;
-      ask(a, k, at, entry[y], free, want);
-      frees += __popcll(__ballot(free && at < hi));
-      wants += __popcll(__ballot(want && at < hi));
-    }
+// A part of a row of the table, looked at 64 entries at a time: its chunks, and in 64 bits those where something changes (a bit
+// stands for 1 << shift chunks).
+struct Part {
+  int32_t lo, hi, n, shift;
+  __device__ __forceinline__ Part(int32_t from, int32_t to) : lo(from), hi(to), n((to - from + kWave - 1) / kWave), shift(0) {
+    while (n >> shift > 64) ++shift;
   }
+  // the first chunk from c on that one of `events` stands for, or n
+  __device__ __forceinline__ int32_t next(uint64_t events, int32_t c) const {
+    if (c >= n) return n;
+    const int32_t bit = c >> shift;
+    const uint64_t rest = bit < 64 ? events >> bit : 0;
+    if (!rest) return n;
+    const int32_t skip = __builtin_ctzll(rest);
+    return skip ? (bit + skip) << shift : c;
+  }
+  __device__ __forceinline__ int32_t at(int32_t c) const { return lo + c * kWave + (int32_t)(threadIdx.x & (kWave - 1)); }
+  __device__ __forceinline__ int32_t entry(const int32_t* row, int32_t c) const { return at(c) < hi ? row[at(c)] : -1; }
+};
+
+// The part of a request's row of the table that wave w takes.
+__device__ __forceinline__ Part part_of(int32_t max_pages, int w) {
+  const int32_t part = ((max_pages + kWaves * kWave - 1) / (kWaves * kWave)) * kWave;
+  const int32_t lo = w * part < max_pages ? w * part : max_pages;
+  return Part(lo, lo + part < max_pages ? lo + part : max_pages);
 }
 
-// Returns and takes them: `returned` and `taken` pages went before, in the ring as it was.
-__device__ __forceinline__ void place_part(const PagesArgs& a, const Keeps& k, int32_t* row, int32_t lo, int32_t hi,
+// Entries of a part that go back, and that the request's rows need, and where.  kAhead loads at once (512 requests of 4100 entries
+// 26.7 us, by twos 28.4, by eights 26.3, but one of 66 6.8, 6.7 and 7.3).
+constexpr int kAhead = 4;
+struct Counts {
+  int32_t frees, wants;
+  uint64_t events;
+};
+__device__ __forceinline__ Counts count_part(const PagesArgs& a, const Keeps& k, const int32_t* row, const Part& part) {
+  Counts sum = {0, 0, 0};
+  for (int32_t c0 = 0; c0 < part.n; c0 += kAhead) {
+    int32_t entry[kAhead];
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) entry[y] = part.entry(row, c0 + y);
+#pragma unroll
+    for (int y = 0; y < kAhead; ++y) {
+      if (c0 + y >= part.n) break;
+      const int32_t at = part.at(c0 + y);
+      bool free, want;
+      ask(a, k, at, entry[y], free, want);
+      const uint64_t frees = __ballot(free && at < part.hi), wants = __ballot(want && at < part.hi);
+      sum.frees += __popcll(frees);
+      sum.wants += __popcll(wants);
+      if (frees | wants) sum.events |= (uint64_t)1 << ((c0 + y) >> part.shift);
+    }
+  }
+  return sum;
+}
+
+// Returns and takes them: `returned` and `taken` pages went before, in the ring as it was.  Only chunks with events are looked at
+// again, each asked for before the one in front of it is done.
+__device__ __forceinline__ void place_part(const PagesArgs& a, const Keeps& k, int32_t* row, const Part& part, uint64_t events,
                                            int32_t first, int32_t held, uint64_t returned, uint64_t taken, bool is_placed) {
   const int lane = threadIdx.x & (kWave - 1);
   const uint64_t below = ((uint64_t)1 << lane) - 1;
   // a place of the ring, whose sum with `first` is below 2^33
   auto place_of = [&](uint64_t x) { return x < (uint64_t)a.n_pages ? x : x - (uint64_t)a.n_pages; };
-  for (int32_t x0 = lo; x0 < hi; x0 += kAhead * kWave) {
-    int32_t entry[kAhead];
-#pragma unroll
-    for (int y = 0; y < kAhead; ++y) {
-      const int32_t at = x0 + y * kWave + lane;
-      entry[y] = at < hi ? row[at] : -1;
+  int32_t c = part.next(events, 0), entry = c < part.n ? part.entry(row, c) : -1;
+  while (c < part.n) {
+    const int32_t c_1 = part.next(events, c + 1), entry_1 = c_1 < part.n ? part.entry(row, c_1) : -1;
+    const int32_t at = part.at(c);
+    bool free, want;
+    ask(a, k, at, entry, free, want);
+    free = free && at < part.hi;
+    want = want && at < part.hi && is_placed;
+    const uint64_t frees = __ballot(free), wants = __ballot(want);
+    if (free) {
+      const uint64_t to = (uint64_t)held + returned + __popcll(frees & below);
+      if (to < (uint64_t)a.n_pages) a.ring[place_of(first + to)] = entry;
+      row[at] = -1;
     }
-#pragma unroll
-    for (int y = 0; y < kAhead; ++y) {
-      if (x0 + y * kWave >= hi) break;
-      const int32_t at = x0 + y * kWave + lane;
-      bool free, want;
-      ask(a, k, at, entry[y], free, want);
-      free = free && at < hi;
-      want = want && at < hi && is_placed;
-      const uint64_t frees = __ballot(free), wants = __ballot(want);
-      if (free) {
-        const uint64_t to = (uint64_t)held + returned + __popcll(frees & below);
-        if (to < (uint64_t)a.n_pages) a.ring[place_of(first + to)] = entry[y];
-        row[at] = -1;
-      }
-      if (want) row[at] = a.ring[place_of(first + taken + __popcll(wants & below))];
-      returned += __popcll(frees);
-      taken += __popcll(wants);
-    }
+    if (want) row[at] = a.ring[place_of(first + taken + __popcll(wants & below))];
+    returned += __popcll(frees);
+    taken += __popcll(wants);
+    c = c_1;
+    entry = entry_1;
   }
 }
 
@@ -161,49 +181,49 @@ __global__ __launch_bounds__(kFewWaves* kWave) void place_few(PagesArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int32_t first = a.state[0], held = a.state[1];
   const bool ring = ring_fits(a, first, held);
-  if (t < kWave) freed_s[t] = wanted_s[t] = 0;
   if (a.slots)
     for (int64_t x = t; x < a.n_d + a.B; x += kFewWaves * kWave) a.slots[x] = -1;
-  __syncthreads();
-  for (int32_t i = wave; i < a.B; i += kFewWaves) {
-    const Keeps k = keeps_of(a, request_at(a.cu, i, a.n_d), a.len[i]);
-    int32_t frees = 0, wants = 0;
-    if (k.known && ring) count_part(a, k, a.table + (int64_t)i * a.max_pages, 0, a.max_pages, frees, wants);
-    if (lane == 0) {
-      freed_s[i] = frees;
-      wanted_s[i] = k.fits(a) ? wants : 0;
-    }
+  const int32_t i = wave;
+  Request r = {};
+  int32_t len = -1;
+  Keeps k = {};
+  Counts counts = {0, 0, 0};
+  const Part part(0, a.max_pages);
+  if (i < a.B) {
+    r = request_at(a.cu, i, a.n_d);
+    len = a.len[i];
+    k = keeps_of(a, r, len);
+    if (k.known && ring) counts = count_part(a, k, a.table + (int64_t)i * a.max_pages, part);
+    if (!k.fits(a)) counts.wants = 0;
   }
+  if (lane == 0) {
+    freed_s[wave] = counts.frees;
+    wanted_s[wave] = counts.wants;
+  }
+  if (t >= kFewWaves && t < kWave) freed_s[t] = wanted_s[t] = 0;
   __syncthreads();
   const uint64_t frees = freed_s[lane], wants = wanted_s[lane];
   const uint64_t returned = wave_inclusive_scan(frees), taken = wave_inclusive_scan(wants);
-  const bool has_room = taken <= (uint64_t)held;
   if (wave == 0 && ring) {
-    const uint64_t served = __ballot(has_room);  // the sums ascend: a run of leading lanes
+    const uint64_t served = __ballot(taken <= (uint64_t)held);  // the sums ascend: a run of leading lanes
     const uint64_t most = served ? lane_value(taken, 63 - __builtin_clzll(served)) : 0;
     const uint64_t all = lane_value(returned, kWave - 1);
     if (lane == 0) write_state(a, first, held, all, most);
   }
-  for (int32_t i = wave; i < a.B; i += kFewWaves) {
-    const Request r = request_at(a.cu, i, a.n_d);
-    const int32_t len = a.len[i];
-    const Keeps k = keeps_of(a, r, len);
-    const uint64_t mine = lane_value(wants, i);
-    const bool is_placed = ring && k.fits(a) && (mine == 0 || lane_value(taken, i) <= (uint64_t)held);
-    if (lane == 0) a.placed[i] = !ring || !k.known ? -1 : (is_placed ? 1 : 0);
-    if (!ring || !k.known) continue;
-    int32_t* const row = a.table + (int64_t)i * a.max_pages;
-    place_part(a, k, row, 0, a.max_pages, first, held, lane_value(returned, i) - lane_value(frees, i),
-               lane_value(taken, i) - mine, is_placed);
-    if (!is_placed || !a.slots) continue;
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the wave's entries
-    write_slots(a, r, row, len, lane, kWave);
-  }
+  if (i >= a.B) return;
+  const bool is_placed = ring && k.fits(a) && (counts.wants == 0 || lane_value(taken, i) <= (uint64_t)held);
+  if (lane == 0) a.placed[i] = !ring || !k.known ? -1 : (is_placed ? 1 : 0);
+  if (!ring || !k.known) return;
+  int32_t* const row = a.table + (int64_t)i * a.max_pages;
+  place_part(a, k, row, part, counts.events, first, held, lane_value(returned, i) - counts.frees,
+             lane_value(taken, i) - counts.wants, is_placed);
+  if (!is_placed || !a.slots) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");  // the wave's entries
+  write_slots(a, r, row, len, lane, kWave);
 }
 
 // What each request returns and takes; slots are -1 until they are known.
 __global__ __launch_bounds__(kThreads) void count(PagesArgs a) {
-  __shared__ int32_t wanted_s[kWaves];
   const int t = threadIdx.x, lane = t & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int32_t i = blockIdx.x;
@@ -216,18 +236,12 @@ __global__ __launch_bounds__(kThreads) void count(PagesArgs a) {
   }
   const Keeps k = keeps_of(a, request_at(a.cu, i, a.n_d), a.len[i]);
   const bool works = k.known && ring_fits(a, first, held);
-  int32_t frees = 0, wants = 0, lo, hi;
-  part_of(a.max_pages, wave, lo, hi);
-  if (works) count_part(a, k, a.table + (int64_t)i * a.max_pages, lo, hi, frees, wants);
+  Counts counts = {0, 0, 0};
+  if (works) counts = count_part(a, k, a.table + (int64_t)i * a.max_pages, part_of(a.max_pages, wave));
   if (lane == 0) {
-    a.freed[(int64_t)i * kWaves + wave] = frees;
-    wanted_s[wave] = wants;
-  }
-  __syncthreads();
-  if (t == 0) {
-    int32_t n = 0;
-    for (int w = 0; w < kWaves; ++w) n += wanted_s[w];
-    a.wanted[i] = works && k.fits(a) ? n : 0;
+    a.freed[(int64_t)i * kWaves + wave] = counts.frees;
+    a.wanted[(int64_t)i * kWaves + wave] = k.fits(a) ? counts.wants : 0;
+    a.events[(int64_t)i * kWaves + wave] = counts.events;
   }
 }
 
@@ -260,18 +274,19 @@ __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
   const int32_t len = a.len[i];
   const Keeps k = keeps_of(a, r, len);
   const bool ring = ring_fits(a, first, held);
-  auto freed_of = [&](int32_t x) {
-    const int4 n = reinterpret_cast<const int4*>(a.freed)[x];
+  auto sum_of = [&](const int32_t* of_waves, int32_t x) {
+    const int4 n = reinterpret_cast<const int4*>(of_waves)[x];
     return (uint64_t)(uint32_t)n.x + (uint32_t)n.y + (uint32_t)n.z + (uint32_t)n.w;
   };
+  const uint64_t events = a.events[(int64_t)i * kWaves + wave];
   // pages returned and taken before this request
   uint64_t returned = 0, taken = 0;
   for (int32_t x = t; x < i; x += kThreads) {
-    returned += freed_of(x);
-    taken += (uint32_t)a.wanted[x];
+    returned += sum_of(a.freed, x);
+    taken += sum_of(a.wanted, x);
   }
   group_sums(returned, taken, sum_s);
-  const int32_t wants = a.wanted[i];
+  const uint64_t wants = sum_of(a.wanted, i);
   const bool is_placed = ring && k.fits(a) && (wants == 0 || taken + wants <= (uint64_t)held);
   if (t == 0) a.placed[i] = !ring || !k.known ? -1 : (is_placed ? 1 : 0);
 
@@ -279,8 +294,8 @@ __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
     uint64_t all = 0, sum = 0, most = 0;
     for (int32_t x0 = 0; x0 < a.B; x0 += kThreads) {
       const int32_t x = x0 + t;
-      const uint64_t mine = x < a.B ? (uint32_t)a.wanted[x] : 0;
-      uint64_t back = x < a.B ? freed_of(x) : 0;
+      const uint64_t mine = x < a.B ? sum_of(a.wanted, x) : 0;
+      uint64_t back = x < a.B ? sum_of(a.freed, x) : 0;
       const uint64_t inc = wave_inclusive_scan(mine);
       uint64_t whole = mine;
       group_sums(back, whole, sum_s);
@@ -305,20 +320,12 @@ __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
   }
 
   if (!ring || !k.known) return;
-  int32_t lo, hi;
-  part_of(a.max_pages, wave, lo, hi);
-  for (int w = 0; w < wave; ++w) returned += (uint32_t)a.freed[(int64_t)i * kWaves + w];
-  int32_t* const row = a.table + (int64_t)i * a.max_pages;
-  // what the parts before this wave's take: counted from the table as it was (entries are written behind the barrier)
-  if (is_placed) {
-    int32_t none = 0, mine = 0;
-    count_part(a, k, row, k.rows > lo ? k.rows : lo, k.hi < hi ? k.hi : hi, none, mine);
-    __syncthreads();
-    if (lane == 0) sum_s[wave][0] = (uint32_t)mine;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) taken += sum_s[w][0];
+  for (int w = 0; w < wave; ++w) {
+    returned += (uint32_t)a.freed[(int64_t)i * kWaves + w];
+    taken += (uint32_t)a.wanted[(int64_t)i * kWaves + w];
   }
-  place_part(a, k, row, lo, hi, first, held, returned, taken, is_placed);
+  int32_t* const row = a.table + (int64_t)i * a.max_pages;
+  place_part(a, k, row, part_of(a.max_pages, wave), events, first, held, returned, taken, is_placed);
   if (!is_placed || !a.slots) return;
   __syncthreads();
   write_slots(a, r, row, len, t, kThreads);
@@ -333,7 +340,7 @@ inline bool is_few(int32_t B, int32_t max_pages) { return B <= kFewWaves && max_
 extern "C" size_t sdv_kv_pages_workspace_bytes(int32_t B, int32_t max_pages) {
   using namespace pages_impl;
   if (B < 1 || B >= kMostRequests || max_pages < 1 || is_few(B, max_pages)) return 0;
-  return up256((size_t)B * kWaves * 4) + up256((size_t)B * 4) + 256;
+  return 2 * up256((size_t)B * kWaves * 4) + up256((size_t)B * kWaves * 8) + 256;
 }
 
 extern "C" int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, int32_t page_size,
@@ -373,9 +380,12 @@ extern "C" int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, i
   a.state = free_state;
   a.placed = placed;
   a.slots = slots;
-  a.freed = static_cast<int32_t*>(workspace);
-  a.wanted = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + up256((size_t)B * kWaves * 4));
-  a.before = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + up256((size_t)B * kWaves * 4) + up256((size_t)B * 4));
+  char* const work = static_cast<char*>(workspace);
+  const size_t counts = up256((size_t)B * kWaves * 4);
+  a.freed = reinterpret_cast<int32_t*>(work);
+  a.wanted = reinterpret_cast<int32_t*>(work + counts);
+  a.events = reinterpret_cast<uint64_t*>(work + 2 * counts);
+  a.before = reinterpret_cast<int32_t*>(work + 2 * counts + up256((size_t)B * kWaves * 8));
   a.n_d = n_draft_rows;
   a.n_pages = n_pages;
   a.B = B;

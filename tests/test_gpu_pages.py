@@ -233,3 +233,18 @@ def test_refusals():
     for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1 << 20, dtype=torch.uint8, device=DEV)[::2]):
         with pytest.raises(ValueError):
             call(table=table, length=length, cu=cu, n_d=0, ring=ring, state=state, workspace=ws)
+
+
+@pytest.mark.parametrize("width", [640, 4100, 16385, 50003])
+@pytest.mark.parametrize("kept", [1.0, 0.02, 0.0004])
+def test_entries_that_change_here_and_there(width, kept):
+    """Rows of the table of which few entries, or runs of them, are returned and taken, at every distance from each other."""
+    rng = np.random.default_rng(width)
+    lens = [(width - 20) * 4, (width - 20) * 2, 64, (width - 20) * 3 + 1]
+    p = Pages([30, 17, 200, 3], lens, 4, 12, width=width, spare=300, window=97, sinks=9)
+    p.table[rng.random(p.table.shape) > kept] = -1
+    got = p.check()
+    assert got[3].tolist() == [1, 1, 1, 1]
+    p.len[:] = [lens[0] // 3, lens[1] + 5, -1, lens[3] + 2]
+    p.table[0, rng.integers(width, size=7)] = got[1][:7]
+    assert p.check()[3].tolist() == [1, 1, 0, 1]
