@@ -2,10 +2,11 @@
 // ones, and the coming rows' slots get pages from it, in the order of the requests.
 //
 // What request i returns and takes follows from its own length and its row of the table alone; where its pages lie in the ring
-// are sums over the requests before it.  So its row is read twice, once to count and once to place, with the sums between: a
-// workgroup per request and a launch each, where every workgroup adds up the counts before its own.  Nothing is atomic, and
-// the ring's order is that of the requests.  Bound by two chains of length, entries and counts: 512 rows of 4100
-// entries (8.5 MB, 1.8 us at a copy's rate) take 5.3 + 8.0 us, one request's 66 entries 3.7 in one launch.
+// are sums over the requests before it.  So its row is read to count, and again where something changes to place it, with the sums
+// between: a workgroup per request and a launch each, where every workgroup adds up the counts before its own.  Nothing is
+// atomic, and the ring's order is that of the requests.  Bound by two chains of length, entries and counts: 512 rows of 4100
+// entries (8.5 MB, 1.8 us at a copy's rate) take 6.0 + 5.0 us (5.3 + 8.0 with the whole row read again), one request's 66 entries 2.3
+// in one launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -172,9 +173,9 @@ __device__ __forceinline__ void write_state(const PagesArgs& a, int32_t first, i
 }
 
 // Few requests with short rows of the table: one workgroup, a wave per request.  Two calls after one another, by this and by the two
-// launches: one request of 66 entries 7.4 us and 12.6, 4 of 515 10.1 and 14.0, 16 of 260 10.7 and 14.2, but 16 of 1028 20.7 and
-// 14.8, one of 4100 26.8 and 17.6, and 64 of 67 (four to a wave) 29 and 14.2.
-constexpr int kFewWaves = 16, kFewPages = 640;
+// launches: one request of 66 entries 5.1 us and 11.2, of 1030 7.7 and 11.8; 16 of 260 8.8 and 12.8, of 515 10.7 and 13.1, of 1028
+// 14.6 and 13.7.
+constexpr int kFewWaves = 16, kFewPages = 896;
 __global__ __launch_bounds__(kFewWaves* kWave) void place_few(PagesArgs a) {
   __shared__ int32_t freed_s[kWave], wanted_s[kWave];
   const int t = threadIdx.x, lane = t & (kWave - 1);
