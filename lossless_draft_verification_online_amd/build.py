@@ -45,7 +45,9 @@ def build_library(out: str = LIBRARY, verbose: bool = False) -> str:
         with ThreadPoolExecutor(max_workers=8) as pool:
             said = list(pool.map(lambda job: _compile([hipcc, *HIPCC_FLAGS, f"-I{os.path.join(ROOT, 'include')}", "-c",
                                                        job[0], "-o", job[1]], job[0]), zip(SOURCES, objects)))
-        said.append(_compile([hipcc, "--offload-arch=gfx950", "-fPIC", "-shared", *objects, "-o", tmp], out))
+        # a name without a directory, by which what is linked with the library finds it
+        said.append(_compile([hipcc, "--offload-arch=gfx950", "-fPIC", "-shared", f"-Wl,-soname,{os.path.basename(LIBRARY)}",
+                              *objects, "-o", tmp], out))
     if verbose and any(said):
         print("".join(said))
     os.replace(tmp, out)
@@ -53,7 +55,7 @@ def build_library(out: str = LIBRARY, verbose: bool = False) -> str:
 
 
 def build_marshal(out: str = MARSHAL) -> str:
-    """_marshal.so, beside libsdv.so, which it is linked with."""
+    """_marshal.so, beside libsdv.so, which it is linked with and which it loads from its own directory."""
     import sysconfig
 
     import torch
@@ -66,7 +68,7 @@ def build_marshal(out: str = MARSHAL) -> str:
               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
               *[x for i in includes for x in ("-isystem", i)], MARSHAL_SOURCE, "-o", tmp,
               f"-L{os.path.join(where, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip",
-              LIBRARY, "-Wl,-rpath,$ORIGIN"], MARSHAL_SOURCE)
+              f"-L{PKG}", f"-l:{os.path.basename(LIBRARY)}", "-Wl,-rpath,$ORIGIN"], MARSHAL_SOURCE)
     os.replace(tmp, out)
     return out
 
