@@ -4,7 +4,7 @@ from __future__ import annotations
 import ctypes
 import os
 
-from .build import LIBRARY
+from .build import LIBRARY, MARSHAL
 
 SDV_BF16, SDV_FP32 = 0, 1
 SDV_MAX_DEPTH = 64
@@ -112,10 +112,12 @@ def marshal():
     global _MARSHAL
     if _MARSHAL is None:
         lib()
+        if not os.path.exists(MARSHAL):
+            raise RuntimeError(f"{MARSHAL} is not built; run __graft_entry__.build()")
         try:
             from . import _marshal
         except ImportError as e:
-            raise RuntimeError("_marshal.so is not built; run __graft_entry__.build()") from e
+            raise RuntimeError(f"{MARSHAL} cannot be loaded: {e}") from e
         _marshal.bind(SdvError)
         _MARSHAL = _marshal
     return _MARSHAL

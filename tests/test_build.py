@@ -39,3 +39,15 @@ def test_a_copy_uses_its_own_library(copy):
                     "print(*sorted({line.split()[-1] for line in open('/proc/self/maps') if 'libsdv' in line}))")
     assert got.returncode == 0, got.stderr
     assert got.stdout.split() == [str(copy.resolve() / NAME / "libsdv.so")]
+
+
+def test_a_module_that_does_not_load_says_why(copy):
+    at = copy / NAME / "_marshal.so"
+    at.write_bytes(bytes(4096))
+    got = run(copy, f"from {NAME} import _native\n_native.marshal()")
+    assert got.returncode != 0 and "RuntimeError" in got.stderr
+    last = got.stderr.strip().splitlines()[-1]
+    assert "is not built" not in last and f"{at.resolve()}: invalid ELF header" in last, last
+    at.unlink()
+    got = run(copy, f"from {NAME} import _native\n_native.marshal()")
+    assert "_marshal.so is not built; run __graft_entry__.build()" in got.stderr.strip().splitlines()[-1]
