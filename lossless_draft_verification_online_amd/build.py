@@ -22,6 +22,7 @@ LIBRARY = os.path.join(PKG, "libsdv.so")
 # The Python module that marshals the newer calls' tensors: host code, on torch's C++ interface.
 MARSHAL_SOURCE = os.path.join(PKG, "csrc", "marshal.cpp")
 MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL_DEPENDS = [MARSHAL_SOURCE, os.path.join(ROOT, "include", "sdv.h")]  # the header's structs are compiled into it
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
@@ -73,11 +74,18 @@ def build_marshal(out: str = MARSHAL) -> str:
     return out
 
 
-def is_stale(path: str = LIBRARY) -> bool:
+def is_stale(path: str | None = None) -> bool:
+    """Whether a library at `path`, or with none given the library or the module, is missing or older than its sources."""
+    if path is None:
+        return is_stale(LIBRARY) or _older(MARSHAL, MARSHAL_DEPENDS)
+    return _older(path, DEPENDS)
+
+
+def _older(path: str, sources: list) -> bool:
     if not os.path.exists(path):
         return True
     t = os.path.getmtime(path)
-    return any(os.path.getmtime(d) > t for d in DEPENDS)
+    return any(os.path.getmtime(d) > t for d in sources)
 
 
 if __name__ == "__main__":

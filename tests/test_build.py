@@ -13,7 +13,7 @@ NAME = os.path.basename(build.PKG)
 
 @pytest.fixture(scope="module", autouse=True)
 def _built():
-    if build.is_stale() or not os.path.exists(build.MARSHAL):
+    if build.is_stale():
         pytest.fail("libsdv.so or _marshal.so is missing or older than its sources; run __graft_entry__.build()")
 
 
@@ -51,3 +51,21 @@ def test_a_module_that_does_not_load_says_why(copy):
     at.unlink()
     got = run(copy, f"from {NAME} import _native\n_native.marshal()")
     assert "_marshal.so is not built; run __graft_entry__.build()" in got.stderr.strip().splitlines()[-1]
+
+
+def test_a_module_older_than_its_sources_is_stale(tmp_path, monkeypatch):
+    module = tmp_path / "_marshal.so"
+    monkeypatch.setattr(build, "MARSHAL", str(module))
+    assert build.is_stale()  # none there
+    module.write_bytes(b"")
+    for source in (build.MARSHAL_SOURCE, os.path.join(build.ROOT, "include", "sdv.h")):
+        t = os.path.getmtime(source)
+        os.utime(module, (t - 1, t - 1))
+        assert build.is_stale(), source
+    os.utime(module, (2 ** 31, 2 ** 31))
+    assert not build.is_stale()
+
+
+def test_the_library_alone_can_be_asked_for(monkeypatch):
+    monkeypatch.setattr(build, "MARSHAL", "/nowhere/_marshal.so")
+    assert not build.is_stale(build.LIBRARY)
