@@ -172,6 +172,8 @@ __device__ __forceinline__ int64_t unit_of_block(int64_t block, int64_t n) {
 // The token tiles that rows j_lo .. j_hi of a request see: [0, near_end) and [lo, hi).
 struct Span {
   int32_t lo, hi, near_end, t_lo, n_near, n;
+  __device__ __forceinline__ int32_t start(int32_t n) const { return (n < n_near ? n : n - n_near + t_lo) * kTile; }
+  __device__ __forceinline__ bool held(int32_t s) const { return (s >= lo && s < hi) || s < near_end; }
 };
 __device__ __forceinline__ Span span_of(int32_t len, int32_t pos_lo, int32_t pos_hi, int32_t window, int32_t sinks) {
   Span s;
@@ -186,6 +188,14 @@ __device__ __forceinline__ Span span_of(int32_t len, int32_t pos_lo, int32_t pos
   }
   s.n = s.n_near + (s.hi + kTile - 1) / kTile - s.t_lo;
   return s;
+}
+
+// The entry of the table for token lane & 31 of tile n, below `end`.
+template <bool kWholePages>
+__device__ __forceinline__ int32_t table_entry(const AttendArgs& a, int32_t i, const Span& own, const Span& span, int32_t n,
+                                               int32_t end) {
+  const int32_t s = span.start(n) + (int32_t)(threadIdx.x & (kTile - 1)), k = s >> a.cache.page_log2;
+  return n < end && (kWholePages || own.held(s)) && k < a.cache.max_pages ? a.cache.table[(int64_t)i * a.cache.max_pages + k] : -1;
 }
 
 // The batch's work is the list of its units (tile of columns, head), request by request, each of its token tiles.
@@ -410,31 +420,16 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   const int32_t c_last = at.c0 + S::kColumns < columns ? at.c0 + S::kColumns - 1 : columns - 1;
   const int32_t j_lo = (uint32_t)at.c0 / (uint32_t)a.G, j_hi = (uint32_t)c_last / (uint32_t)a.G;  // rows of this tile
   bool ok = len_fits(len, K);
-  // the tiles are those of the rows, or of all the request's rows; what this tile's rows see of them is the same
-  const int32_t tail_lo = a.parents ? 0 : j_lo, tail_hi = a.parents ? K : j_hi;
-  const Span own = span_of(len, tail_lo, tail_hi, a.window, a.sinks);
-  const Span span = pos_all ? span_of(len, 0, K, a.window, a.sinks) : own;
-  const int32_t lo = own.lo, hi = own.hi, near_end = own.near_end, n_near = span.n_near, t_lo = span.t_lo;
-  if (!pos_all) {
-    w_lo = 0;
-    w_hi = span.n;
-  }
-  if (!ok) w_hi = w_lo;
-  auto start = [&](int32_t n) { return (n < n_near ? n : n - n_near + t_lo) * kTile; };
-  auto held = [&](int32_t s) { return (s >= lo && s < hi) || s < near_end; };
-  // The table's entry of token lane & 31 as it is, checked when it is used: a check would wait for it, and for
-  // the keys and values asked for before it.
-  const int32_t* const table = a.cache.table + (int64_t)i * a.cache.max_pages;
-  auto entry_at = [&](int32_t n) -> int32_t {
-    const int32_t s = start(n) + (lane & (kTile - 1)), k = s >> a.cache.page_log2;
-    return n < w_hi && (kWholePages || held(s)) && k < a.cache.max_pages ? table[k] : -1;
-  };
   // Everything waits for the first pages: 8 bits ask for them before the queries (16 requests of one row on up to 4096 tokens
   // 35.7 us for 37.1 behind them; caches of the rows' type as they were).
-  int32_t entry_0 = -1, entry_1 = -1;
+  [[maybe_unused]] int32_t first_0 = -1, first_1 = -1;
   if constexpr (k8) {
-    entry_0 = entry_at(w_lo + wave);
-    entry_1 = entry_at(w_lo + wave + kWaves);
+    const int32_t tail_lo = a.parents ? 0 : j_lo, tail_hi = a.parents ? K : j_hi;
+    const Span own = span_of(len, tail_lo, tail_hi, a.window, a.sinks);
+    const Span span = pos_all ? span_of(len, 0, K, a.window, a.sinks) : own;
+    const int32_t first = (pos_all ? w_lo : 0) + wave, end = !ok ? 0 : (pos_all ? w_hi : span.n);
+    first_0 = table_entry<kWholePages>(a, i, own, span, first, end);
+    first_1 = table_entry<kWholePages>(a, i, own, span, first + kWaves, end);
     __builtin_amdgcn_sched_barrier(0);
   }
   if (a.parents && ok) {
@@ -506,8 +501,21 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
     }
   }
 
+  // The tiles are those of the rows, or of all the request's rows; what this tile's rows see of them is the same.  (Found here and
+  // not before the queries, and written out: units of 256 values keep 28 registers in memory, and 32 otherwise, of the
+  // first keys among them, which wait for their load: 512 requests of one row on 4000 tokens 1492 us for 1807.)
+  const int32_t tail_lo = a.parents ? 0 : j_lo, tail_hi = a.parents ? K : j_hi;
+  const Span own = span_of(len, tail_lo, tail_hi, a.window, a.sinks);
+  const Span span = pos_all ? span_of(len, 0, K, a.window, a.sinks) : own;
+  const int32_t lo = own.lo, hi = own.hi, near_end = own.near_end, n_near = span.n_near, t_lo = span.t_lo;
+  if (!pos_all) {
+    w_lo = 0;
+    w_hi = span.n;
+  }
   if (!ok) w_hi = w_lo;
   const int32_t far = len + tail_hi;  // the largest position
+  auto start = [&](int32_t n) { return (n < n_near ? n : n - n_near + t_lo) * kTile; };
+  auto held = [&](int32_t s) { return (s >= lo && s < hi) || s < near_end; };
 
   f32x4 acc[QB][kDB];
   float m[QB], l[QB];
@@ -534,6 +542,13 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   uint32_t byte_1 = 0;  // the next tile's scale of token lane & 31: of its keys, in the upper half of its values
   float scale = 0.0f;
   float vf[kBf16 ? 1 : 8][kDB];
+  // The table's entry of token lane & 31 as it is, checked when it is used: a check would wait for it, and for
+  // the keys and values asked for before it.
+  const int32_t* const table = a.cache.table + (int64_t)i * a.cache.max_pages;
+  auto entry_at = [&](int32_t n) -> int32_t {
+    const int32_t s = start(n) + (lane & (kTile - 1)), k = s >> a.cache.page_log2;
+    return n < w_hi && (kWholePages || held(s)) && k < a.cache.max_pages ? table[k] : -1;
+  };
   auto page_of = [&](int32_t entry) { return entry >= 0 && entry < a.cache.n_pages ? entry : -1; };
   // the lane's byte offsets within 16 tokens' rows
   const uint32_t k_off = col * kLine + 16 * g;
@@ -598,11 +613,7 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
 
   int32_t n = w_lo + wave;
   // the pages of two tiles ahead: a page read behind a tile's loads would wait for them
-  if constexpr (!k8) {
-    entry_0 = entry_at(n);
-    entry_1 = entry_at(n + kWaves);
-  }
-  int32_t page = page_of(entry_0);
+  int32_t page = page_of(k8 ? first_0 : entry_at(n)), entry_1 = k8 ? first_1 : entry_at(n + kWaves);
   if (n < w_hi) {
     if constexpr (k8) load_scales(n, page);
     load_keys(n, page);
