@@ -3,10 +3,10 @@
 //
 // What request i returns and takes follows from its own length and its row of the table alone; where its pages lie in the ring
 // are sums over the requests before it.  So its row is read to count, and again where something changes to place it, with the sums
-// between: a workgroup per request and a launch each, where every workgroup adds up the counts before its own.  Nothing is
-// atomic, and the ring's order is that of the requests.  Bound by two chains of length, entries and counts: 512 rows of 4100
-// entries (8.5 MB, 1.8 us at a copy's rate) take 6.0 + 5.0 us (5.3 + 8.0 with the whole row read again), one request's 66 entries 2.3
-// in one launch.
+// between: a workgroup per request and a launch each, where every workgroup adds up the counts before its own (of many requests a
+// launch between the two does).  Nothing is atomic, and the ring's order is that of the requests.  Bound by two chains of length,
+// entries and counts: 512 rows of 4100 entries (8.5 MB, 1.8 us at a copy's rate) take 6.0 + 5.0 us (5.3 + 8.0 with the whole row
+// read again), one request's 66 entries 2.3 in one launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -30,6 +30,7 @@ struct PagesArgs {
   int32_t* wanted;   // [B][kWaves] and takes; none if its rows are beyond the table
   uint64_t* events;  // [B][kWaves] where
   int32_t* before;   // [2] the ring's state before the call
+  uint64_t* sums;    // [B][2] pages returned and taken before each request: of many requests only
   int64_t n_d, n_pages;
   int32_t B, max_pages, page_log2, window, sinks;
 };
@@ -264,7 +265,65 @@ __device__ __forceinline__ void group_sums(uint64_t& x, uint64_t& y, uint64_t (*
   }
 }
 
+// A request's counts, of its row's parts.
+__device__ __forceinline__ uint64_t sum_of(const int32_t* of_waves, int32_t x) {
+  static_assert(kWaves == 4, "one load");
+  const int4 n = reinterpret_cast<const int4*>(of_waves)[x];
+  return (uint64_t)(uint32_t)n.x + (uint32_t)n.y + (uint32_t)n.z + (uint32_t)n.w;
+}
+
+// Many requests: the sums before each, and the ring's state behind the call, by one workgroup, since adding them up in every
+// workgroup of `place` reads the square of the requests.
+constexpr int kSumWaves = 16, kSumThreads = kSumWaves * kWave;
+__global__ __launch_bounds__(kSumThreads) void sum_up(PagesArgs a) {
+  __shared__ uint64_t of_wave[2][kSumWaves][2];
+  const int t = threadIdx.x, lane = t & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
+  const int32_t first = a.before[0], held = a.before[1];
+  uint64_t returned = 0, taken = 0, most = 0;  // before this round's requests; the largest sum that the ring held
+  uint64_t back = t < a.B ? sum_of(a.freed, t) : 0, want = t < a.B ? sum_of(a.wanted, t) : 0;
+  for (int32_t x0 = 0, turn = 0; x0 < a.B; x0 += kSumThreads, turn ^= 1) {
+    const int32_t x = x0 + t, x_1 = x + kSumThreads;
+    const uint64_t back_1 = x_1 < a.B ? sum_of(a.freed, x_1) : 0, want_1 = x_1 < a.B ? sum_of(a.wanted, x_1) : 0;
+    const uint64_t back_to = wave_inclusive_scan(back), want_to = wave_inclusive_scan(want);
+    if (lane == kWave - 1) {
+      of_wave[turn][wave][0] = back_to;
+      of_wave[turn][wave][1] = want_to;
+    }
+    __syncthreads();  // (the next round writes the other half)
+    uint64_t back_before = returned, want_before = taken;
+#pragma unroll
+    for (int w = 0; w < kSumWaves; ++w) {
+      const uint64_t b = of_wave[turn][w][0], n = of_wave[turn][w][1];
+      back_before += w < wave ? b : 0;
+      want_before += w < wave ? n : 0;
+      returned += b;
+      taken += n;
+    }
+    if (x < a.B) {
+      a.sums[2 * (int64_t)x] = back_before + back_to - back;
+      a.sums[2 * (int64_t)x + 1] = want_before + want_to - want;
+    }
+    const uint64_t here = want_before + want_to;
+    if (here <= (uint64_t)(uint32_t)held && here > most) most = here;
+    back = back_1;
+    want = want_1;
+  }
+#pragma unroll
+  for (int step = 1; step < kWave; step *= 2) {
+    const uint64_t o = __shfl_xor((unsigned long long)most, step);
+    most = o > most ? o : most;
+  }
+  __syncthreads();
+  if (lane == 0) of_wave[0][wave][0] = most;
+  __syncthreads();
+  if (t != 0 || !ring_fits(a, first, held)) return;
+  for (int w = 1; w < kSumWaves; ++w) most = of_wave[0][w][0] > most ? of_wave[0][w][0] : most;
+  write_state(a, first, held, returned, most);
+}
+
 // A workgroup per request returns its pages and takes those that it has a right to.
+template <bool kSummed>
 __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
   __shared__ uint64_t sum_s[kWaves][2];
   const int t = threadIdx.x, lane = t & (kWave - 1);
@@ -275,23 +334,24 @@ __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
   const int32_t len = a.len[i];
   const Keeps k = keeps_of(a, r, len);
   const bool ring = ring_fits(a, first, held);
-  auto sum_of = [&](const int32_t* of_waves, int32_t x) {
-    const int4 n = reinterpret_cast<const int4*>(of_waves)[x];
-    return (uint64_t)(uint32_t)n.x + (uint32_t)n.y + (uint32_t)n.z + (uint32_t)n.w;
-  };
   const uint64_t events = a.events[(int64_t)i * kWaves + wave];
   // pages returned and taken before this request
   uint64_t returned = 0, taken = 0;
-  for (int32_t x = t; x < i; x += kThreads) {
-    returned += sum_of(a.freed, x);
-    taken += sum_of(a.wanted, x);
+  if constexpr (kSummed) {
+    returned = a.sums[2 * (int64_t)i];
+    taken = a.sums[2 * (int64_t)i + 1];
+  } else {
+    for (int32_t x = t; x < i; x += kThreads) {
+      returned += sum_of(a.freed, x);
+      taken += sum_of(a.wanted, x);
+    }
+    group_sums(returned, taken, sum_s);
   }
-  group_sums(returned, taken, sum_s);
   const uint64_t wants = sum_of(a.wanted, i);
   const bool is_placed = ring && k.fits(a) && (wants == 0 || taken + wants <= (uint64_t)held);
   if (t == 0) a.placed[i] = !ring || !k.known ? -1 : (is_placed ? 1 : 0);
 
-  if (i == 0 && ring) {  // the ring's state behind the call
+  if (!kSummed && i == 0 && ring) {  // the ring's state behind the call
     uint64_t all = 0, sum = 0, most = 0;
     for (int32_t x0 = 0; x0 < a.B; x0 += kThreads) {
       const int32_t x = x0 + t;
@@ -334,6 +394,11 @@ __global__ __launch_bounds__(kThreads) void place(PagesArgs a) {
 
 inline size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 constexpr int32_t kMostRequests = 1 << 24;
+// The sums before each request by a launch of their own above this many (a replayed call, rows of 64 entries, by place's workgroups
+// and by the launch: 512 requests 9.3 and 13.2 us, 8192 56.2 and 60.4, 10240 71.4 and 72.4, 12288 95 and 85, 16384 155 and 111; of
+// 8 entries 65536 2164 and 420, 131072 8580 and 832).
+constexpr int32_t kManyRequests = 10240;
+inline bool is_many(int32_t B) { return B > kManyRequests; }
 inline bool is_few(int32_t B, int32_t max_pages) { return B <= kFewWaves && max_pages <= kFewPages; }
 
 }  // namespace pages_impl
@@ -341,7 +406,7 @@ inline bool is_few(int32_t B, int32_t max_pages) { return B <= kFewWaves && max_
 extern "C" size_t sdv_kv_pages_workspace_bytes(int32_t B, int32_t max_pages) {
   using namespace pages_impl;
   if (B < 1 || B >= kMostRequests || max_pages < 1 || is_few(B, max_pages)) return 0;
-  return 2 * up256((size_t)B * kWaves * 4) + up256((size_t)B * kWaves * 8) + 256;
+  return 2 * up256((size_t)B * kWaves * 4) + up256((size_t)B * kWaves * 8) + 256 + (is_many(B) ? (size_t)B * 16 : 0);
 }
 
 extern "C" int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, int32_t page_size,
@@ -387,6 +452,7 @@ extern "C" int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, i
   a.wanted = reinterpret_cast<int32_t*>(work + counts);
   a.events = reinterpret_cast<uint64_t*>(work + 2 * counts);
   a.before = reinterpret_cast<int32_t*>(work + 2 * counts + up256((size_t)B * kWaves * 8));
+  a.sums = reinterpret_cast<uint64_t*>(a.before + 64);
   a.n_d = n_draft_rows;
   a.n_pages = n_pages;
   a.B = B;
@@ -400,6 +466,11 @@ extern "C" int sdv_kv_pages(int32_t* page_table, int32_t B, int32_t max_pages, i
     return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
   }
   hipLaunchKernelGGL(count, dim3((unsigned)B), dim3(kThreads), 0, s, a);
-  hipLaunchKernelGGL(place, dim3((unsigned)B), dim3(kThreads), 0, s, a);
+  if (is_many(B)) {
+    hipLaunchKernelGGL(sum_up, dim3(1), dim3(kSumThreads), 0, s, a);
+    hipLaunchKernelGGL(place<true>, dim3((unsigned)B), dim3(kThreads), 0, s, a);
+  } else {
+    hipLaunchKernelGGL(place<false>, dim3((unsigned)B), dim3(kThreads), 0, s, a);
+  }
   return hipGetLastError() == hipSuccess ? SDV_OK : SDV_ERR_HIP;
 }
