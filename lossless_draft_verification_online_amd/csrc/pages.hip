@@ -75,7 +75,7 @@ __device__ __forceinline__ void ask(const PagesArgs& a, const Keeps& k, int32_t 
 struct Part {
   int32_t lo, hi, n, shift;
   __device__ __forceinline__ Part(int32_t from, int32_t to) : lo(from), hi(to), n((to - from + kWave - 1) / kWave), shift(0) {
-    while (n >> shift > 64) ++shift;
+    while ((n - 1) >> shift > 63) ++shift;  // of the last chunk, too
   }
   // the first chunk from c on that one of `events` stands for, or n
   __device__ __forceinline__ int32_t next(uint64_t events, int32_t c) const {
