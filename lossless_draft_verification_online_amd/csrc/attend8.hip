@@ -13,8 +13,8 @@ using namespace attend_impl;
 enum Mode { kUnits, kFewUnits, kRanges, kSmallPages, kRows };
 
 // The rules, by what the host knows: the batch's mean columns of a request, and for its lengths the page table's width (under a
-// window, the window).  Times of 8 heads of 128 values, bf16 rows, for one side and the other; a tile is of 32 tokens, a unit of 16
-// columns on one head.
+// window, the window).  Times of 8 heads of 128 values, bf16 rows, for one side and the other, each that of a call in a replayed
+// graph (from Python a call takes 5 us at least); a tile is of 32 tokens, a unit of 16 columns on one head.
 //
 // attend_rows from this many columns of a request and this many workgroups on: 16 requests of 256 columns on 1000 tokens 47.9 us for
 // 50.6 by units, of 512 on 4000 181 for 293, one of 4096 on 1000 59 for 86; 64 of 128 on 4000 340 for 316, 4 of 512 on 4000
@@ -22,15 +22,18 @@ enum Mode { kUnits, kFewUnits, kRanges, kSmallPages, kRows };
 constexpr int64_t kManyColumns = 256, kManyWorkgroups = 256;
 
 // Eight waves for a unit instead of four, up to as many units: a wave waits 1 us for each of its tiles (one request of 47 tiles 15.2 us
-// for 18.0, 16 of 63 20.3 for 25.9, 24 of 63 22.1 for 31.0).  A second round of such workgroups costs more than they gain (32
-// requests of 12 or 20 columns on 16 tiles, over 256 units, 17.7 for 13.0).
+// for 18.0, 16 of 63 20.3 for 25.9, 24 of 63 22.0 for 30.7).  A second round of such workgroups costs more than they gain (32
+// requests of 20 columns on 16 tiles, 512 units, 19.1 for 14.8).  The bound is lower than it could be: at 256 units, 32 requests
+// of 16 columns, eight waves take 13.8, 17.5, 26.6 and 52.3 on 16, 32, 63 and 125 tiles for the 15.1, 20.0, 32.7 and 61.3 of the plans
+// taken; binary32 rows of 64 values, 16 of 32 columns on 125 tiles, 31.7 for 39.8.
 constexpr int64_t kEightWaves = 192;
 constexpr int kFewWaves = 8;
 
 // Units of 16 columns up to which they are not paired (32 requests of 32 columns on 1000 tokens, 512 units, 21.0 us for 25.3 in
 // pairs, 40 of them 25.5 for 26.2, 64 42.3 for 31.3).  Ranges are in pairs: they read the cache again for each column tile (64 of 20
 // columns on 4000 tokens 105 us for 190).  Heads of 256 values never are: a pair takes the registers of all waves (16 of 64 columns
-// on 4000 tokens 72 us for 106 by ranges, 84 for 93 by units), nor are binary32 ones above 64.
+// on 4000 tokens 69 us by ranges and 85 by units, 95 in pairs by units; 16 of 32 columns 51, 61 and 94; 64 of 32 columns on 1000 tokens
+// 42, 35 and 39, but on 4000 136, 117 and 112, of which the rule takes the ranges), nor are binary32 ones above 64.
 constexpr int64_t kUnpaired = 640;
 
 // Ranges from more tiles on than this: one request on 47 tiles 15.6 us for 15.2 by units, on 63 12.5 for 17.9; 16 (128 units) on 126

@@ -370,6 +370,7 @@ __global__ __launch_bounds__(kRowsWaves* kWave, 2) void attend_rows(AttendArgs a
     const float frame = m == -__builtin_inff() ? 0.0f : m;
     float sum = 0.0f;
     bf16x8 p[4];
+    // weights in 8 bits for the product with the values, as in attend_unit; their sum is of 32
     auto weigh = [&](int blk, int e) {
       const float x = fast_exp2(fmaf(sc[blk][e], a.scale2, -frame));
       sum += x;

@@ -393,8 +393,12 @@ __device__ __forceinline__ void add_to(char* out, int d, float v) {
 // are bound by what a compute unit loads (1000 tokens of a head, 512 KB, in about 8 us; 8 waves instead of 4 take as long).
 //
 // 8 bits: a code times its scale is a bf16 number, converted in registers (keys) or on the way to shared memory (values).  The
-// same 64 requests 123 us, 4.4 TB/s of 0.53 GB, and 6.5 for the join; three of 200 000 tokens in all 75 us, 5.4 TB/s.  Binary32
-// rows take three bf16 products for one (16 trees 14.6 us, of a binary32 cache 24.8).
+// same 64 requests 119 us, 4.5 TB/s of 0.53 GB, and 6.2 for the join; three of 200 000 tokens in all 76 us, 5.4 TB/s.  Binary32
+// rows take three bf16 products for one (16 trees 14.0 us, of a binary32 cache 24.8).
+//
+// Weights of bf16 rows go into the second product as bf16 numbers, off by 2^-8 at most each, as a result's own rounding is; as
+// three terms they would take its time three times.  Errors against 64 bits, of results that are rounded from 32 bits in
+// brackets: the 64 requests 0.0019 (0.0016) of the results' size, one row on 1000 tokens 0.0020 (0.0017), prompts 0.0023 (0.0017).
 template <class E, int D, int QB, int kWaves, bool kWholePages, bool k8>
 __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, QB, kWaves, k8>& sh, const TileOf& at,
                                             int32_t len, int32_t head, bool pos_all, int32_t w_lo, int32_t w_hi, int64_t slot) {
@@ -909,7 +913,8 @@ __device__ __forceinline__ void attend_unit(const AttendArgs& a, Scratch<E, D, Q
   }
 }
 
-// Two waves per SIMD hide each other's loads; sums of 64 columns, or of 256 values, take the registers of both.
+// Two waves per SIMD hide each other's loads; sums of 64 columns, or of 256 values, take the registers of both.  (Of 256 bf16
+// values two waves keep registers in memory: units 28, ranges 55, ranges over 8 bits 27.)
 template <class E, int D, int QB>
 constexpr int kMinWaves = E::kBytes == 4 ? (D <= 128 ? 2 : 1) : (D * QB <= 256 ? 2 : 1);
 

@@ -161,7 +161,11 @@ constexpr int kTurns = 16;  // tokens whose angles are held at once
 // that of the values as given, since a rotation is not needed to know it (316 sqrt(2) < 448).
 //
 // Many rows are bound by memory: 4 prompts of 4096 rows at most, 100 MB, 20.8 us, 4.8 TB/s (a large copy's rate).  Few are bound by
-// the chain of offsets, length, page, and rows: 256 requests of K in 0 .. 8, 27 MB, 14 us (5.7 at a copy's rate); one 5.3.
+// the chain of offsets, length, page, and rows: 256 requests of K in 0 .. 8, 27 MB, 14.0 us (5.7 at a copy's rate); one 5.4.  Binary32
+// rows: 194 MB of prompts 45 us (40.5 at a copy's rate), the 256 requests 17.6 (10.9), one 6.0.
+//
+// Eight waves per SIMD leave 64 registers, of which the rare binary64 path takes part: with pairs half a rotation apart bf16 rows keep
+// 4 registers in memory and binary32 ones 10; with neighbours, none.
 // Slower: rows held in registers between the passes (with the rotation's operands they leave fewer waves), several heads to a
 // wave, the tables of angles in binary64 (in the place of the few values that need it computing their own), the list of
 // units in shared memory.

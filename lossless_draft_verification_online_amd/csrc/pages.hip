@@ -97,8 +97,8 @@ __device__ __forceinline__ Part part_of(int32_t max_pages, int w) {
   return Part(lo, lo + part < max_pages ? lo + part : max_pages);
 }
 
-// Entries of a part that go back, and that the request's rows need, and where.  kAhead loads at once (512 requests of 4100 entries
-// 26.7 us, by twos 28.4, by eights 26.3, but one of 66 6.8, 6.7 and 7.3).
+// Entries of a part that go back, and that the request's rows need, and where.  kAhead loads at once (two calls, where the whole row
+// was read again to place it: 512 requests of 4100 entries 26.7 us, by twos 28.4, by eights 26.3, but one of 66 6.8, 6.7 and 7.3).
 constexpr int kAhead = 4;
 struct Counts {
   int32_t frees, wants;
@@ -173,9 +173,11 @@ __device__ __forceinline__ void write_state(const PagesArgs& a, int32_t first, i
   a.state[1] = (int32_t)((uint64_t)held + back - most);
 }
 
-// Few requests with short rows of the table: one workgroup, a wave per request.  Two calls after one another, by this and by the two
-// launches: one request of 66 entries 5.1 us and 11.2, of 1030 7.7 and 11.8; 16 of 260 8.8 and 12.8, of 515 10.7 and 13.1, of 1028
-// 14.6 and 13.7.
+// Few requests with short rows of the table: one workgroup, a wave per request.  Two calls after one another in a replayed graph, by
+// this and by the two launches: one request of 515 entries 8.5 us and 13.4, of 890 9.9 and 13.7, of 1540 13.2 and 14.2, of 2050 15.3
+// and 15.0; 4 of 890 10.8 and 15.8, of 2050 16.2 and 17.3, of 3000 20.0 and 18.2; 16 of 515 13.2 and 15.7, of 890 15.7 and 15.7, of 1030
+// 17.0 and 16.8.  One bound of the width for all: fewer than 16 requests would be faster by this up to about 1540 entries.  (A
+// user's two calls from Python take 10 to 11 us at least.)
 constexpr int kFewWaves = 16, kFewPages = 896;
 __global__ __launch_bounds__(kFewWaves* kWave) void place_few(PagesArgs a) {
   __shared__ int32_t freed_s[kWave], wanted_s[kWave];
