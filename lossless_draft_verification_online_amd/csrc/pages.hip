@@ -282,7 +282,7 @@ __global__ __launch_bounds__(kSumThreads) void sum_up(PagesArgs a) {
   const int t = threadIdx.x, lane = t & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(t / kWave);
   const int32_t first = a.before[0], held = a.before[1];
-  uint64_t returned = 0, taken = 0, most = 0;  // before this round's requests; the largest sum that the ring held
+  uint64_t returned = 0, taken = 0, most = 0;  // before the requests at hand; the largest sum that the ring held
   uint64_t back = t < a.B ? sum_of(a.freed, t) : 0, want = t < a.B ? sum_of(a.wanted, t) : 0;
   for (int32_t x0 = 0, turn = 0; x0 < a.B; x0 += kSumThreads, turn ^= 1) {
     const int32_t x = x0 + t, x_1 = x + kSumThreads;
@@ -292,7 +292,7 @@ __global__ __launch_bounds__(kSumThreads) void sum_up(PagesArgs a) {
       of_wave[turn][wave][0] = back_to;
       of_wave[turn][wave][1] = want_to;
     }
-    __syncthreads();  // (the next round writes the other half)
+    __syncthreads();  // (the next requests go to the other half)
     uint64_t back_before = returned, want_before = taken;
 #pragma unroll
     for (int w = 0; w < kSumWaves; ++w) {
